@@ -14,6 +14,11 @@ from __future__ import annotations
 import ctypes as C
 import os
 
+from .attention import (CACHE_BAD, CACHE_FULL, CACHE_TABLE_FULL, Cache, attn_decode, attn_error, attn_prompt,  # noqa: F401
+                        cache_append, cache_compact, cache_copy, cache_extend, cache_fork, cache_free, cache_release,
+                        cache_reserve)
+from .attention import declare as _declare_attention
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtfx_exl3.so")
 
@@ -98,6 +103,7 @@ def lib() -> C.CDLL:
         L.tfx_exl3_debug_set_spin_limit.restype = C.c_int64
         L.tfx_exl3_debug_launch_count.argtypes = []
         L.tfx_exl3_debug_launch_count.restype = C.c_int64
+        _declare_attention(L)
         _lib = L
     return _lib
 

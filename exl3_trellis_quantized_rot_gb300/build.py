@@ -33,12 +33,14 @@ def _flags() -> list[str]:
 
 
 def _sources():
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "tfx_exl3.h")]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     jobs = [(os.path.join(CSRC, "exl3_bits.cu"), os.path.join(OUT, f"exl3_b{b}.o"), [f"-DTFX_BITS={b}"])
             for b in range(1, 9)]
     jobs.append((os.path.join(CSRC, "exl3_host.cu"), os.path.join(OUT, "exl3_host.o"), []))
     jobs.append((os.path.join(CSRC, "exl3_noalloc.cu"), os.path.join(OUT, "exl3_noalloc.o"), []))
     jobs.append((os.path.join(CSRC, "exl3_encode.cu"), os.path.join(OUT, "exl3_encode.o"), []))
+    for name in ("attn_host", "attn_warp", "cache_ops"):
+        jobs.append((os.path.join(CSRC, name + ".cu"), os.path.join(OUT, name + ".o"), []))
     return deps, jobs
 
 

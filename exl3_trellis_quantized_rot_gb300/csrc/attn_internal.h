@@ -1,0 +1,110 @@
+// Internal interface between the attention and cache translation units (not installed).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tfx_attn.h"
+#include "exl3_internal.h"
+
+namespace tfx {
+
+constexpr int kAttnMaxSeqs = 512;  // sequences of one prompt launch (longer lists take several launches)
+
+// Work of one prompt launch, in the kernel's parameters: nothing is copied to
+// the device and a captured launch keeps it.
+struct PromptArgs {
+  CUtensorMap k, v;
+  const void* q;
+  void* out;
+  long long ldq, ldo;
+  float scale_log2;  // scale * log2(e)
+  int heads_q, heads_kv, group;
+  int n;
+  int* err;
+  long long spin;
+  int begin[kAttnMaxSeqs];  // first row of sequence i
+  int len[kAttnMaxSeqs];
+};
+
+// A decode call. Key slices of kSlice tokens, numbered through: first those of
+// the shared prefix (for each K/V head and 16-row tile of the batch's rows),
+// then the sequences' own (for each K/V head and 16-row tile of a sequence's
+// heads, sequence after sequence). Warp w takes the slices [w*per, (w+1)*per);
+// a run of them inside one group is a segment with its own partial result, in
+// slot w + (number of the group).
+struct DecodeAttnArgs {
+  CUtensorMap k, v;
+  const void* q;
+  void* out;
+  long long ldq, ldo;
+  const int* seqs;
+  const int* lens;
+  const int* tables;
+  float scale_log2;
+  int heads_q, heads_kv, group, batch, shared;
+  int page_size, page_shift, pages, slots, width;
+  int warps;          // NW
+  int own_rows;       // rows of an own slot: min(16, group)
+  int* starts;        // [batch + 1] own slices before sequence i; then per
+  float* own_o;       // [NW + groups][own_rows][dim]
+  float2* own_ml;     // [NW + groups][own_rows]: (reference of the exponents, sum)
+  float* pre_o;       // [NW + prefix groups][16][dim]
+  float2* pre_ml;
+  int* err;
+  long long spin;
+};
+
+// One-CTA book kernels of the page operations.
+struct BookArgs {
+  int *book, *lens, *refs, *tables;
+  const int *list0, *list1;  // seqs / sources; offsets / targets
+  int n, slots, width, pages, page_size, row_cap;
+  // scratch: free pages in order; moves; where a page is after a compact; per
+  // list entry its length before the call (-1: left alone); token slot of each
+  // new row; moves or rows counted
+  int *free_list, *move_src, *move_dst, *map, *start, *row_slot, *count;
+};
+
+struct AppendArgs {
+  const void *k_new, *v_new;
+  void *k, *v;         // the layer's pages
+  long long ldk, ldv;  // 16-byte words
+  int row;             // 16-byte words of a token's K (or V)
+  const int *row_slot, *count;
+};
+
+enum Tables { kTablesNone = 0, kTablesFork = 1, kTablesCompact = 2 };
+struct MoveArgs {
+  void *k, *v;
+  int *book, *refs, *table;
+  const int *list0, *list1, *move_src, *move_dst, *map, *start;
+  const int* count;  // moves (null: n)
+  int n, layers, pages, slots, width, page_size;
+  long long page_words;  // 16-byte words of one page of one layer
+  Tables tables;
+};
+
+int launch_extend(const BookArgs& a, cudaStream_t s);
+int launch_append(const AppendArgs& a, int rows, cudaStream_t s);
+int launch_free(const BookArgs& a, cudaStream_t s);
+int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStream_t s);
+
+int launch_prompt(const PromptArgs& a, int act, int dim, int max_len, cudaStream_t s);
+int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
+
+// exl3_host.cu
+tfx_exl3_driver driver_hooks();
+bool driver_is_runtime();
+long long spin_limit();
+int multiprocessors();
+int launch_kernel(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t s, void* arg, bool pdl, int cluster);
+int opt_in_smem(const void* fn, size_t smem);
+int fail_with(int code, const char* fmt, ...);
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled tensor_map_encoder();
+
+}  // namespace tfx

@@ -13,6 +13,7 @@
 #include <string>
 
 #include "../../include/tfx_exl3.h"
+#include "attn_internal.h"
 #include "exl3_internal.h"
 #include "exl3_tc.cuh"
 
@@ -1086,4 +1087,22 @@ const char* tfx_exl3_last_error(void) { return g_err.c_str(); }
 // Error reporting for the other C-ABI translation units.
 namespace tfx {
 int report_error(int code, const char* msg) { return fail(code, "%s", msg); }
+int fail_with(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return code;
+}
+tfx_exl3_driver driver_hooks() { return drv(); }
+bool driver_is_runtime() { return drv().alloc == rt_alloc; }
+long long spin_limit() { return g_spin.load(std::memory_order_relaxed); }
+int multiprocessors() { return sm_count(); }
+int launch_kernel(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t s, void* arg, bool pdl, int cluster) {
+  return launch(fn, grid, block, smem, s, arg, pdl, cluster);
+}
+int opt_in_smem(const void* fn, size_t smem) { return set_smem(fn, smem); }
+EncodeTiled tensor_map_encoder() { return encode_tiled(); }
 }  // namespace tfx
