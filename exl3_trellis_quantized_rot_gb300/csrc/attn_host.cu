@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -56,20 +57,44 @@ int check_rows(const char* what, const void* p, int64_t ld, int64_t width) {
   return 0;
 }
 
-// K or V as (64 values, tokens, dim/64 column blocks, heads, pages).
-int make_map(CUtensorMap* tm, const void* base, int act, int dim, int heads, int64_t tokens, int64_t ld, int64_t pages,
-             int64_t page_pitch, int box_tokens) {
+int encode_map(CUtensorMap* tm, const void* base, int act, const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4],
+               const cuuint32_t (&box)[5]) {
   const tfx::EncodeTiled enc = tfx::tensor_map_encoder();
   if (!enc) return fail_with(TFX_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t dims[5] = {64, (cuuint64_t)tokens, (cuuint64_t)dim / 64, (cuuint64_t)heads, (cuuint64_t)pages};
-  cuuint64_t strides[4] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)dim * 2, (cuuint64_t)page_pitch * 2};
-  cuuint32_t box[5] = {64, (cuuint32_t)box_tokens, (cuuint32_t)dim / 64, 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = enc(tm, act == TFX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail_with(TFX_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return 0;
+}
+
+// K or V as (64 values, tokens, dim/64 column blocks, heads, pages), in boxes of
+// some tokens of some column blocks of one head.
+int make_map(CUtensorMap* tm, const void* base, int act, int dim, int heads, int64_t tokens, int64_t ld, int64_t pages,
+             int64_t page_pitch, int box_tokens, int box_blocks) {
+  const cuuint64_t dims[5] = {64, (cuuint64_t)tokens, (cuuint64_t)dim / 64, (cuuint64_t)heads, (cuuint64_t)pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)dim * 2, (cuuint64_t)page_pitch * 2};
+  const cuuint32_t box[5] = {64, (cuuint32_t)box_tokens, (cuuint32_t)box_blocks, 1, 1};
+  return encode_map(tm, base, act, dims, strides, box);
+}
+
+// Q as (64 values, heads, tokens, dim/64 column blocks), in boxes of one column
+// block of some heads of some tokens: the rows of a tile in order.
+int make_q_map(CUtensorMap* tm, const void* base, int act, int dim, int heads, int64_t tokens, int64_t ld, int box_heads,
+               int box_tokens) {
+  const cuuint64_t dims[5] = {64, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)dim / 64, 1};
+  const cuuint64_t strides[4] = {(cuuint64_t)dim * 2, (cuuint64_t)ld * 2, 128, 16};
+  const cuuint32_t box[5] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1, 1};
+  return encode_map(tm, base, act, dims, strides, box);
+}
+
+// Query heads of one K/V head that share a 128-row tile: the most that divide
+// the group and leave at most one row in 16 of the tile empty.
+int heads_per_tile(int group) {
+  int g = group;
+  while (group % g || 128 / g * g < 120) g--;
+  return g;
 }
 
 int check_cache(const tfx_cache* c) {
@@ -220,31 +245,42 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
   if ((rc = check_rows("k", k, ldk, (int64_t)h->heads_kv * h->dim))) return rc;
   if ((rc = check_rows("v", v, ldv, (int64_t)h->heads_kv * h->dim))) return rc;
   if ((rc = check_rows("out", out, ldo, (int64_t)h->heads_q * h->dim))) return rc;
-  tfx::PromptArgs a = {};
+  tfx::PromptArgs a;
   const int64_t rows = offsets[n];
-  if ((rc = make_map(&a.k, k, h->act, h->dim, h->heads_kv, rows, ldk, 1, 8, 16))) return rc;
-  if ((rc = make_map(&a.v, v, h->act, h->dim, h->heads_kv, rows, ldv, 1, 8, 16))) return rc;
-  a.q = q;
-  a.out = out;
-  a.ldq = ldq;
-  a.ldo = ldo;
-  a.scale_log2 = h->scale * 1.4426950408889634f;
-  a.heads_q = h->heads_q;
   a.heads_kv = h->heads_kv;
   a.group = h->heads_q / h->heads_kv;
+  a.per_tile = heads_per_tile(a.group);
+  a.tokens = 128 / a.per_tile;
+  if ((rc = make_q_map(&a.qmap, q, h->act, h->dim, h->heads_q, rows, ldq, a.per_tile, a.tokens))) return rc;
+  if ((rc = make_map(&a.k, k, h->act, h->dim, h->heads_kv, rows, ldk, 1, 8, 64, h->dim / 64))) return rc;
+  if ((rc = make_map(&a.v, v, h->act, h->dim, h->heads_kv, rows, ldv, 1, 8, 128, h->dim / 128))) return rc;
+  a.vbase = v;
+  a.out = out;
+  a.ldv = ldv;
+  a.ldo = ldo;
+  a.scale_log2 = h->scale * 1.4426950408889634f;
   a.err = error_word();
   a.spin = tfx::spin_limit();
   if (!a.err) return fail_with(TFX_ECUDA, "no device error word");
+  const int tile = 2 * a.tokens, per_token_tile = a.heads_kv * (a.group / a.per_tile);
   for (int i = 0; i < n;) {
-    int most = 0;
-    for (a.n = 0; i < n && a.n < tfx::kAttnMaxSeqs; i++) {
-      const int len = offsets[i + 1] - offsets[i];
-      if (!len) continue;
-      a.begin[a.n] = offsets[i];
-      a.len[a.n++] = len;
-      if (len > most) most = len;
+    struct Seq {
+      int begin, len;
+    } seqs[tfx::kAttnMaxSeqs];
+    for (a.n = 0; i < n && a.n < tfx::kAttnMaxSeqs; i++)
+      if (offsets[i + 1] > offsets[i]) seqs[a.n++] = {offsets[i], offsets[i + 1] - offsets[i]};
+    if (!a.n) break;
+    std::stable_sort(seqs, seqs + a.n, [](const Seq& x, const Seq& y) { return x.len > y.len; });
+    int64_t total = 0;
+    for (int s = 0; s < a.n; s++) {
+      a.begin[s] = seqs[s].begin;
+      a.len[s] = seqs[s].len;
+      a.count[s] = (seqs[s].len + tile - 1) / tile;
+      total += a.count[s];
+      a.before[s] = (int)(total - (int64_t)a.count[s] * (s + 1));
     }
-    if (a.n && (rc = tfx::launch_prompt(a, h->act, h->dim, most, stream))) return rc;
+    if (total * per_token_tile > (1 << 30)) return fail_with(TFX_EUNSUPPORTED, "%lld tiles", (long long)(total * per_token_tile));
+    if ((rc = tfx::launch_prompt(a, h->act, h->dim, (int)total * per_token_tile, stream))) return rc;
   }
   return 0;
 }
@@ -382,8 +418,8 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   const int64_t layer_values = (int64_t)c->pages * page_values(c), ld = (int64_t)c->heads_kv * c->dim;
   const uint16_t* kl = static_cast<const uint16_t*>(c->k) + layer * layer_values;
   const uint16_t* vl = static_cast<const uint16_t*>(c->v) + layer * layer_values;
-  if ((rc = make_map(&a.k, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16))) return rc;
-  if ((rc = make_map(&a.v, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16))) return rc;
+  if ((rc = make_map(&a.k, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
+  if ((rc = make_map(&a.v, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
   a.q = q;
   a.out = out;
   a.ldq = ldq;

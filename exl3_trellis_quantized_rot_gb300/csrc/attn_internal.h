@@ -13,19 +13,25 @@ namespace tfx {
 constexpr int kAttnMaxSeqs = 512;  // sequences of one prompt launch (longer lists take several launches)
 
 // Work of one prompt launch, in the kernel's parameters: nothing is copied to
-// the device and a captured launch keeps it.
+// the device and a captured launch keeps it. A tile is 2 x `tokens` tokens of
+// per_tile query heads that share a K/V head. The sequences are ordered by their
+// number of tiles, most first, and tiles are started from the last (the most
+// keys) to the first: level by level, at each the sequences that have it.
+// before[s] is the number of tiles that come before level count[s] - 1.
 struct PromptArgs {
-  CUtensorMap k, v;
-  const void* q;
+  CUtensorMap qmap, k, v;
+  const void* vbase;
   void* out;
-  long long ldq, ldo;
+  long long ldv, ldo;
   float scale_log2;  // scale * log2(e)
-  int heads_q, heads_kv, group;
+  int heads_kv, group, per_tile, tokens;
   int n;
   int* err;
   long long spin;
-  int begin[kAttnMaxSeqs];  // first row of sequence i
+  int begin[kAttnMaxSeqs];  // first row of a sequence
   int len[kAttnMaxSeqs];
+  int count[kAttnMaxSeqs];   // its tiles
+  int before[kAttnMaxSeqs];
 };
 
 // A decode call. Key slices of kSlice tokens, numbered through: first those of
@@ -91,7 +97,7 @@ int launch_append(const AppendArgs& a, int rows, cudaStream_t s);
 int launch_free(const BookArgs& a, cudaStream_t s);
 int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStream_t s);
 
-int launch_prompt(const PromptArgs& a, int act, int dim, int max_len, cudaStream_t s);
+int launch_prompt(const PromptArgs& a, int act, int dim, int pairs, cudaStream_t s);
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 
 // exl3_host.cu

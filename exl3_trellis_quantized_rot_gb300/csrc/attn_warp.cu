@@ -295,47 +295,6 @@ __device__ __forceinline__ void gave_up(int* err, int lane) {
   while (clock64() - t0 < 2000000) __nanosleep(1000);
 }
 
-// Packed prompts: warp (blockIdx.x * 4 + warp) of sequence blockIdx.z takes 16
-// of the rows (token, head of the group) of K/V head blockIdx.y.
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) prompt_warp_kernel(const __grid_constant__ PromptArgs a) {
-  extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t full[kWarps][kStages];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Ring rg = make_ring<D>(dyn, full, warp, lane);
-  const int n = a.len[blockIdx.z], row0 = a.begin[blockIdx.z], kvh = blockIdx.y;
-  const long long first = ((long long)blockIdx.x * kWarps + warp) * 16, total = (long long)n * a.group;
-  if (first >= total) return;
-  Rows<T, D> R;
-  const T* rp[2];
-  T* op[2];
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const long long r = first + (lane >> 2) + 8 * h;
-    const bool in = r < total;
-    const int tok = in ? (int)(r / a.group) : 0, head = kvh * a.group + (in ? (int)(r % a.group) : 0);
-    rp[h] = in ? reinterpret_cast<const T*>(a.q) + (row0 + (long long)tok) * a.ldq + (long long)head * D : nullptr;
-    op[h] = in ? reinterpret_cast<T*>(a.out) + (row0 + (long long)tok) * a.ldo + (long long)head * D : nullptr;
-    R.hi[h] = in ? tok + 1 : 0;
-  }
-  R.load(rp[0], rp[1], lane);
-  const long long last = min(first + 15, total - 1);
-  const int keys = (int)(last / a.group) + 1;
-  Keys ks = {&a.k, &a.v, nullptr, 0, 0, 0, row0, kvh};
-  if (!attend<T, D>(R, ks, rg, 0, (keys + Slice<D>::kKeys - 1) / Slice<D>::kKeys, 0, a.scale_log2, lane, a.spin)) {
-    gave_up(a.err, lane);
-    return;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    if (!op[h]) continue;
-    const float inv = 1.f / R.l[h];
-#pragma unroll
-    for (int i = 0; i < D / 8; i++)
-      *reinterpret_cast<uint32_t*>(op[h] + i * 8 + 2 * (lane & 3)) = pack2<T>(R.o[i][2 * h] * inv, R.o[i][2 * h + 1] * inv);
-  }
-}
-
 __device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int i) {
   const int s = a.seqs[i];
   if (s < 0 || s >= a.slots) return 0;
@@ -541,15 +500,6 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
 }
 
 template <typename T, int D>
-int prompt_of(const PromptArgs& a, int max_len, cudaStream_t s) {
-  const void* fn = (const void*)prompt_warp_kernel<T, D>;
-  int rc = opt_in_smem(fn, warp_smem<D>());
-  if (rc) return rc;
-  const long long rows = (long long)max_len * a.group;
-  return launch_kernel(fn, dim3((unsigned)((rows + 16 * kWarps - 1) / (16 * kWarps)), a.heads_kv, a.n), dim3(kWarps * 32),
-                       warp_smem<D>(), s, const_cast<PromptArgs*>(&a), false, 1);
-}
-template <typename T, int D>
 int decode_of(const DecodeAttnArgs& a, cudaStream_t s) {
   const void* fn = (const void*)decode_warp_kernel<T, D>;
   int rc = opt_in_smem(fn, warp_smem<D>());
@@ -563,10 +513,6 @@ int decode_of(const DecodeAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int launch_prompt(const PromptArgs& a, int act, int dim, int max_len, cudaStream_t s) {
-  if (act == TFX_F16) return dim == 128 ? prompt_of<__half, 128>(a, max_len, s) : prompt_of<__half, 256>(a, max_len, s);
-  return dim == 128 ? prompt_of<__nv_bfloat16, 128>(a, max_len, s) : prompt_of<__nv_bfloat16, 256>(a, max_len, s);
-}
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s) {
   if (act == TFX_F16) return dim == 128 ? decode_of<__half, 128>(a, s) : decode_of<__half, 256>(a, s);
   return dim == 128 ? decode_of<__nv_bfloat16, 128>(a, s) : decode_of<__nv_bfloat16, 256>(a, s);

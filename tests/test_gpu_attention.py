@@ -116,6 +116,30 @@ def test_prompt_other_rows_do_not_leak(bad):
     assert torch.equal(tfx.attn_prompt(q, k, v, off)[70:270], want)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("hq,hkv,dim", [(6, 1, 256), (8, 2, 128), (2, 2, 256)])
+def test_prompt_later_values_do_not_reach_earlier_rows(hq, hkv, dim, dtype):
+    """Infinite and NaN values of K and V are seen by their own and later rows only, and there as the formula has them."""
+    T = 400
+    q, k, v = normal((T, hq, dim), dtype, 1), normal((T, hkv, dim), dtype, 2), normal((T, hkv, dim), dtype, 3)
+    off = offsets_of([10, 390])
+    want = tfx.attn_prompt(q, k, v, off)
+    v[140, 0, 5], v[141, 0, 5], v[150, 0, 7], v[155, 0, dim - 1] = float("inf"), -float("inf"), float("nan"), -float("inf")
+    out = tfx.attn_prompt(q, k, v, off)
+    assert torch.equal(out[:140], want[:140])
+    g = hq // hkv
+    assert bool((out[140, :g, 5] == float("inf")).all()) and out[141:, :g, 5].isnan().all()
+    assert torch.equal(out[:150, :, 7], want[:150, :, 7]) and out[150:, :g, 7].isnan().all()
+    assert bool((out[155:, :g, dim - 1] == -float("inf")).all())
+    other = [c for c in range(dim) if c not in (5, 7, dim - 1)]
+    assert torch.equal(out[:, :, other], want[:, :, other]) and torch.equal(out[:, g:], want[:, g:])
+    v[:] = torch.nan_to_num(v, 0.0, 0.0, 0.0)
+    want = tfx.attn_prompt(q, k, v, off)
+    k[200, 0, 3] = float("nan")
+    out = tfx.attn_prompt(q, k, v, off)
+    assert torch.equal(out[:200], want[:200]) and out[200:, :g].isnan().all()
+
+
 def test_prompt_sequence_bits_do_not_depend_on_the_call():
     lens = [300, 17, 129]
     T = sum(lens)
