@@ -5,6 +5,7 @@
 
 #include <climits>
 
+#include "attn_internal.h"
 #include "exl3_kernels.cuh"
 
 namespace tfx {
@@ -165,6 +166,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// Tokens that sequence i of a decode batch holds; 0 for a slot out of range.
+__device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int i) {
+  const int s = a.seqs[i];
+  if (s < 0 || s >= a.slots) return 0;
+  return min(max(a.lens[s], 0), (int)min((long long)a.width << a.page_shift, (long long)INT_MAX));
 }
 
 }  // namespace tfx

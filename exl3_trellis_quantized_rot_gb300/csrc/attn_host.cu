@@ -199,6 +199,18 @@ tfx::MoveArgs move_args(const tfx_cache* c, const tfx::BookArgs& b, tfx::Tables 
   return m;
 }
 
+// The shared prefix on the tensor cores: in so many shares that the items
+// (heads, 256-row tiles of the batch's rows, shares) fill the pairs of SMs once.
+int prefix_splits(int batch, int heads_q, int heads_kv, int shared) {
+  const int group = heads_q / heads_kv, per = heads_per_tile(group), seqs = 2 * (128 / per);
+  const int64_t rest = (int64_t)heads_kv * (group / per) * ((batch + seqs - 1) / seqs);
+  const int64_t fill = tfx::multiprocessors() / 2 / rest, tiles = (shared + 127) / 128;
+  return (int)(fill < 1 ? 1 : fill > tiles ? tiles : fill);
+}
+int64_t prefix_rows(int batch, int heads_q, int heads_kv) {
+  return (int64_t)prefix_splits(batch, heads_q, heads_kv, INT32_MAX - 127) * batch * heads_q;
+}
+
 // Decode scratch for `batch` sequences: byte offsets of its parts.
 struct DecodeScratch {
   size_t starts, own_ml, pre_ml, own_o, pre_o, bytes;
@@ -208,7 +220,8 @@ DecodeScratch decode_scratch(int batch, int heads_q, int heads_kv, int dim, int 
   const int64_t ptiles = (batch * group + kRowTile - 1) / kRowTile;
   const int64_t own_rows = group < kRowTile ? group : kRowTile;
   const int64_t own = (warps + heads_kv * tiles * batch) * own_rows;
-  const int64_t pre = (warps + heads_kv * ptiles) * kRowTile;
+  const int64_t few = (warps + heads_kv * ptiles) * kRowTile, many = prefix_rows(batch, heads_q, heads_kv);
+  const int64_t pre = few > many ? few : many;
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
   DecodeScratch d;
   int64_t at = 0;
@@ -280,7 +293,8 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
       a.before[s] = (int)(total - (int64_t)a.count[s] * (s + 1));
     }
     if (total * per_token_tile > (1 << 30)) return fail_with(TFX_EUNSUPPORTED, "%lld tiles", (long long)(total * per_token_tile));
-    if ((rc = tfx::launch_prompt(a, h->act, h->dim, (int)total * per_token_tile, stream))) return rc;
+    a.items = (int)total * per_token_tile;
+    if ((rc = tfx::launch_prompt(a, h->act, h->dim, stream))) return rc;
   }
   return 0;
 }
@@ -305,7 +319,11 @@ int tfx_cache_reserve(tfx_cache* c, int max_batch, int heads_q, cudaStream_t str
   const size_t ints = 4 + 5 * (size_t)list_cap(c) + (size_t)c->pages * c->page_size;
   if ((rc = grow(reinterpret_cast<void**>(&pv->pages), &pv->pages_bytes, ints * 4, stream))) return rc;
   const int b = max_batch > pv->max_batch ? max_batch : pv->max_batch, hq = heads_q > pv->heads_q ? heads_q : pv->heads_q;
-  const size_t part = decode_scratch(b, hq, c->heads_kv, c->dim, decode_warps()).bytes;
+  size_t part = 0;  // the most that a batch up to b takes (fewer sequences can mean more shares of the prefix)
+  for (int i = 1; i <= b; i++) {
+    const size_t bytes = decode_scratch(i, hq, c->heads_kv, c->dim, decode_warps()).bytes;
+    if (bytes > part) part = bytes;
+  }
   if ((rc = grow(reinterpret_cast<void**>(&pv->part), &pv->part_bytes, part, stream))) return rc;
   pv->max_batch = b;
   pv->heads_q = hq;
@@ -438,9 +456,23 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.pages = c->pages;
   a.slots = c->slots;
   a.width = c->width;
+  // A tensor-core tile costs the same for 1 row as for 256; from about two 16-row
+  // tiles on, the warps' reading K and V again for each costs more.
+  if (batch * a.group > 32 && shared >= 256) {
+    a.per_tile = heads_per_tile(a.group);
+    a.tokens = 128 / a.per_tile;
+    a.pre_splits = prefix_splits(batch, h->heads_q, h->heads_kv, shared);
+    const int mt = (batch + 2 * a.tokens - 1) / (2 * a.tokens), box = c->page_size < 64 ? c->page_size : 64;
+    a.items = a.heads_kv * (a.group / a.per_tile) * mt * a.pre_splits;
+    if ((rc = make_q_map(&a.qmap, q, c->act, c->dim, h->heads_q, batch, ldq, a.per_tile, a.tokens))) return rc;
+    if ((rc = make_map(&a.kt, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), box, 1))) return rc;
+    if ((rc = make_map(&a.vt, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), box, 1))) return rc;
+  }
   a.warps = decode_warps();
   a.own_rows = a.group < kRowTile ? a.group : kRowTile;
   const DecodeScratch d = decode_scratch(batch, h->heads_q, c->heads_kv, c->dim, a.warps);
+  if (d.bytes > pv->part_bytes)
+    return fail_with(TFX_ENOTRESERVED, "%d sequences of %d heads take more scratch than was reserved", batch, h->heads_q);
   a.starts = reinterpret_cast<int*>(pv->part + d.starts);
   a.own_ml = reinterpret_cast<float2*>(pv->part + d.own_ml);
   a.pre_ml = reinterpret_cast<float2*>(pv->part + d.pre_ml);
@@ -449,6 +481,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.err = error_word();
   a.spin = tfx::spin_limit();
   if (!a.err) return fail_with(TFX_ECUDA, "no device error word");
+  if (a.pre_splits && (rc = tfx::launch_prefix(a, c->act, c->dim, stream))) return rc;
   return tfx::launch_decode(a, c->act, c->dim, stream);
 }
 

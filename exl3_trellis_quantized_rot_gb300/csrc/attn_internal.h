@@ -25,7 +25,7 @@ struct PromptArgs {
   long long ldv, ldo;
   float scale_log2;  // scale * log2(e)
   int heads_kv, group, per_tile, tokens;
-  int n;
+  int n, items;
   int* err;
   long long spin;
   int begin[kAttnMaxSeqs];  // first row of a sequence
@@ -34,14 +34,17 @@ struct PromptArgs {
   int before[kAttnMaxSeqs];
 };
 
-// A decode call. Key slices of kSlice tokens, numbered through: first those of
-// the shared prefix (for each K/V head and 16-row tile of the batch's rows),
-// then the sequences' own (for each K/V head and 16-row tile of a sequence's
-// heads, sequence after sequence). Warp w takes the slices [w*per, (w+1)*per);
-// a run of them inside one group is a segment with its own partial result, in
-// slot w + (number of the group).
+// A decode call. The shared prefix goes to the tensor-core kernel where the
+// batch has enough rows (pre_splits > 0: the prefix in that many shares, each
+// with its own partial result); the rest is cut into slices of 16 KB of K and V,
+// numbered through: first those of the prefix where it was not taken (for each
+// K/V head and 16-row tile of the batch's rows), then the sequences' own (for
+// each K/V head and 16-row tile of a sequence's heads, sequence after sequence).
+// Warp w takes the slices [w*per, (w+1)*per); a run of them inside one group is
+// a segment with its own partial result, in slot w + (number of the group).
 struct DecodeAttnArgs {
-  CUtensorMap k, v;
+  CUtensorMap k, v;           // boxes of 16 tokens, all of a head's values
+  CUtensorMap qmap, kt, vt;   // tensor-core kernel: tiles of Q; boxes of up to 64 tokens of 64 values
   const void* q;
   void* out;
   long long ldq, ldo;
@@ -51,12 +54,13 @@ struct DecodeAttnArgs {
   float scale_log2;
   int heads_q, heads_kv, group, batch, shared;
   int page_size, page_shift, pages, slots, width;
+  int per_tile, tokens, pre_splits, items;  // tensor-core kernel
   int warps;          // NW
   int own_rows;       // rows of an own slot: min(16, group)
   int* starts;        // [batch + 1] own slices before sequence i; then per
   float* own_o;       // [NW + groups][own_rows][dim]
   float2* own_ml;     // [NW + groups][own_rows]: (reference of the exponents, sum)
-  float* pre_o;       // [NW + prefix groups][16][dim]
+  float* pre_o;       // [NW + prefix groups][16][dim], or [pre_splits][batch][heads_q][dim]
   float2* pre_ml;
   int* err;
   long long spin;
@@ -97,7 +101,8 @@ int launch_append(const AppendArgs& a, int rows, cudaStream_t s);
 int launch_free(const BookArgs& a, cudaStream_t s);
 int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStream_t s);
 
-int launch_prompt(const PromptArgs& a, int act, int dim, int pairs, cudaStream_t s);
+int launch_prompt(const PromptArgs& a, int act, int dim, cudaStream_t s);
+int launch_prefix(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 
 // exl3_host.cu

@@ -21,11 +21,15 @@
 // thread: S0, [S1, P0 V0], [S2, P1 V1], ...: S(j+1) goes to the buffer whose
 // probabilities P(j-1) V(j-1) has read before it.
 //
-// Warps of a CTA: 0..3 softmax (thread = row) and epilogue; 4 issues the MMAs
-// (in the even CTA); 5 asks for K, V and Q; 6 and 7 look after V where a tile
-// has keys that some row must not see: 0 * inf and 0 * NaN are NaN, so V's rows
-// past the sequence become zeros, and later tokens' values that are not finite
-// too; the epilogue gives the latter to the rows that do see them.
+// Warps of a CTA: 0..7 softmax and results; 8 issues the MMAs (in the even CTA);
+// 9 asks for K, V and Q; 10 and 11 look after V where a tile has keys that some
+// row must not see: 0 * inf and 0 * NaN are NaN, so V's rows past the sequence
+// become zeros, and later tokens' values that are not finite too; the rows that
+// do see the latter get them when the result is stored.
+//
+// A pair walks its items (a tile of rows and its key tiles) without a stop: K, V
+// and the next Q are asked for as soon as their memory is free, and the next
+// item's first scores are computed while the last one's result is stored.
 //
 // Every wait is bounded (see exl3_tc.cuh); on a timeout all roles of the CTA
 // leave at their next wait, copies and MMAs in flight get time to land, and the
@@ -33,16 +37,20 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "attn_device.cuh"
 #include "attn_internal.h"
 
 namespace tfx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kEdgeWarp = 10;  // 0..7 softmax, 10 and 11 edges
 constexpr int kTileKeys = 128;
 constexpr float kSlack = 8.f;  // log2 by which a row's maximum may pass its reference
 constexpr uint32_t kScoreCol = 256;
+constexpr int kEdgeBars = 4, kFixes = 8;
 
 template <int D>
 struct Geom {
@@ -53,12 +61,13 @@ struct Geom {
 };
 
 struct Barriers {
-  uint64_t q_full;
+  uint64_t q_full, q_empty;
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t v_edge[4];    // V tiles that warps 6 and 7 look at before the MMAs may
-  uint64_t s_full[2];    // scores are in tensor memory
-  uint64_t p_full[2];    // probabilities of both CTAs are
-  uint64_t pv_done;      // P V of a tile is added
+  uint64_t v_edge[kEdgeBars];  // V tiles that warps 10 and 11 look at before the MMAs may
+  uint64_t s_full[2];          // scores are in tensor memory
+  uint64_t p_full[2];          // probabilities of both CTAs are
+  uint64_t pv_done;            // P V of a tile is added
+  uint64_t o_empty;            // both CTAs have read an item's result
 };
 
 struct Ctx {
@@ -125,21 +134,24 @@ __host__ __device__ constexpr uint32_t idesc(int N, bool mn) {
          ((uint32_t)(256 >> 4) << 24);
 }
 
-// What one pair of CTAs does.
+// 256 rows against some key tiles. The rows are those of `per_tile` heads of
+// 2 * tokens consecutive "tokens": of a prompt, or, for the shared prefix of a
+// decode batch, the batch's sequences (one token each).
 struct Item {
-  int row0;        // first token row of the sequence in q, k, v, out
-  int t0;          // first token of the tile within the sequence
-  int end;         // tokens of the sequence
+  int row0;        // row of q of the tile's first token
+  int end_row;     // tokens of the tile before this one exist
+  int key_row;     // row of key 0 in k and v (prompt)
+  int t0;          // position of the first token in its sequence (prompt)
+  int first;       // first key tile
   int tiles;       // key tiles
-  int edge;        // first key tile with keys that some row must not see
+  int keys;        // keys of the sequence
+  int hidden;      // first key that some row must not see
   int kvh, head0;  // K/V head; first query head
+  int split;       // which share of the prefix
 };
 
-__device__ __forceinline__ Item prompt_item(const PromptArgs& a) {
-  const int sub = a.group / a.per_tile, hg = a.heads_kv * sub;
-  const int pair = blockIdx.x >> 1, i = pair / hg, h = pair % hg;
-  // the sequences by tiles, most first; a.before[s]: tiles of the list before
-  // the first s+1 sequences are all in play at tile count a.count[s]
+__device__ __forceinline__ Item item_of(const PromptArgs& a, int x) {
+  const int sub = a.group / a.per_tile, hg = a.heads_kv * sub, i = x / hg, h = x % hg;
   int lo = 0, hi = a.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -147,26 +159,136 @@ __device__ __forceinline__ Item prompt_item(const PromptArgs& a) {
   }
   const int r = i - a.before[lo], tile = a.count[lo] - 1 - r / (lo + 1), s = r % (lo + 1);
   Item it;
-  it.row0 = a.begin[s];
-  it.end = a.len[s];
+  it.key_row = a.begin[s];
+  it.keys = a.len[s];
   it.t0 = tile * 2 * a.tokens;
-  const int last = min(it.end, it.t0 + 2 * a.tokens) - 1;
-  it.tiles = last / kTileKeys + 1;
-  it.edge = (it.t0 + 1) / kTileKeys;
+  it.row0 = it.key_row + it.t0;
+  it.end_row = it.key_row + it.keys;
+  it.first = 0;
+  it.tiles = (min(it.keys, it.t0 + 2 * a.tokens) - 1) / kTileKeys + 1;
+  it.hidden = it.t0 + 1;
+  it.kvh = h / sub;
+  it.head0 = it.kvh * a.group + h % sub * a.per_tile;
+  it.split = 0;
+  return it;
+}
+
+__device__ __forceinline__ Item item_of(const DecodeAttnArgs& a, int x) {
+  const int sub = a.group / a.per_tile, hg = a.heads_kv * sub, h = x % hg, y = x / hg;
+  const int mt = (a.batch + 2 * a.tokens - 1) / (2 * a.tokens), all = (a.shared + kTileKeys - 1) / kTileKeys;
+  Item it;
+  it.split = y / mt;
+  it.row0 = y % mt * 2 * a.tokens;
+  it.end_row = a.batch;
+  it.key_row = it.t0 = 0;
+  it.first = (int)((long long)all * it.split / a.pre_splits);
+  it.tiles = (int)((long long)all * (it.split + 1) / a.pre_splits) - it.first;
+  it.keys = it.hidden = a.shared;
   it.kvh = h / sub;
   it.head0 = it.kvh * a.group + h % sub * a.per_tile;
   return it;
 }
 
+// The x-th item of a pair of CTAs, or -1: rounds over the pairs, to and fro, so
+// that the sizes (most keys first) even out.
+template <typename A>
+__device__ __forceinline__ int nth(const A& a, int r) {
+  const int pairs = gridDim.x >> 1, p = blockIdx.x >> 1;
+  const long long x = (long long)r * pairs + (r & 1 ? pairs - 1 - p : p);
+  return x < a.items ? (int)x : -1;
+}
+
+// Keys that row `tok` (a token of the tile) sees.
+__device__ __forceinline__ int sees(const PromptArgs&, const Item& it, int tok) { return it.t0 + tok + 1; }
+__device__ __forceinline__ int sees(const DecodeAttnArgs& a, const Item& it, int tok) {
+  return min(a.shared, seq_len(a, it.row0 + tok));
+}
+
+// One lane's share of the copies of K's 64 keys and V's 128 keys of a tile.
+template <int D>
+__device__ __forceinline__ void copy_k(const PromptArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar, int lane) {
+  if (lane == 0) tma_load_5d_pair(dst, &a.k, 0, it.key_row + j * kTileKeys + 64 * rank, 0, it.kvh, 0, bar);
+}
+template <int D>
+__device__ __forceinline__ void copy_v(const PromptArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar, int lane) {
+  if (lane == 0) tma_load_5d_pair(dst, &a.v, 0, it.key_row + j * kTileKeys, rank * (D / 128), it.kvh, 0, bar);
+}
+// Pages: boxes of up to 64 tokens of one page and one column block of 64 values.
+__device__ __forceinline__ int page_of(const DecodeAttnArgs& a, int key) {
+  const int s = a.seqs[0], p = key >> a.page_shift;
+  const int page = s >= 0 && s < a.slots && p < a.width ? __ldg(a.tables + (long long)s * a.width + p) : -1;
+  return page >= 0 && page < a.pages ? page : -1;  // -1 is out of the map's range: zeros
+}
+template <int D>
+__device__ __forceinline__ void copy_k(const DecodeAttnArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar,
+                                       int lane) {
+  const int shift = min(a.page_shift, 6), key0 = (it.first + j) * kTileKeys + 64 * rank;
+  for (int x = lane; x < (64 >> shift) * (D / 64); x += 32) {
+    const int b = x / (D / 64), ch = x % (D / 64), key = key0 + (b << shift);
+    tma_load_5d_pair(dst + ch * 8192 + (b << shift) * 128, &a.kt, 0, key & (a.page_size - 1), ch, it.kvh, page_of(a, key), bar);
+  }
+}
+template <int D>
+__device__ __forceinline__ void copy_v(const DecodeAttnArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar,
+                                       int lane) {
+  const int shift = min(a.page_shift, 6), key0 = (it.first + j) * kTileKeys;
+  for (int x = lane; x < (128 >> shift) * (D / 128); x += 32) {
+    const int b = x / (D / 128), ch = x % (D / 128), key = key0 + (b << shift);
+    tma_load_5d_pair(dst + ch * 16384 + (b << shift) * 128, &a.vt, 0, key & (a.page_size - 1), rank * (D / 128) + ch, it.kvh,
+                     page_of(a, key), bar);
+  }
+}
+
+// 32 columns of a row's result, from column `col` on: o is the accumulator's, inv = 1 / sum.
 template <typename T, int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_constant__ PromptArgs a) {
+__device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, int tok, int head, int col, float (&o)[32],
+                                          float inv, bool mend) {
+  if (mend) {  // values that were taken out of V: this row's own
+    const T* v = reinterpret_cast<const T*>(a.vbase) + (long long)it.key_row * a.ldv + (long long)it.kvh * D + col;
+    for (int key = it.hidden; key <= it.t0 + tok; key++) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(v + (long long)key * a.ldv);
+#pragma unroll
+      for (int k = 0; k < 16; k++) {
+        const uint32_t x = w[k], m = not_finite<T>(x);
+        if (m & 0x8000u) o[2 * k] += value_of<T>(x, 0);
+        if (m & 0x80000000u) o[2 * k + 1] += value_of<T>(x, 1);
+      }
+    }
+  }
+  T* out = reinterpret_cast<T*>(a.out) + (long long)(it.row0 + tok) * a.ldo + (long long)head * D + col;
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    uint4 w;
+    w.x = pack2<T>(o[8 * k] * inv, o[8 * k + 1] * inv);
+    w.y = pack2<T>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
+    w.z = pack2<T>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
+    w.w = pack2<T>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
+    *reinterpret_cast<uint4*>(out + 8 * k) = w;
+  }
+}
+template <typename T, int D>
+__device__ __forceinline__ void store_row(const DecodeAttnArgs& a, const Item& it, int tok, int head, int col, float (&o)[32],
+                                          float, bool) {
+  float* po = a.pre_o + (((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head) * D + col;
+#pragma unroll
+  for (int k = 0; k < 8; k++)
+    *reinterpret_cast<float4*>(po + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+}
+__device__ __forceinline__ void store_sum(const PromptArgs&, const Item&, int, int, float, float) {}
+__device__ __forceinline__ void store_sum(const DecodeAttnArgs& a, const Item& it, int tok, int head, float ref, float l) {
+  a.pre_ml[((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head] = make_float2(ref, l);
+}
+
+template <typename T, int D, typename A>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ A a) {
   using G = Geom<D>;
   constexpr int ST = G::kStages;
   extern __shared__ uint8_t dyn[];
   __shared__ Barriers bars;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ uint32_t fix;  // V values that were not finite were taken out of a tile
+  __shared__ int fix[kFixes];  // round + 1 of the item whose V had values that were not finite taken out
+  __shared__ float shared_max[2][2][128], shared_sum[2][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
   const uint32_t base = s_addr(dyn) + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
@@ -175,23 +297,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prompt_
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    fix = 0;
     mbar_init(&bars.q_full, 2);
+    mbar_init(&bars.q_empty, 1);
     for (int i = 0; i < 4; i++) {
       mbar_init(&bars.k_full[i], 2);
       mbar_init(&bars.k_empty[i], 1);
       mbar_init(&bars.v_full[i], 2);
       mbar_init(&bars.v_empty[i], 1);
-      mbar_init(&bars.v_edge[i], 1);
     }
+    for (int i = 0; i < kEdgeBars; i++) mbar_init(&bars.v_edge[i], 1);
+    for (int i = 0; i < kFixes; i++) fix[i] = 0;
     for (int i = 0; i < 2; i++) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 8);
+      mbar_init(&bars.p_full[i], 16);
     }
     mbar_init(&bars.pv_done, 1);
+    mbar_init(&bars.o_empty, 16);
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s_addr(&tmem_slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -200,219 +324,230 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prompt_
   cluster_sync();
   fence_after_sync();
   const uint32_t tm = *(volatile uint32_t*)&tmem_slot;
-  const Item it = prompt_item(a);
-  const int n = it.tiles;
+  griddep_launch();  // what follows waits for this grid before it reads what it wrote
 
-  if (warp == 5) {
+  if (warp == kCopyWarp) {
     // ---- copies: this CTA's rows of Q, its 64 keys of K, its dim/2 columns of V
-    if (lane == 0) {
-      auto lead = [&](uint64_t* bar) { return peer_addr(s_addr(bar), 0); };
-      const int t = it.t0 + (int)rank * a.tokens;
-      expect_tx_at(lead(&bars.q_full), a.tokens * a.per_tile * D * 2);
-      for (int ch = 0; ch < D / 64; ch++)
-        tma_load_5d_pair(sq + ch * 16384, &a.qmap, 0, it.head0, it.row0 + t, ch, 0, lead(&bars.q_full));
-      int edges = 0;
-      for (int j = 0; j < n; j++) {
-        const int st = j % ST;
-        const uint32_t par = ((j / ST) & 1) ^ 1;
-        if (!wait(c, &bars.k_empty[st], par)) break;
-        expect_tx_at(lead(&bars.k_full[st]), G::kKV);
-        tma_load_5d_pair(sk + st * G::kKV, &a.k, 0, it.row0 + j * kTileKeys + 64 * (int)rank, 0, it.kvh, 0,
-                         lead(&bars.k_full[st]));
-        if (!wait(c, &bars.v_empty[st], par)) break;
-        uint32_t bar = lead(&bars.v_full[st]);
-        if (j >= it.edge) {
-          bar = s_addr(&bars.v_edge[edges++ % 4]);
-          bar = peer_addr(bar, rank);
-        }
-        expect_tx_at(bar, G::kKV);
-        tma_load_5d_pair(sv + st * G::kKV, &a.v, 0, it.row0 + j * kTileKeys, (int)rank * (D / 128), it.kvh, 0, bar);
+    auto lead = [&](uint64_t* bar) { return peer_addr(s_addr(bar), 0); };
+    int edges = 0, g = 0;
+    bool ok = true;
+    for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
+      const Item it = item_of(a, x);
+      if (!(ok = wait_warp(c, &bars.q_empty, (r & 1) ^ 1))) break;
+      if (lane == 0) {
+        expect_tx_at(lead(&bars.q_full), a.tokens * a.per_tile * D * 2);
+        for (int ch = 0; ch < D / 64; ch++)
+          tma_load_5d_pair(sq + ch * 16384, &a.qmap, 0, it.head0, it.row0 + (int)rank * a.tokens, ch, 0, lead(&bars.q_full));
+      }
+      for (int j = 0; j < it.tiles; j++, g++) {
+        const int st = g % ST;
+        const uint32_t par = ((g / ST) & 1) ^ 1;
+        if (!(ok = wait_warp(c, &bars.k_empty[st], par))) break;
+        uint32_t bar = lead(&bars.k_full[st]);
+        if (lane == 0) expect_tx_at(bar, G::kKV);
+        __syncwarp();
+        copy_k<D>(a, it, j, (int)rank, sk + st * G::kKV, bar, lane);
+        if (!(ok = wait_warp(c, &bars.v_empty[st], par))) break;
+        bar = (it.first + j + 1) * kTileKeys > it.hidden ? peer_addr(s_addr(&bars.v_edge[edges++ % kEdgeBars]), rank)
+                                                         : lead(&bars.v_full[st]);
+        if (lane == 0) expect_tx_at(bar, G::kKV);
+        __syncwarp();
+        copy_v<D>(a, it, j, (int)rank, sv + st * G::kKV, bar, lane);
       }
     }
-  } else if (warp == 4) {
+  } else if (warp == kMmaWarp) {
     // ---- MMAs
     if (rank == 0 && lane == 0) {
       constexpr uint32_t is = idesc<T>(kTileKeys, false), ip = idesc<T>(D, true);
       constexpr uint64_t kmaj = operand_bits(16), vmaj = operand_bits(kTileKeys * 128);
-      auto scores = [&](int j) -> bool {
-        const int st = j % ST;
-        if (!wait(c, &bars.k_full[st], (j / ST) & 1)) return false;
+      int g = 0;
+      bool ok = true;
+      auto scores = [&](int y) -> bool {
+        const int st = y % ST;
+        if (!wait(c, &bars.k_full[st], (y / ST) & 1)) return false;
         fence_after_sync();
         const uint64_t qd = operand(sq, kmaj), kd = operand(sk + st * G::kKV, kmaj);
-        const uint32_t d = tm + kScoreCol + (j & 1) * 128;
+        const uint32_t d = tm + kScoreCol + (y & 1) * 128;
 #pragma unroll
         for (int k = 0; k < D / 16; k++)
           mma2_ss(d, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kd + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), is, k > 0);
-        commit2(&bars.s_full[j & 1]);
+        commit2(&bars.s_full[y & 1]);
         commit2(&bars.k_empty[st]);
         return true;
       };
-      bool ok = wait(c, &bars.q_full, 0) && scores(0);
-      for (int j = 0; ok && j < n; j++) {
-        if (j + 1 < n && !scores(j + 1)) break;
-        const int st = j % ST;
-        if (!wait(c, &bars.v_full[st], (j / ST) & 1)) break;
-        if (!wait(c, &bars.p_full[j & 1], (j >> 1) & 1)) break;
-        fence_after_sync();
-        const uint64_t vd = operand(sv + st * G::kKV, vmaj);
-        const uint32_t p = tm + kScoreCol + (j & 1) * 128;
+      for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
+        const int n = item_of(a, x).tiles;
+        if (!(ok = wait(c, &bars.q_full, r & 1) && scores(g))) break;
+        if (n == 1) commit2(&bars.q_empty);
+        for (int j = 0; j < n; j++, g++) {
+          if (j + 1 < n) {
+            if (!(ok = scores(g + 1))) break;
+            if (j + 2 == n) commit2(&bars.q_empty);
+          }
+          const int st = g % ST;
+          if (!(ok = wait(c, &bars.v_full[st], (g / ST) & 1) && wait(c, &bars.p_full[g & 1], (g >> 1) & 1))) break;
+          if (j == 0 && r > 0 && !(ok = wait(c, &bars.o_empty, (r - 1) & 1))) break;
+          fence_after_sync();
+          const uint64_t vd = operand(sv + st * G::kKV, vmaj);
+          const uint32_t p = tm + kScoreCol + (g & 1) * 128;
 #pragma unroll
-        for (int k = 0; k < kTileKeys / 16; k++) mma2_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
-        commit2(&bars.v_empty[st]);
-        commit2(&bars.pv_done);
+          for (int k = 0; k < kTileKeys / 16; k++) mma2_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
+          commit2(&bars.v_empty[st]);
+          commit2(&bars.pv_done);
+        }
       }
     }
-  } else if (warp >= 6) {
+  } else if (warp >= kEdgeWarp) {
     // ---- V tiles with keys that some row must not see
-    int edges = 0;
-    for (int j = it.edge; j < n; j++, edges++) {
-      const int st = j % ST;
-      // both warps meet at the barrier below for every tile, also after a timeout;
-      // then nothing is handed on: v_full may still be in an earlier tile's
-      // phase, which takes that tile's two arrivals and no more
-      const bool ok = wait_warp(c, &bars.v_edge[edges % 4], (edges / 4) & 1);
-      const int from = max(it.t0 + 1 - j * kTileKeys, 0);
-      constexpr int kPieces = D / 16;  // 16-byte pieces of a row in this CTA
-      bool found = false;
-      for (int x = threadIdx.x - 192; ok && x < (kTileKeys - from) * kPieces; x += 64) {
-        const int r = from + x / kPieces, p = x % kPieces;
-        const uint32_t at = sv + st * G::kKV + (p >> 3) * (kTileKeys * 128) + r * 128 + (p & 7) * 16;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (j * kTileKeys + r < it.end) {
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
-          const uint32_t m[4] = {not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w)};
-          if (!(m[0] | m[1] | m[2] | m[3])) continue;
-          found = true;
-          // 0xFFFF where bit 15 of the half is set
-          w.x &= ~((m[0] >> 15) * 0xFFFFu);
-          w.y &= ~((m[1] >> 15) * 0xFFFFu);
-          w.z &= ~((m[2] >> 15) * 0xFFFFu);
-          w.w &= ~((m[3] >> 15) * 0xFFFFu);
+    int edges = 0, g = 0;
+    for (int r = 0, x; (x = nth(a, r)) >= 0; r++) {
+      const Item it = item_of(a, x);
+      for (int j = 0; j < it.tiles; j++, g++) {
+        const int key0 = (it.first + j) * kTileKeys;
+        if (key0 + kTileKeys <= it.hidden) continue;
+        const int st = g % ST;
+        // both warps meet at the barrier below for every tile, also after a timeout;
+        // then nothing is handed on: v_full may still be in an earlier tile's
+        // phase, which takes that tile's two arrivals and no more
+        const bool ok = wait_warp(c, &bars.v_edge[edges % kEdgeBars], (edges / kEdgeBars) & 1);
+        edges++;
+        const int from = max(it.hidden - key0, 0);
+        constexpr int kPieces = D / 16;  // 16-byte pieces of a row in this CTA
+        bool found = false;
+        for (int y = threadIdx.x - kEdgeWarp * 32; ok && y < (kTileKeys - from) * kPieces; y += 64) {
+          const int row = from + y / kPieces, p = y % kPieces;
+          const uint32_t at = sv + st * G::kKV + (p >> 3) * (kTileKeys * 128) + row * 128 + (p & 7) * 16;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (key0 + row < it.keys) {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
+            const uint32_t m[4] = {not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w)};
+            if (!(m[0] | m[1] | m[2] | m[3])) continue;
+            found = true;
+            // 0xFFFF where bit 15 of the half is set
+            w.x &= ~((m[0] >> 15) * 0xFFFFu);
+            w.y &= ~((m[1] >> 15) * 0xFFFFu);
+            w.z &= ~((m[2] >> 15) * 0xFFFFu);
+            w.w &= ~((m[3] >> 15) * 0xFFFFu);
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
         }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+        if (found) {
+          store_at(peer_addr(s_addr(&fix[r % kFixes]), 0), r + 1);
+          store_at(peer_addr(s_addr(&fix[r % kFixes]), 1), r + 1);
+        }
+        fence_async_smem();
+        asm volatile("bar.sync 5, 64;" ::: "memory");
+        if (threadIdx.x == kEdgeWarp * 32 && ok && !*c.abort_flag) arrive_at(peer_addr(s_addr(&bars.v_full[st]), 0));
       }
-      if (found) {
-        store_at(peer_addr(s_addr(&fix), 0), 1);
-        store_at(peer_addr(s_addr(&fix), 1), 1);
-      }
-      fence_async_smem();
-      asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (threadIdx.x == 192 && ok && !*c.abort_flag) arrive_at(peer_addr(s_addr(&bars.v_full[st]), 0));
     }
   } else {
-    // ---- softmax: thread = row
-    const int row = threadIdx.x;
-    const int tok = it.t0 + (int)rank * a.tokens + row / a.per_tile;
-    const bool live = row < a.tokens * a.per_tile && tok < it.end;
-    const int hi = live ? tok + 1 : 0;  // keys the row sees
-    const uint32_t tw = tm + ((uint32_t)warp << 21);
+    // ---- softmax: warps w and w + 4 share 32 rows (thread = row), and halve their
+    // columns. A wait that gave up changes only what is handed on: the two warps
+    // go on meeting at their barrier.
+    const int q4 = warp & 3, half = warp >> 2, row = q4 * 32 + lane;
+    const uint32_t tw = tm + ((uint32_t)q4 << 21);
     const float cs = a.scale_log2;
-    float ref = -INFINITY, l = 0.f;
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory"); };
+    const int my_tok = row / a.per_tile, my_head = row % a.per_tile;
+    int g = 0;
     bool ok = true;
-    for (int j = 0; j < n; j++) {
-      if (!(ok = wait_warp(c, &bars.s_full[j & 1], (j >> 1) & 1))) break;
-      fence_after_sync();
-      const uint32_t ts = tw + kScoreCol + (j & 1) * 128;
-      float s[128];
+    for (int r = 0, x; (x = nth(a, r)) >= 0; r++) {
+      const Item it = item_of(a, x);
+      const int tok = (int)rank * a.tokens + my_tok;
+      const bool live = my_tok < a.tokens && it.row0 + tok < it.end_row;
+      const int hi = live ? sees(a, it, tok) : 0;  // keys the row sees
+      float ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < it.tiles; j++, g++) {
+        ok = wait_warp(c, &bars.s_full[g & 1], (g >> 1) & 1) && ok;
+        fence_after_sync();
+        const uint32_t ts = tw + kScoreCol + (g & 1) * 128;
+        float s[64];
+        tmem_ld32(ts + half * 64, s);
+        tmem_ld32(ts + half * 64 + 32, s + 32);
+        tmem_wait_ld_();
+        const int left = hi - (it.first + j) * kTileKeys - half * 64;
+        if (left < 64) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) tmem_ld32(ts + 32 * i, s + 32 * i);
-      tmem_wait_ld_();
-      const int left = hi - j * kTileKeys;
-      if (left < kTileKeys) {
+          for (int i = 0; i < 64; i++)
+            if (i >= left) s[i] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 0; i < 128; i++)
-          if (i >= left) s[i] = -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int i = 4; i < 128; i++) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-      const float want = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs - Exponent<T>::kShift;
-      const bool move = want > ref + kSlack;  // never for a row that sees nothing; always for its first keys
-      if (__any_sync(~0u, move)) {
-        const float f = move ? exp2_fast(ref - want) : 1.f;
-        if (move) ref = want;
-        l *= f;
-        if (j > 0) {
-          if (!(ok = wait_warp(c, &bars.pv_done, (j - 1) & 1))) break;
-          fence_after_sync();
-          const uint64_t ff = pair_of(f, f);
+        for (int i = 4; i < 64; i++) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        shared_max[g & 1][half][row] = mine;
+        meet();  // also: both warps hold their scores, whose columns the probabilities overwrite
+        const float want = fmaxf(mine, shared_max[g & 1][half ^ 1][row]) * cs - Exponent<T>::kShift;
+        const bool move = want > ref + kSlack;  // never for a row that sees nothing; always for its first keys
+        if (__any_sync(~0u, move)) {
+          const float f = move ? exp2_fast(ref - want) : 1.f;
+          if (move) ref = want;
+          l *= f;
+          if (j > 0) {
+            ok = wait_warp(c, &bars.pv_done, (g - 1) & 1) && ok;
+            fence_after_sync();
+            const uint64_t ff = pair_of(f, f);
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            float o[32];
-            tmem_ld32(tw + i, o);
-            tmem_wait_ld_();
-            uint32_t u[32];
+            for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
+              float o[32];
+              tmem_ld32(tw + i, o);
+              tmem_wait_ld_();
+              uint32_t u[32];
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float x, y;
-              parts_of(mul2(pair_of(o[k], o[k + 1]), ff), x, y);
-              u[k] = __float_as_uint(x);
-              u[k + 1] = __float_as_uint(y);
+              for (int k = 0; k < 32; k += 2) {
+                float y0, y1;
+                parts_of(mul2(pair_of(o[k], o[k + 1]), ff), y0, y1);
+                u[k] = __float_as_uint(y0);
+                u[k + 1] = __float_as_uint(y1);
+              }
+              tmem_st32(tw + i, u);
             }
-            tmem_st32(tw + i, u);
           }
         }
-      }
-      const float off = ref == -INFINITY ? 0.f : -ref;
-      const uint64_t c2 = pair_of(cs, cs), o2 = pair_of(off, off);
-      uint64_t sum2[2] = {0, 0};
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
+        const float off = ref == -INFINITY ? 0.f : -ref;
+        const uint64_t c2 = pair_of(cs, cs), o2 = pair_of(off, off);
+        uint64_t sum2[2] = {0, 0};
         uint32_t p[32];
 #pragma unroll
         for (int i = 0; i < 32; i++) {
-          float x, y;
-          parts_of(fma2(pair_of(s[h * 64 + 2 * i], s[h * 64 + 2 * i + 1]), c2, o2), x, y);
-          x = exp2_fast(x);
-          y = exp2_fast(y);
-          sum2[i & 1] = add2(sum2[i & 1], pair_of(x, y));
-          p[i] = pack2<T>(x, y);  // matrix operands of the inputs' type; their sum stays FP32
+          float y0, y1;
+          parts_of(fma2(pair_of(s[2 * i], s[2 * i + 1]), c2, o2), y0, y1);
+          y0 = exp2_fast(y0);
+          y1 = exp2_fast(y1);
+          sum2[i & 1] = add2(sum2[i & 1], pair_of(y0, y1));
+          p[i] = pack2<T>(y0, y1);  // matrix operands of the inputs' type; their sum stays FP32
         }
-        tmem_st32(ts + h * 32, p);
+        tmem_st32(ts + half * 32, p);
+        tmem_wait_st_();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.p_full[g & 1]), 0));
+        float y0, y1;
+        parts_of(add2(sum2[0], sum2[1]), y0, y1);
+        l += y0 + y1;
       }
-      tmem_wait_st_();
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive_at(peer_addr(s_addr(&bars.p_full[j & 1]), 0));
-      float x, y;
-      parts_of(add2(sum2[0], sum2[1]), x, y);
-      l += x + y;
-    }
-    // the last two: a parity says nothing of a phase that has yet to begin
-    if (ok && (n < 2 || wait_warp(c, &bars.pv_done, (n - 2) & 1)) && wait_warp(c, &bars.pv_done, (n - 1) & 1)) {
+      shared_sum[half][row] = l;
+      meet();
+      l += shared_sum[half ^ 1][row];
+      // the last two additions: a parity says nothing of a phase that has yet to begin
+      if (g > 1) ok = wait_warp(c, &bars.pv_done, (g - 2) & 1) && ok;
+      ok = wait_warp(c, &bars.pv_done, (g - 1) & 1) && ok;
       fence_after_sync();
       const float inv = 1.f / l;
-      const bool mend = *(volatile uint32_t*)&fix != 0;
-      T* out = reinterpret_cast<T*>(a.out) + (it.row0 + (long long)tok) * a.ldo + (long long)(it.head0 + row % a.per_tile) * D;
-      const T* v = reinterpret_cast<const T*>(a.vbase) + (long long)it.row0 * a.ldv + (long long)it.kvh * D;
+      const bool mend = *(volatile int*)&fix[r % kFixes] == r + 1;
+      if (live && ok && half == 0) store_sum(a, it, tok, it.head0 + my_head, ref, l);
 #pragma unroll 1
-      for (int i = 0; i < D; i += 32) {
+      for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
         float o[32];
         tmem_ld32(tw + i, o);
         tmem_wait_ld_();
-        if (live) {
-          if (mend)
-            for (int key = it.t0 + 1; key < hi; key++) {
-              const uint32_t* w = reinterpret_cast<const uint32_t*>(v + (long long)key * a.ldv + i);
-  #pragma unroll
-              for (int k = 0; k < 16; k++) {
-                const uint32_t x = w[k], m = not_finite<T>(x);
-                if (m & 0x8000u) o[2 * k] += value_of<T>(x, 0);
-                if (m & 0x80000000u) o[2 * k + 1] += value_of<T>(x, 1);
-              }
-            }
-  #pragma unroll
-          for (int k = 0; k < 4; k++) {
-            uint4 w;
-            w.x = pack2<T>(o[8 * k] * inv, o[8 * k + 1] * inv);
-            w.y = pack2<T>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-            w.z = pack2<T>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-            w.w = pack2<T>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
-            *reinterpret_cast<uint4*>(out + i + 8 * k) = w;
-          }
-        }
+        if (live && ok) store_row<T, D>(a, it, tok, it.head0 + my_head, i, o, inv, mend);
         __syncwarp();
       }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.o_empty), 0));
+      meet();  // shared_sum may be written again
     }
   }
   __syncwarp();
@@ -425,25 +560,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) prompt_
   fence_before_sync();
   __syncthreads();
   cluster_sync();
-  if (warp == 4) {
+  if (warp == kMmaWarp) {
     fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
   }
 }
 
-template <typename T, int D>
-int prompt_of(const PromptArgs& a, int pairs, cudaStream_t s) {
-  const void* fn = (const void*)prompt_tc_kernel<T, D>;
+template <typename T, int D, typename A>
+int launch_of(const A& a, cudaStream_t s) {
+  const void* fn = (const void*)attn_tc_kernel<T, D, A>;
   const int rc = opt_in_smem(fn, Geom<D>::kSmem);
   if (rc) return rc;
-  return launch_kernel(fn, dim3(2u * (unsigned)pairs), dim3(kThreads), Geom<D>::kSmem, s, const_cast<PromptArgs*>(&a), false, 1);
+  const int pairs = std::min(a.items, multiprocessors() / 2);
+  return launch_kernel(fn, dim3(2u * (unsigned)pairs), dim3(kThreads), Geom<D>::kSmem, s, const_cast<A*>(&a), false, 1);
+}
+template <typename A>
+int launch_any(const A& a, int act, int dim, cudaStream_t s) {
+  if (act == TFX_F16) return dim == 128 ? launch_of<__half, 128>(a, s) : launch_of<__half, 256>(a, s);
+  return dim == 128 ? launch_of<__nv_bfloat16, 128>(a, s) : launch_of<__nv_bfloat16, 256>(a, s);
 }
 
 }  // namespace
 
-int launch_prompt(const PromptArgs& a, int act, int dim, int pairs, cudaStream_t s) {
-  if (act == TFX_F16) return dim == 128 ? prompt_of<__half, 128>(a, pairs, s) : prompt_of<__half, 256>(a, pairs, s);
-  return dim == 128 ? prompt_of<__nv_bfloat16, 128>(a, pairs, s) : prompt_of<__nv_bfloat16, 256>(a, pairs, s);
-}
+int launch_prompt(const PromptArgs& a, int act, int dim, cudaStream_t s) { return launch_any(a, act, dim, s); }
+int launch_prefix(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s) { return launch_any(a, act, dim, s); }
 
 }  // namespace tfx

@@ -295,12 +295,6 @@ __device__ __forceinline__ void gave_up(int* err, int lane) {
   while (clock64() - t0 < 2000000) __nanosleep(1000);
 }
 
-__device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int i) {
-  const int s = a.seqs[i];
-  if (s < 0 || s >= a.slots) return 0;
-  return min(max(a.lens[s], 0), (int)min((long long)a.width << a.page_shift, (long long)INT_MAX));
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) decode_warp_kernel(const __grid_constant__ DecodeAttnArgs a) {
   constexpr int KS = Slice<D>::kKeys;
@@ -309,7 +303,9 @@ __global__ void __launch_bounds__(kWarps * 32) decode_warp_kernel(const __grid_c
   __shared__ int starts[TFX_ATTN_MAX_BATCH + 1];
   __shared__ int wsum[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
+  // after the tensor-core kernel, this one starts where that leaves room: they
+  // share no memory that is written, and that one began after all that came before
+  if (!a.pre_splits) griddep_wait();
   Ring rg = make_ring<D>(dyn, full, warp, lane);
   // own slices before each sequence
   int carry = 0;
@@ -338,7 +334,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_warp_kernel(const __grid_c
   __syncthreads();
   const int own = starts[a.batch];
   const int tiles = (a.group + 15) / 16, ptiles = (a.batch * a.group + 15) / 16;
-  const int sp = (a.shared + KS - 1) / KS;
+  const int sp = a.pre_splits ? 0 : (a.shared + KS - 1) / KS;
   const long long pre_total = (long long)a.heads_kv * ptiles * sp;
   const long long total = pre_total + (long long)a.heads_kv * tiles * own;
   const long long per = max((total + a.warps - 1) / a.warps, 4LL);
@@ -421,6 +417,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_warp_kernel(const __grid_c
     }
     x += s1 - s0;
   }
+  if (a.pre_splits) griddep_wait();  // this grid's end says to the next that both are done
 }
 
 // One CTA per (sequence, query head): the row's partial results, prefix first,
@@ -436,7 +433,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
   const int i = blockIdx.x / a.heads_q, head = blockIdx.x % a.heads_q;
   const int kvh = head / a.group, gh = head % a.group;
   const int tiles = (a.group + 15) / 16, ptiles = (a.batch * a.group + 15) / 16;
-  const int sp = (a.shared + KS - 1) / KS, own = a.starts[a.batch];
+  const int sp = a.pre_splits ? 0 : (a.shared + KS - 1) / KS, own = a.starts[a.batch];
   const long long per = a.starts[a.batch + 1];
   const long long pre_total = (long long)a.heads_kv * ptiles * sp;
   float m = -INFINITY, l = 0.f, o[V];
@@ -456,6 +453,10 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
     }
     m = mn;
   };
+  for (int z = warp; z < a.pre_splits; z += kWarps) {
+    const long long row = (long long)z * a.batch * a.heads_q + blockIdx.x;
+    take(a.pre_o + row * D, a.pre_ml[row]);
+  }
   if (sp) {
     const int r = i * a.group + gh, grp = kvh * ptiles + r / 16;
     const long long x0 = (long long)grp * sp, x1 = x0 + sp;
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
     f[w] = exp2_fast(sml[w].x - ref);
     sum += sml[w].y * f[w];
   }
-  const float inv = seq_len(a, i) == 0 ? 0.f : 1.f / sum;  // a sequence without tokens: zeros
+  const bool none = seq_len(a, i) == 0;  // a sequence without tokens: zeros
+  const float inv = 1.f / sum;
   T* out = reinterpret_cast<T*>(a.out) + (long long)i * a.ldo + (long long)head * D;
   for (int c = threadIdx.x * 2; c < D; c += kWarps * 64) {
     float x = 0.f, y = 0.f;
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
       x += so[w][c] * f[w];
       y += so[w][c + 1] * f[w];
     }
-    *reinterpret_cast<uint32_t*>(out + c) = pack2<T>(x * inv, y * inv);
+    *reinterpret_cast<uint32_t*>(out + c) = none ? 0u : pack2<T>(x * inv, y * inv);
   }
 }
 
@@ -505,7 +507,7 @@ int decode_of(const DecodeAttnArgs& a, cudaStream_t s) {
   int rc = opt_in_smem(fn, warp_smem<D>());
   if (rc) return rc;
   rc = launch_kernel(fn, dim3((unsigned)(a.warps / kWarps)), dim3(kWarps * 32), warp_smem<D>(), s,
-                     const_cast<DecodeAttnArgs*>(&a), false, 1);
+                     const_cast<DecodeAttnArgs*>(&a), a.pre_splits > 0, 1);
   if (rc) return rc;
   return launch_kernel((const void*)decode_join_kernel<T, D>, dim3((unsigned)(a.batch * a.heads_q)), dim3(kWarps * 32), 0,
                        s, const_cast<DecodeAttnArgs*>(&a), true, 1);

@@ -247,6 +247,11 @@ DECODES = [
     (28, 4, 128, 64, 4100, [77, 1, 2, 190] * 10),
     (6, 1, 256, 64, 2048, [(7 * i) % 90 + 1 for i in range(64)]),
     (24, 4, 256, 64, 9, [(7 * i) % 90 + 1 for i in range(70)]),
+    (24, 4, 256, 128, 1100, [(5 * i) % 33 + 1 for i in range(45)]),
+    (24, 4, 256, 16, 1003, [1] * 20),
+    (12, 4, 256, 32, 300, [3, 70, 1] * 5),
+    (128, 1, 128, 16, 700, [3, 4, 50]),
+    (8, 8, 256, 64, 640, [2, 9] * 20),
 ]
 
 
@@ -263,7 +268,7 @@ def test_decode(dtype, hq, hkv, dim, page, shared, lens):
     check_decode(tfx.attn_decode(c, 1, q, seqs, shared=shared), c, 1, q, seqs)
 
 
-@pytest.mark.parametrize("shared", [0, 128, 130])
+@pytest.mark.parametrize("shared", [0, 128, 130, 600, 640])
 def test_decode_of_uneven_batches(shared):
     """An empty sequence, a slot out of range, one shorter than the shared prefix."""
     lens = [40, 2000, 7, 0]
