@@ -49,12 +49,12 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kCopyWarp = 9, kEdgeWarp = 10;  // 0..7 softmax, 10 and 11 edges
 constexpr int kTileKeys = 128;
 constexpr float kSlack = 8.f;  // log2 by which a row's maximum may pass its reference
-constexpr uint32_t kScoreCol = 256;
 constexpr int kEdgeBars = 4, kFixes = 8;
 
 template <int D>
 struct Geom {
   static constexpr int kStages = D == 256 ? 2 : 4;
+  static constexpr int kScores = D == 256 ? 2 : 3;  // score buffers: what O leaves of the 512 columns, at most 3
   static constexpr int kQ = 128 * D * 2;       // bytes of Q in a CTA
   static constexpr int kKV = 64 * D * 2;       // bytes of K, or of V, of a stage in a CTA
   static constexpr size_t kSmem = (size_t)kQ + 2 * kStages * kKV + 1024;
@@ -64,9 +64,11 @@ struct Barriers {
   uint64_t q_full, q_empty;
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t v_edge[kEdgeBars];  // V tiles that warps 10 and 11 look at before the MMAs may
-  uint64_t s_full[2];          // scores are in tensor memory
-  uint64_t p_full[2];          // probabilities of both CTAs are
-  uint64_t pv_done;            // P V of a tile is added
+  uint64_t s_full[3];          // scores are in tensor memory
+  uint64_t p_full[3];          // probabilities of both CTAs are
+  // P V of a tile is added. One a score buffer, like the two above: a parity tells
+  // two phases apart, and a tile's scores come after the addition SB tiles before.
+  uint64_t pv_done[3];
   uint64_t o_empty;            // both CTAs have read an item's result
 };
 
@@ -78,9 +80,10 @@ struct Ctx {
 };
 
 __device__ __forceinline__ bool wait(const Ctx& c, uint64_t* bar, uint32_t parity) {
-  if (mbar_poll_cluster(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_poll_cluster(bar, parity)) {
+  while (true) {
+    for (int i = 0; i < 16; i++)
+      if (mbar_poll(bar, parity)) return true;
     if (*c.abort_flag) return false;
     if (clock64() - t0 > c.spin) {
       *c.abort_flag = 1;
@@ -88,17 +91,23 @@ __device__ __forceinline__ bool wait(const Ctx& c, uint64_t* bar, uint32_t parit
       return false;
     }
   }
-  return true;
 }
-
-// For a whole warp: one lane waits, so that the lanes are together again for the
-// warp-wide instructions that follow, after a timeout too.
+// For a whole warp. One lane does the waiting proper, so that the lanes are
+// together again for the warp-wide instructions that follow, after a timeout too.
 __device__ __forceinline__ bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(~0u, mbar_poll(bar, parity))) return true;
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = wait(c, bar, parity);
   ok = __shfl_sync(~0u, ok, 0);
-  __syncwarp();
   return ok != 0;
+}
+
+// The two warps that share rows meet at their named barrier.
+__device__ __forceinline__ void bar_meet(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
 }
 
 template <typename T>
@@ -282,7 +291,7 @@ __device__ __forceinline__ void store_sum(const DecodeAttnArgs& a, const Item& i
 template <typename T, int D, typename A>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ A a) {
   using G = Geom<D>;
-  constexpr int ST = G::kStages;
+  constexpr int ST = G::kStages, SB = G::kScores;
   extern __shared__ uint8_t dyn[];
   __shared__ Barriers bars;
   __shared__ uint32_t tmem_slot;
@@ -307,11 +316,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     }
     for (int i = 0; i < kEdgeBars; i++) mbar_init(&bars.v_edge[i], 1);
     for (int i = 0; i < kFixes; i++) fix[i] = 0;
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < 3; i++) {
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.p_full[i], 16);
+      mbar_init(&bars.pv_done[i], 1);
     }
-    mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.o_empty, 16);
     fence_mbar_init();
   }
@@ -325,6 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   fence_after_sync();
   const uint32_t tm = *(volatile uint32_t*)&tmem_slot;
   griddep_launch();  // what follows waits for this grid before it reads what it wrote
+  // registers: 384 x 168 at launch; 256 x 208 + 128 x 80 = 63,488 of those 64,512 from here on
+  if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
 
   if (warp == kCopyWarp) {
     // ---- copies: this CTA's rows of Q, its 64 keys of K, its dim/2 columns of V
@@ -357,43 +368,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     }
   } else if (warp == kMmaWarp) {
     // ---- MMAs
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t is = idesc<T>(kTileKeys, false), ip = idesc<T>(D, true);
       constexpr uint64_t kmaj = operand_bits(16), vmaj = operand_bits(kTileKeys * 128);
       int g = 0;
       bool ok = true;
-      auto scores = [&](int y) -> bool {
+      auto scores = [&](int y, bool last) -> bool {
         const int st = y % ST;
-        if (!wait(c, &bars.k_full[st], (y / ST) & 1)) return false;
+        if (!wait_warp(c, &bars.k_full[st], (y / ST) & 1)) return false;
         fence_after_sync();
         const uint64_t qd = operand(sq, kmaj), kd = operand(sk + st * G::kKV, kmaj);
-        const uint32_t d = tm + kScoreCol + (y & 1) * 128;
+        const uint32_t d = tm + D + (y % SB) * 128;
+        if (elected()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; k++)
-          mma2_ss(d, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kd + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), is, k > 0);
-        commit2(&bars.s_full[y & 1]);
-        commit2(&bars.k_empty[st]);
+          for (int k = 0; k < D / 16; k++)
+            mma2_ss(d, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kd + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), is, k > 0);
+          commit2(&bars.s_full[y % SB]);
+          commit2(&bars.k_empty[st]);
+          if (last) commit2(&bars.q_empty);
+        }
+        __syncwarp();
         return true;
       };
       for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
         const int n = item_of(a, x).tiles;
-        if (!(ok = wait(c, &bars.q_full, r & 1) && scores(g))) break;
-        if (n == 1) commit2(&bars.q_empty);
+        if (!(ok = wait_warp(c, &bars.q_full, r & 1))) break;
+        int ahead = 0;  // scores of the item's tiles issued: up to SB - 1 more than the products with V
         for (int j = 0; j < n; j++, g++) {
-          if (j + 1 < n) {
-            if (!(ok = scores(g + 1))) break;
-            if (j + 2 == n) commit2(&bars.q_empty);
-          }
+          for (; ok && ahead < n && ahead < j + SB; ahead++) ok = scores(g - j + ahead, ahead + 1 == n);
+          if (!ok) break;
           const int st = g % ST;
-          if (!(ok = wait(c, &bars.v_full[st], (g / ST) & 1) && wait(c, &bars.p_full[g & 1], (g >> 1) & 1))) break;
-          if (j == 0 && r > 0 && !(ok = wait(c, &bars.o_empty, (r - 1) & 1))) break;
+          if (!(ok = wait_warp(c, &bars.v_full[st], (g / ST) & 1) && wait_warp(c, &bars.p_full[g % SB], (g / SB) & 1))) break;
+          if (j == 0 && r > 0 && !(ok = wait_warp(c, &bars.o_empty, (r - 1) & 1))) break;
           fence_after_sync();
           const uint64_t vd = operand(sv + st * G::kKV, vmaj);
-          const uint32_t p = tm + kScoreCol + (g & 1) * 128;
+          const uint32_t p = tm + D + (g % SB) * 128;
+          if (elected()) {
 #pragma unroll
-          for (int k = 0; k < kTileKeys / 16; k++) mma2_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
-          commit2(&bars.v_empty[st]);
-          commit2(&bars.pv_done);
+            for (int k = 0; k < kTileKeys / 16; k++) mma2_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
+            commit2(&bars.v_empty[st]);
+            commit2(&bars.pv_done[g % SB]);
+          }
+          __syncwarp();
         }
       }
     }
@@ -434,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         if (found) {
           store_at(peer_addr(s_addr(&fix[r % kFixes]), 0), r + 1);
           store_at(peer_addr(s_addr(&fix[r % kFixes]), 1), r + 1);
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
         fence_async_smem();
         asm volatile("bar.sync 5, 64;" ::: "memory");
@@ -444,10 +461,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     // ---- softmax: warps w and w + 4 share 32 rows (thread = row), and halve their
     // columns. A wait that gave up changes only what is handed on: the two warps
     // go on meeting at their barrier.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int q4 = warp & 3, half = warp >> 2, row = q4 * 32 + lane;
     const uint32_t tw = tm + ((uint32_t)q4 << 21);
     const float cs = a.scale_log2;
-    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory"); };
     const int my_tok = row / a.per_tile, my_head = row % a.per_tile;
     int g = 0;
     bool ok = true;
@@ -457,13 +474,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       const bool live = my_tok < a.tokens && it.row0 + tok < it.end_row;
       const int hi = live ? sees(a, it, tok) : 0;  // keys the row sees
       float ref = -INFINITY, l = 0.f;
+      float s[64];
+      auto scores_of = [&](int y) {  // asks for this warp's columns of a tile's scores
+        const uint32_t t = tw + D + (y % SB) * 128 + half * 64;
+        tmem_ld32(t, s);
+        tmem_ld32(t + 32, s + 32);
+      };
       for (int j = 0; j < it.tiles; j++, g++) {
-        ok = wait_warp(c, &bars.s_full[g & 1], (g >> 1) & 1) && ok;
+        ok = wait_warp(c, &bars.s_full[g % SB], (g / SB) & 1) && ok;
         fence_after_sync();
-        const uint32_t ts = tw + kScoreCol + (g & 1) * 128;
-        float s[64];
-        tmem_ld32(ts + half * 64, s);
-        tmem_ld32(ts + half * 64 + 32, s + 32);
+        scores_of(g);
         tmem_wait_ld_();
         const int left = hi - (it.first + j) * kTileKeys - half * 64;
         if (left < 64) {
@@ -473,10 +493,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < 64; i++) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int i = 4; i < 60; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; k++) mx[k] = max3(mx[k], s[i + k], s[i + k + 4]);
+#pragma unroll
+        for (int k = 0; k < 4; k++) mx[k] = fmaxf(mx[k], s[60 + k]);
+        const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         shared_max[g & 1][half][row] = mine;
-        meet();  // also: both warps hold their scores, whose columns the probabilities overwrite
+        bar_meet(1 + q4);  // also: both warps hold their scores, whose columns the probabilities overwrite
         const float want = fmaxf(mine, shared_max[g & 1][half ^ 1][row]) * cs - Exponent<T>::kShift;
         const bool move = want > ref + kSlack;  // never for a row that sees nothing; always for its first keys
         if (__any_sync(~0u, move)) {
@@ -484,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
           if (move) ref = want;
           l *= f;
           if (j > 0) {
-            ok = wait_warp(c, &bars.pv_done, (g - 1) & 1) && ok;
+            ok = wait_warp(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
             fence_after_sync();
             const uint64_t ff = pair_of(f, f);
 #pragma unroll 1
@@ -507,31 +531,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         const float off = ref == -INFINITY ? 0.f : -ref;
         const uint64_t c2 = pair_of(cs, cs), o2 = pair_of(off, off);
         uint64_t sum2[2] = {0, 0};
-        uint32_t p[32];
+        const uint32_t tp = tw + D + (g % SB) * 128 + half * 32;
 #pragma unroll
-        for (int i = 0; i < 32; i++) {
-          float y0, y1;
-          parts_of(fma2(pair_of(s[2 * i], s[2 * i + 1]), c2, o2), y0, y1);
-          y0 = exp2_fast(y0);
-          y1 = exp2_fast(y1);
-          sum2[i & 1] = add2(sum2[i & 1], pair_of(y0, y1));
-          p[i] = pack2<T>(y0, y1);  // matrix operands of the inputs' type; their sum stays FP32
+        for (int h = 0; h < 2; h++) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            float y0, y1;
+            parts_of(fma2(pair_of(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1]), c2, o2), y0, y1);
+            y0 = exp2_fast(y0);
+            y1 = exp2_fast(y1);
+            sum2[i & 1] = add2(sum2[i & 1], pair_of(y0, y1));
+            p[i] = pack2<T>(y0, y1);  // matrix operands of the inputs' type; their sum stays FP32
+          }
+          tmem_st16u(tp + h * 16, p);
         }
-        tmem_st32(ts + half * 32, p);
         tmem_wait_st_();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.p_full[g & 1]), 0));
+        if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.p_full[g % SB]), 0));
         float y0, y1;
         parts_of(add2(sum2[0], sum2[1]), y0, y1);
         l += y0 + y1;
       }
       shared_sum[half][row] = l;
-      meet();
+      bar_meet(1 + q4);
       l += shared_sum[half ^ 1][row];
-      // the last two additions: a parity says nothing of a phase that has yet to begin
-      if (g > 1) ok = wait_warp(c, &bars.pv_done, (g - 2) & 1) && ok;
-      ok = wait_warp(c, &bars.pv_done, (g - 1) & 1) && ok;
+      ok = wait_warp(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
       fence_after_sync();
       const float inv = 1.f / l;
       const bool mend = *(volatile int*)&fix[r % kFixes] == r + 1;
@@ -546,8 +572,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       }
       fence_before_sync();
       __syncwarp();
-      if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.o_empty), 0));
-      meet();  // shared_sum may be written again
+      // only where another item follows: see arrive_at
+      if (lane == 0 && ok && nth(a, r + 1) >= 0) arrive_at(peer_addr(s_addr(&bars.o_empty), 0));
+      bar_meet(1 + q4);  // shared_sum may be written again
     }
   }
   __syncwarp();
