@@ -328,6 +328,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s_addr(&tmem_slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  // rows of Q that no copy writes
+  for (int x = a.tokens * a.per_tile * 8 + threadIdx.x; x < 128 * 8; x += kThreads)
+    for (int ch = 0; ch < D / 64; ch++)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(sq + ch * 16384 + x * 16), "r"(0u) : "memory");
+  fence_async_smem();
   fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -472,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       const Item it = item_of(a, x);
       const int tok = (int)rank * a.tokens + my_tok;
       const bool live = my_tok < a.tokens && it.row0 + tok < it.end_row;
-      const int hi = live ? sees(a, it, tok) : 0;  // keys the row sees
+      const int hi = live ? sees(a, it, tok) : INT_MAX;  // keys the row sees; a row that is no token's is not stored
       float ref = -INFINITY, l = 0.f;
       float s[64];
       auto scores_of = [&](int y) {  // asks for this warp's columns of a tile's scores
@@ -486,7 +491,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         scores_of(g);
         tmem_wait_ld_();
         const int left = hi - (it.first + j) * kTileKeys - half * 64;
-        if (left < 64) {
+        if (__any_sync(~0u, left < 64)) {
+          asm volatile("");  // keeps this a branch: as 64 selects in every tile it took a third of the time
 #pragma unroll
           for (int i = 0; i < 64; i++)
             if (i >= left) s[i] = -INFINITY;
