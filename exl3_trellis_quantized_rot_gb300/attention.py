@@ -9,6 +9,14 @@ every step runs in the kernels of ``libtfx_exl3.so``. Names follow the C ABI:
 from __future__ import annotations
 
 import ctypes as C
+import sys
+
+try:
+    import torch
+except ImportError:  # the package itself imports without it; the calls below take its tensors
+    torch = None
+
+_pkg = sys.modules[__package__]  # being imported when this runs: its functions are looked up at each call
 
 CACHE_FULL, CACHE_BAD, CACHE_TABLE_FULL = 1, 2, 4
 MAX_BATCH = 4096
@@ -48,41 +56,53 @@ def declare(L: C.CDLL) -> None:
     L.tfx_cache_book_ints.restype = l64
 
 
-def _base():
-    import exl3_trellis_quantized_rot_gb300 as tfx
-    return tfx
+_act_of = {torch.float16: 0, torch.bfloat16: 1} if torch else {}  # TFX_F16, TFX_BF16
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if torch else None  # absent without CUDA
+
+
+def _lib():
+    return _pkg.lib()
+
+
+def _check(rc: int) -> None:
+    if rc:
+        raise _pkg.TfxError(rc, _pkg.last_error())
+
+
+def _stream(stream, device: int) -> int:
+    """A stream's handle; by default torch's current one on the device."""
+    if stream is None:
+        return _raw_stream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _act(dtype) -> int:
-    import torch
-    tfx = _base()
-    if dtype == torch.float16:
-        return tfx.F16
-    if dtype == torch.bfloat16:
-        return tfx.BF16
-    raise ValueError(f"dtype {dtype}: float16 or bfloat16")
+    act = _act_of.get(dtype)
+    if act is None:
+        raise ValueError(f"dtype {dtype}: float16 or bfloat16")
+    return act
 
 
-def _rows(name: str, t, heads: int, dim: int, like) -> None:
-    """t is (rows, heads, dim) with whole rows (heads and values contiguous), on one device and in one type."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} of shape {tuple(t.shape)}: (rows, {heads}, {dim}) is wanted")
-    if t.dtype != like.dtype or t.device != like.device or not t.is_cuda:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, not {like.dtype} on {like.device} (a CUDA device)")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+def _rows(name: str, t, heads: int, dim: int, dtype, device: int) -> tuple:
+    """Checks that t is (rows, heads, dim) with whole rows (heads and values lie next
+    to each other) of a type and on a CUDA device; (rows, pitch, address)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} of shape {tuple(shape)}: (rows, {heads}, {dim}) is wanted")
+    if t.dtype is not dtype or device < 0 or t.get_device() != device:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}: {dtype} on CUDA device {device} is wanted")
+    row, head, value = t.stride()
+    if value != 1 or (head != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a row must lie next to each other")
-
-
-def _pitch(t) -> int:
     # a single row's pitch is not used, and torch may give it any stride
-    return t.stride(0) if t.shape[0] > 1 else max(8, t.shape[1] * t.shape[2])
+    return shape[0], row if shape[0] > 1 else heads * dim, t.data_ptr()
 
 
-def _ints(name: str, t, device) -> int:
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1) or t.device != device:
-        raise ValueError(f"{name}: a contiguous int32 vector on {device} is wanted")
-    return t.data_ptr()
+def _ints(name: str, t, device: int) -> tuple:
+    """(length, address) of a contiguous int32 vector; device -1 is the CPU."""
+    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 vector on {'the CPU' if device < 0 else f'CUDA device {device}'} is wanted")
+    return t.numel(), t.data_ptr()
 
 
 def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=None):
@@ -91,33 +111,28 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
     int32 tensor on the CPU, sequence i is rows offsets[i]:offsets[i+1].
     scale: 1/sqrt(dim) by default. Returns out (rows outside the sequences of
     an out that is made here are zero)."""
-    import torch
-    tfx = _base()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v are (rows, heads, dim)")
-    T, hq, dim = q.shape
-    hkv = k.shape[1]
-    _rows("q", q, hq, dim, q)
-    _rows("k", k, hkv, dim, q)
-    _rows("v", v, hkv, dim, q)
-    po = _ints("offsets", offsets, torch.device("cpu"))
-    n = offsets.numel() - 1
-    if n < 0:
+    _, hq, dim = q.shape
+    hkv, dtype, dev = k.shape[1], q.dtype, q.get_device()
+    T, ldq, pq = _rows("q", q, hq, dim, dtype, dev)
+    Tk, ldk, pk = _rows("k", k, hkv, dim, dtype, dev)
+    Tv, ldv, pv = _rows("v", v, hkv, dim, dtype, dev)
+    n, po = _ints("offsets", offsets, -1)
+    if n < 1:
         raise ValueError("offsets holds at least one value")
-    first, last = int(offsets[0]), int(offsets[-1])
-    if last > min(T, k.shape[0], v.shape[0]):
+    first, last = C.c_int32.from_address(po).value, C.c_int32.from_address(po + 4 * (n - 1)).value
+    if last > min(T, Tk, Tv):
         raise ValueError(f"offsets end at {last}, past the rows of q, k or v")
     if out is None:
-        out = torch.empty((T, hq, dim), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, hq, dim), dtype=dtype, device=q.device)
         if first > 0 or last < T:
             out.zero_()
-    else:
-        _rows("out", out, hq, dim, q)
-        if out.shape[0] < last:
-            raise ValueError(f"out has {out.shape[0]} rows, offsets end at {last}")
-    h = HeadsStruct(hq, hkv, dim, _act(q.dtype), dim ** -0.5 if scale is None else scale)
-    tfx._check(tfx.lib().tfx_attn_prompt(C.byref(h), q.data_ptr(), _pitch(q), k.data_ptr(), _pitch(k), v.data_ptr(),
-                                         _pitch(v), po, n, out.data_ptr(), _pitch(out), tfx._stream(stream)))
+    To, ldo, pout = _rows("out", out, hq, dim, dtype, dev)
+    if To < last:
+        raise ValueError(f"out has {To} rows, offsets end at {last}")
+    h = HeadsStruct(hq, hkv, dim, _act(dtype), dim ** -0.5 if scale is None else scale)
+    _check(_lib().tfx_attn_prompt(C.byref(h), pq, ldq, pk, ldk, pv, ldv, po, n - 1, pout, ldo, _stream(stream, dev)))
     return out
 
 
@@ -130,7 +145,6 @@ class Cache:
     """
 
     def __init__(self, k, v, slots: int, width: int, book=None):
-        import torch
         if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v are (layers, pages, page_size, kv_heads, dim), of one shape, type and device")
         if not k.is_contiguous() or not v.is_contiguous():
@@ -144,7 +158,8 @@ class Cache:
             book[4 + slots + pages:] = -1
         elif book.numel() != ints:
             raise ValueError(f"book of {book.numel()} values, {ints} are wanted")
-        self.s.book = _ints("book", book, k.device)
+        self.device, self.dtype, self.heads_kv, self.dim = k.get_device(), k.dtype, heads, dim
+        self.s.book = _ints("book", book, self.device)[1]
         self.k, self.v, self.book = k, v, book
 
     @property
@@ -168,107 +183,95 @@ class Cache:
 
     def __del__(self):
         try:
-            tfx = _base()
-            if self.s.priv and tfx._lib is not None:
-                tfx._lib.tfx_cache_release(C.byref(self.s))
+            if self.s.priv and _pkg._lib is not None:
+                _pkg._lib.tfx_cache_release(C.byref(self.s))
         except Exception:
             pass
 
 
 def cache_reserve(c: Cache, max_batch: int, heads: int, stream=None) -> None:
     """Scratch for attn_decode over up to max_batch sequences of `heads` query heads, and for the page calls."""
-    tfx = _base()
-    tfx._check(tfx.lib().tfx_cache_reserve(c.ref(), max_batch, heads, tfx._stream(stream)))
+    _check(_lib().tfx_cache_reserve(c.ref(), max_batch, heads, _stream(stream, c.device)))
 
 
 def cache_release(c: Cache) -> None:
-    tfx = _base()
-    tfx._check(tfx.lib().tfx_cache_release(c.ref()))
+    _check(_lib().tfx_cache_release(c.ref()))
 
 
 def cache_extend(c: Cache, seqs, offsets, stream=None) -> None:
     """Room for offsets[i+1] - offsets[i] new tokens of sequence seqs[i] (int32 vectors on the cache's device)."""
-    tfx = _base()
-    n = seqs.numel()
-    if offsets.numel() != n + 1:
-        raise ValueError(f"{offsets.numel()} offsets for {n} sequences")
-    tfx._check(tfx.lib().tfx_cache_extend(c.ref(), _ints("seqs", seqs, c.k.device), _ints("offsets", offsets, c.k.device), n,
-                                          tfx._stream(stream)))
+    n, ps = _ints("seqs", seqs, c.device)
+    m, po = _ints("offsets", offsets, c.device)
+    if m != n + 1:
+        raise ValueError(f"{m} offsets for {n} sequences")
+    _check(_lib().tfx_cache_extend(c.ref(), ps, po, n, _stream(stream, c.device)))
 
 
 def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=None) -> None:
     """K and V (rows, kv_heads, dim) of one layer's new tokens, into the room that
     the last cache_extend made. seqs and offsets are that call's and may be left
     out: where each row goes was settled there."""
-    tfx = _base()
-    _rows("k", k, c.s.heads_kv, c.s.dim, c.k)
-    _rows("v", v, c.s.heads_kv, c.s.dim, c.k)
-    if k.shape[0] != v.shape[0]:
-        raise ValueError(f"{k.shape[0]} rows of k, {v.shape[0]} of v")
+    n, ldk, pk = _rows("k", k, c.heads_kv, c.dim, c.dtype, c.device)
+    m, ldv, pv = _rows("v", v, c.heads_kv, c.dim, c.dtype, c.device)
+    if n != m:
+        raise ValueError(f"{n} rows of k, {m} of v")
     if offsets is not None and seqs is not None and offsets.numel() != seqs.numel() + 1:
         raise ValueError(f"{offsets.numel()} offsets for {seqs.numel()} sequences")
-    tfx._check(tfx.lib().tfx_cache_append(c.ref(), layer, k.data_ptr(), _pitch(k), v.data_ptr(), _pitch(v), k.shape[0],
-                                          tfx._stream(stream)))
+    _check(_lib().tfx_cache_append(c.ref(), layer, pk, ldk, pv, ldv, n, _stream(stream, c.device)))
 
 
-def _pair(name: str, c: Cache, src, dst):
-    if src.numel() != dst.numel():
-        raise ValueError(f"{name}: {src.numel()} sources, {dst.numel()} targets")
-    return _ints("src", src, c.k.device), _ints("dst", dst, c.k.device), src.numel()
+def _pair(c: Cache, src, dst) -> tuple:
+    n, ps = _ints("src", src, c.device)
+    m, pd = _ints("dst", dst, c.device)
+    if n != m:
+        raise ValueError(f"{n} sources, {m} targets")
+    return ps, pd, n
 
 
 def cache_fork(c: Cache, src, dst, stream=None) -> None:
     """Slot dst[i] becomes a copy of sequence src[i]: full pages shared, a partly filled last one copied."""
-    tfx = _base()
-    tfx._check(tfx.lib().tfx_cache_fork(c.ref(), *_pair("fork", c, src, dst), tfx._stream(stream)))
+    _check(_lib().tfx_cache_fork(c.ref(), *_pair(c, src, dst), _stream(stream, c.device)))
 
 
 def cache_free(c: Cache, seqs, stream=None) -> None:
     """The sequences give their pages back."""
-    tfx = _base()
-    tfx._check(tfx.lib().tfx_cache_free(c.ref(), _ints("seqs", seqs, c.k.device), seqs.numel(), tfx._stream(stream)))
+    n, ps = _ints("seqs", seqs, c.device)
+    _check(_lib().tfx_cache_free(c.ref(), ps, n, _stream(stream, c.device)))
 
 
 def cache_compact(c: Cache, stream=None) -> None:
     """Moves the used pages to the front of the pool; book[1] is the number moved."""
-    tfx = _base()
-    tfx._check(tfx.lib().tfx_cache_compact(c.ref(), tfx._stream(stream)))
+    _check(_lib().tfx_cache_compact(c.ref(), _stream(stream, c.device)))
 
 
 def cache_copy(c: Cache, src, dst, stream=None) -> None:
     """Contents of page src[i] to page dst[i], all layers."""
-    tfx = _base()
-    tfx._check(tfx.lib().tfx_cache_copy(c.ref(), *_pair("copy", c, src, dst), tfx._stream(stream)))
+    _check(_lib().tfx_cache_copy(c.ref(), *_pair(c, src, dst), _stream(stream, c.device)))
 
 
 def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | None = None, out=None, stream=None):
     """Attention of one new token of each sequence seqs[i] over the cache's tokens
     (tfx_attn_decode). q: (batch, heads, dim); the first `shared` tokens, the same
     in all of them, are read once. Returns out."""
-    import torch
-    tfx = _base()
     if q.dim() != 3:
         raise ValueError("q is (batch, heads, dim)")
-    b, hq, dim = q.shape
-    _rows("q", q, hq, c.s.dim, c.k)
-    ps = _ints("seqs", seqs, c.k.device)
-    if seqs.numel() != b:
-        raise ValueError(f"{seqs.numel()} sequences for {b} rows of q")
+    hq, dim, dev = q.shape[1], c.dim, c.device
+    b, ldq, pq = _rows("q", q, hq, dim, c.dtype, dev)
+    n, ps = _ints("seqs", seqs, dev)
+    if n != b:
+        raise ValueError(f"{n} sequences for {b} rows of q")
     if out is None:
-        out = torch.empty((b, hq, dim), dtype=q.dtype, device=q.device)
-    else:
-        _rows("out", out, hq, dim, q)
-        if out.shape[0] != b:
-            raise ValueError(f"out has {out.shape[0]} rows, q {b}")
-    h = HeadsStruct(hq, c.s.heads_kv, dim, c.s.act, dim ** -0.5 if scale is None else scale)
-    tfx._check(tfx.lib().tfx_attn_decode(c.ref(), layer, C.byref(h), q.data_ptr(), _pitch(q), ps, b, shared, out.data_ptr(),
-                                         _pitch(out), tfx._stream(stream)))
+        out = torch.empty((b, hq, dim), dtype=c.dtype, device=q.device)
+    bo, ldo, po = _rows("out", out, hq, dim, c.dtype, dev)
+    if bo != b:
+        raise ValueError(f"out has {bo} rows, q {b}")
+    h = HeadsStruct(hq, c.heads_kv, dim, c.s.act, dim ** -0.5 if scale is None else scale)
+    _check(_lib().tfx_attn_decode(c.ref(), layer, C.byref(h), pq, ldq, ps, b, shared, po, ldo, _stream(stream, dev)))
     return out
 
 
 def attn_error() -> int:
     """The attention kernels' device error word (0, or 1: a bounded wait gave up); reading clears it."""
-    tfx = _base()
     e = C.c_int()
-    tfx._check(tfx.lib().tfx_attn_debug_error(C.byref(e)))
+    _check(_lib().tfx_attn_debug_error(C.byref(e)))
     return e.value

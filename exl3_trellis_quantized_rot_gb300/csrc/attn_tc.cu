@@ -213,46 +213,67 @@ __device__ __forceinline__ int sees(const DecodeAttnArgs& a, const Item& it, int
   return min(a.shared, seq_len(a, it.row0 + tok));
 }
 
-// One lane's share of the copies of K's 64 keys and V's 128 keys of a tile.
+// The copies of K's 64 keys and V's 128 keys of a tile, by a warp. Each lane holds
+// the page of one block of 16 of the tile's keys, asked for a tile ahead.
+struct Pages {
+  const int* table;  // the shared prefix's: sequence 0's
+  int page;
+};
+__device__ __forceinline__ Pages pages_of(const PromptArgs&) { return {nullptr, 0}; }
+__device__ __forceinline__ Pages pages_of(const DecodeAttnArgs& a) {
+  const int s = a.seqs[0];
+  return {a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width, -1};
+}
+__device__ __forceinline__ void look_up(const PromptArgs&, Pages&, int, int) {}
+__device__ __forceinline__ void look_up(const DecodeAttnArgs& a, Pages& pg, int tile, int lane) {
+  const int p = (tile * kTileKeys + (lane & 7) * 16) >> a.page_shift;
+  pg.page = p < a.width ? __ldg(pg.table + p) : -1;
+}
 template <int D>
-__device__ __forceinline__ void copy_k(const PromptArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar, int lane) {
+__device__ __forceinline__ void copy_k(const PromptArgs& a, const Item& it, const Pages&, int j, int rank, uint32_t dst,
+                                       uint32_t bar, int lane) {
   if (lane == 0) tma_load_5d_pair(dst, &a.k, 0, it.key_row + j * kTileKeys + 64 * rank, 0, it.kvh, 0, bar);
 }
 template <int D>
-__device__ __forceinline__ void copy_v(const PromptArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar, int lane) {
+__device__ __forceinline__ void copy_v(const PromptArgs& a, const Item& it, const Pages&, int j, int rank, uint32_t dst,
+                                       uint32_t bar, int lane) {
   if (lane == 0) tma_load_5d_pair(dst, &a.v, 0, it.key_row + j * kTileKeys, rank * (D / 128), it.kvh, 0, bar);
 }
-// Pages: boxes of up to 64 tokens of one page and one column block of 64 values.
-__device__ __forceinline__ int page_of(const DecodeAttnArgs& a, int key) {
-  const int s = a.seqs[0], p = key >> a.page_shift;
-  const int page = s >= 0 && s < a.slots && p < a.width ? __ldg(a.tables + (long long)s * a.width + p) : -1;
-  return page >= 0 && page < a.pages ? page : -1;  // -1 is out of the map's range: zeros
-}
+// Pages: boxes of up to 64 tokens of one page and one column block of 64 values;
+// a page out of range becomes -1, out of the map's range: zeros.
 template <int D>
-__device__ __forceinline__ void copy_k(const DecodeAttnArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar,
-                                       int lane) {
-  const int shift = min(a.page_shift, 6), key0 = (it.first + j) * kTileKeys + 64 * rank;
-  for (int x = lane; x < (64 >> shift) * (D / 64); x += 32) {
-    const int b = x / (D / 64), ch = x % (D / 64), key = key0 + (b << shift);
-    tma_load_5d_pair(dst + ch * 8192 + (b << shift) * 128, &a.kt, 0, key & (a.page_size - 1), ch, it.kvh, page_of(a, key), bar);
+__device__ __forceinline__ void copy_k(const DecodeAttnArgs& a, const Item& it, const Pages& pg, int j, int rank, uint32_t dst,
+                                       uint32_t bar, int lane) {
+  const int shift = min(a.page_shift, 6), key0 = (it.first + j) * kTileKeys;
+  const int page = (unsigned)pg.page < (unsigned)a.pages ? pg.page : -1;
+#pragma unroll
+  for (int x0 = 0; x0 < 4 * (D / 64); x0 += 32) {
+    const int x = x0 + lane, b = x / (D / 64), ch = x % (D / 64), key = 64 * rank + (b << shift);
+    const int pid = __shfl_sync(~0u, page, (key >> 4) & 7);
+    if (x < (64 >> shift) * (D / 64))
+      tma_load_5d_pair(dst + ch * 8192 + (b << shift) * 128, &a.kt, 0, (key0 + key) & (a.page_size - 1), ch, it.kvh, pid, bar);
   }
 }
 template <int D>
-__device__ __forceinline__ void copy_v(const DecodeAttnArgs& a, const Item& it, int j, int rank, uint32_t dst, uint32_t bar,
-                                       int lane) {
+__device__ __forceinline__ void copy_v(const DecodeAttnArgs& a, const Item& it, const Pages& pg, int j, int rank, uint32_t dst,
+                                       uint32_t bar, int lane) {
   const int shift = min(a.page_shift, 6), key0 = (it.first + j) * kTileKeys;
-  for (int x = lane; x < (128 >> shift) * (D / 128); x += 32) {
-    const int b = x / (D / 128), ch = x % (D / 128), key = key0 + (b << shift);
-    tma_load_5d_pair(dst + ch * 16384 + (b << shift) * 128, &a.vt, 0, key & (a.page_size - 1), rank * (D / 128) + ch, it.kvh,
-                     page_of(a, key), bar);
+  const int page = (unsigned)pg.page < (unsigned)a.pages ? pg.page : -1;
+#pragma unroll
+  for (int x0 = 0; x0 < 8 * (D / 128); x0 += 32) {
+    const int x = x0 + lane, b = x / (D / 128), ch = x % (D / 128), key = b << shift;
+    const int pid = __shfl_sync(~0u, page, (key >> 4) & 7);
+    if (x < (128 >> shift) * (D / 128))
+      tma_load_5d_pair(dst + ch * 16384 + (b << shift) * 128, &a.vt, 0, (key0 + key) & (a.page_size - 1), rank * (D / 128) + ch,
+                       it.kvh, pid, bar);
   }
 }
 
-// 32 columns of a row's result, from column `col` on: o is the accumulator's, inv = 1 / sum.
+// 32 columns of a row's result, from column `col` on: o is the accumulator's, inv = 1 / sum. All lanes call it.
 template <typename T, int D>
 __device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, int tok, int head, int col, float (&o)[32],
-                                          float inv, bool mend) {
-  if (mend) {  // values that were taken out of V: this row's own
+                                          float inv, bool live, bool mend, uint4* stage) {
+  if (mend && live) {  // values that were taken out of V: this row's own
     const T* v = reinterpret_cast<const T*>(a.vbase) + (long long)it.key_row * a.ldv + (long long)it.kvh * D + col;
     for (int key = it.hidden; key <= it.t0 + tok; key++) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(v + (long long)key * a.ldv);
@@ -264,20 +285,32 @@ __device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, i
       }
     }
   }
-  T* out = reinterpret_cast<T*>(a.out) + (long long)(it.row0 + tok) * a.ldo + (long long)head * D + col;
+  // a row's 64 bytes, to be stored by four lanes: 8 rows an instruction instead of 32
+  uint4 w[4];
 #pragma unroll
   for (int k = 0; k < 4; k++) {
-    uint4 w;
-    w.x = pack2<T>(o[8 * k] * inv, o[8 * k + 1] * inv);
-    w.y = pack2<T>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-    w.z = pack2<T>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-    w.w = pack2<T>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
-    *reinterpret_cast<uint4*>(out + 8 * k) = w;
+    w[k].x = pack2<T>(o[8 * k] * inv, o[8 * k + 1] * inv);
+    w[k].y = pack2<T>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
+    w[k].z = pack2<T>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
+    w[k].w = pack2<T>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
   }
+  T* out = live ? reinterpret_cast<T*>(a.out) + (long long)(it.row0 + tok) * a.ldo + (long long)head * D + col : nullptr;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 4; k++) stage[lane * 4 + (k ^ ((lane >> 1) & 3))] = w[k];  // 8 lanes' pieces in 8 different columns of banks
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const int r = k * 8 + (lane >> 2), p = lane & 3;
+    T* to = reinterpret_cast<T*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(out), r));
+    if (to) *reinterpret_cast<uint4*>(to + p * 8) = stage[r * 4 + (p ^ ((r >> 1) & 3))];
+  }
+  __syncwarp();
 }
 template <typename T, int D>
 __device__ __forceinline__ void store_row(const DecodeAttnArgs& a, const Item& it, int tok, int head, int col, float (&o)[32],
-                                          float, bool) {
+                                          float, bool live, bool, uint4*) {
+  if (!live) return;
   float* po = a.pre_o + (((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head) * D + col;
 #pragma unroll
   for (int k = 0; k < 8; k++)
@@ -298,6 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   __shared__ int abort_flag;
   __shared__ int fix[kFixes];  // round + 1 of the item whose V had values that were not finite taken out
   __shared__ float shared_max[2][2][128], shared_sum[2][128];
+  __shared__ uint4 stage[8][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_rank();
   const uint32_t base = s_addr(dyn) + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
@@ -347,8 +381,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     auto lead = [&](uint64_t* bar) { return peer_addr(s_addr(bar), 0); };
     int edges = 0, g = 0;
     bool ok = true;
+    Pages here = pages_of(a), ahead = here;
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
+      look_up(a, ahead, it.first, lane);
       if (!(ok = wait_warp(c, &bars.q_empty, (r & 1) ^ 1))) break;
       if (lane == 0) {
         expect_tx_at(lead(&bars.q_full), a.tokens * a.per_tile * D * 2);
@@ -358,17 +394,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       for (int j = 0; j < it.tiles; j++, g++) {
         const int st = g % ST;
         const uint32_t par = ((g / ST) & 1) ^ 1;
+        here = ahead;
+        look_up(a, ahead, it.first + j + 1, lane);
         if (!(ok = wait_warp(c, &bars.k_empty[st], par))) break;
         uint32_t bar = lead(&bars.k_full[st]);
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_k<D>(a, it, j, (int)rank, sk + st * G::kKV, bar, lane);
+        copy_k<D>(a, it, here, j, (int)rank, sk + st * G::kKV, bar, lane);
         if (!(ok = wait_warp(c, &bars.v_empty[st], par))) break;
         bar = (it.first + j + 1) * kTileKeys > it.hidden ? peer_addr(s_addr(&bars.v_edge[edges++ % kEdgeBars]), rank)
                                                          : lead(&bars.v_full[st]);
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_v<D>(a, it, j, (int)rank, sv + st * G::kKV, bar, lane);
+        copy_v<D>(a, it, here, j, (int)rank, sv + st * G::kKV, bar, lane);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -435,22 +473,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         const int from = max(it.hidden - key0, 0);
         constexpr int kPieces = D / 16;  // 16-byte pieces of a row in this CTA
         bool found = false;
-        for (int y = threadIdx.x - kEdgeWarp * 32; ok && y < (kTileKeys - from) * kPieces; y += 64) {
-          const int row = from + y / kPieces, p = y % kPieces;
-          const uint32_t at = sv + st * G::kKV + (p >> 3) * (kTileKeys * 128) + row * 128 + (p & 7) * 16;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (key0 + row < it.keys) {
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
-            const uint32_t m[4] = {not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w)};
-            if (!(m[0] | m[1] | m[2] | m[3])) continue;
-            found = true;
-            // 0xFFFF where bit 15 of the half is set
-            w.x &= ~((m[0] >> 15) * 0xFFFFu);
-            w.y &= ~((m[1] >> 15) * 0xFFFFu);
-            w.z &= ~((m[2] >> 15) * 0xFFFFu);
-            w.w &= ~((m[3] >> 15) * 0xFFFFu);
+        const int all = ok ? (kTileKeys - from) * kPieces : 0;
+        for (int y0 = threadIdx.x - kEdgeWarp * 32; y0 < all; y0 += 256) {
+          uint4 w[4];
+          uint32_t at[4];
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const int y = y0 + 64 * k, row = from + y / kPieces, p = y % kPieces;
+            at[k] = sv + st * G::kKV + (p >> 3) * (kTileKeys * 128) + row * 128 + (p & 7) * 16;
+            if (y < all)
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w) : "r"(at[k]));
           }
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const int y = y0 + 64 * k;
+            if (y >= all) continue;
+            if (key0 + from + y / kPieces < it.keys) {
+              const uint32_t m[4] = {not_finite<T>(w[k].x), not_finite<T>(w[k].y), not_finite<T>(w[k].z), not_finite<T>(w[k].w)};
+              if (!(m[0] | m[1] | m[2] | m[3])) continue;
+              found = true;
+              // 0xFFFF where bit 15 of the half is set
+              w[k].x &= ~((m[0] >> 15) * 0xFFFFu);
+              w[k].y &= ~((m[1] >> 15) * 0xFFFFu);
+              w[k].z &= ~((m[2] >> 15) * 0xFFFFu);
+              w[k].w &= ~((m[3] >> 15) * 0xFFFFu);
+            } else {
+              w[k] = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at[k]), "r"(w[k].x), "r"(w[k].y), "r"(w[k].z), "r"(w[k].w)
+                         : "memory");
+          }
         }
         if (found) {
           store_at(peer_addr(s_addr(&fix[r % kFixes]), 0), r + 1);
@@ -473,9 +525,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     const int my_tok = row / a.per_tile, my_head = row % a.per_tile;
     int g = 0;
     bool ok = true;
-    for (int r = 0, x; (x = nth(a, r)) >= 0; r++) {
-      const Item it = item_of(a, x);
-      const int tok = (int)rank * a.tokens + my_tok;
+    const int tok = (int)rank * a.tokens + my_tok;
+    int x = nth(a, 0);
+    Item it, next = {};
+    if (x >= 0) it = item_of(a, x);
+    for (int r = 0; x >= 0; r++, it = next) {
       const bool live = my_tok < a.tokens && it.row0 + tok < it.end_row;
       const int hi = live ? sees(a, it, tok) : INT_MAX;  // keys the row sees; a row that is no token's is not stored
       float ref = -INFINITY, l = 0.f;
@@ -561,6 +615,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         l += y0 + y1;
       }
       shared_sum[half][row] = l;
+      x = nth(a, r + 1);  // while the last product runs
+      if (x >= 0) next = item_of(a, x);
       bar_meet(1 + q4);
       l += shared_sum[half ^ 1][row];
       ok = wait_warp(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
@@ -573,13 +629,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         float o[32];
         tmem_ld32(tw + i, o);
         tmem_wait_ld_();
-        if (live && ok) store_row<T, D>(a, it, tok, it.head0 + my_head, i, o, inv, mend);
+        store_row<T, D>(a, it, tok, it.head0 + my_head, i, o, inv, live && ok, mend, stage[warp]);
         __syncwarp();
       }
       fence_before_sync();
       __syncwarp();
       // only where another item follows: see arrive_at
-      if (lane == 0 && ok && nth(a, r + 1) >= 0) arrive_at(peer_addr(s_addr(&bars.o_empty), 0));
+      if (lane == 0 && ok && x >= 0) arrive_at(peer_addr(s_addr(&bars.o_empty), 0));
       bar_meet(1 + q4);  // shared_sum may be written again
     }
   }
