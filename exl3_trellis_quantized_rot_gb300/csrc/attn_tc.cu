@@ -153,7 +153,7 @@ struct Item {
   int t0;          // position of the first token in its sequence (prompt)
   int first;       // first key tile
   int tiles;       // key tiles
-  int keys;        // keys of the sequence
+  int seen;        // keys from here on are seen by no row
   int hidden;      // first key that some row must not see
   int kvh, head0;  // K/V head; first query head
   int split;       // which share of the prefix
@@ -169,12 +169,12 @@ __device__ __forceinline__ Item item_of(const PromptArgs& a, int x) {
   const int r = i - a.before[lo], tile = a.count[lo] - 1 - r / (lo + 1), s = r % (lo + 1);
   Item it;
   it.key_row = a.begin[s];
-  it.keys = a.len[s];
   it.t0 = tile * 2 * a.tokens;
   it.row0 = it.key_row + it.t0;
-  it.end_row = it.key_row + it.keys;
+  it.end_row = it.key_row + a.len[s];
   it.first = 0;
-  it.tiles = (min(it.keys, it.t0 + 2 * a.tokens) - 1) / kTileKeys + 1;
+  it.seen = min(a.len[s], it.t0 + 2 * a.tokens);
+  it.tiles = (it.seen - 1) / kTileKeys + 1;
   it.hidden = it.t0 + 1;
   it.kvh = h / sub;
   it.head0 = it.kvh * a.group + h % sub * a.per_tile;
@@ -192,7 +192,7 @@ __device__ __forceinline__ Item item_of(const DecodeAttnArgs& a, int x) {
   it.key_row = it.t0 = 0;
   it.first = (int)((long long)all * it.split / a.pre_splits);
   it.tiles = (int)((long long)all * (it.split + 1) / a.pre_splits) - it.first;
-  it.keys = it.hidden = a.shared;
+  it.seen = it.hidden = a.shared;
   it.kvh = h / sub;
   it.head0 = it.kvh * a.group + h % sub * a.per_tile;
   return it;
@@ -271,7 +271,7 @@ __device__ __forceinline__ void copy_v(const DecodeAttnArgs& a, const Item& it, 
 
 // 32 columns of a row's result, from column `col` on: o is the accumulator's, inv = 1 / sum. All lanes call it.
 template <typename T, int D>
-__device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, int tok, int head, int col, float (&o)[32],
+__device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, int tok, int head, int col, float* o,
                                           float inv, bool live, bool mend, uint4* stage) {
   if (mend && live) {  // values that were taken out of V: this row's own
     const T* v = reinterpret_cast<const T*>(a.vbase) + (long long)it.key_row * a.ldv + (long long)it.kvh * D + col;
@@ -308,7 +308,7 @@ __device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, i
   __syncwarp();
 }
 template <typename T, int D>
-__device__ __forceinline__ void store_row(const DecodeAttnArgs& a, const Item& it, int tok, int head, int col, float (&o)[32],
+__device__ __forceinline__ void store_row(const DecodeAttnArgs& a, const Item& it, int tok, int head, int col, float* o,
                                           float, bool live, bool, uint4*) {
   if (!live) return;
   float* po = a.pre_o + (((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head) * D + col;
@@ -434,7 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         return true;
       };
       for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
-        const int n = item_of(a, x).tiles;
+        const Item it = item_of(a, x);
+        const int n = it.tiles, last_steps = (min(it.seen - (it.first + n - 1) * kTileKeys, kTileKeys) + 15) >> 4;
         if (!(ok = wait_warp(c, &bars.q_full, r & 1))) break;
         int ahead = 0;  // scores of the item's tiles issued: up to SB - 1 more than the products with V
         for (int j = 0; j < n; j++, g++) {
@@ -447,8 +448,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
           const uint64_t vd = operand(sv + st * G::kKV, vmaj);
           const uint32_t p = tm + D + (g % SB) * 128;
           if (elected()) {
+            const int steps = j + 1 < n ? kTileKeys / 16 : last_steps;
 #pragma unroll
-            for (int k = 0; k < kTileKeys / 16; k++) mma2_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
+            for (int k = 0; k < kTileKeys / 16; k++)
+              if (k < steps) mma2_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
             commit2(&bars.v_empty[st]);
             commit2(&bars.pv_done[g % SB]);
           }
@@ -473,7 +476,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         const int from = max(it.hidden - key0, 0);
         constexpr int kPieces = D / 16;  // 16-byte pieces of a row in this CTA
         bool found = false;
-        const int all = ok ? (kTileKeys - from) * kPieces : 0;
+        const int till = min((it.seen - key0 + 15) & ~15, kTileKeys);  // the product takes 16 keys at a time, and no more
+        const int all = ok ? (till - from) * kPieces : 0;
         for (int y0 = threadIdx.x - kEdgeWarp * 32; y0 < all; y0 += 256) {
           uint4 w[4];
           uint32_t at[4];
@@ -488,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
           for (int k = 0; k < 4; k++) {
             const int y = y0 + 64 * k;
             if (y >= all) continue;
-            if (key0 + from + y / kPieces < it.keys) {
+            if (key0 + from + y / kPieces < it.seen) {
               const uint32_t m[4] = {not_finite<T>(w[k].x), not_finite<T>(w[k].y), not_finite<T>(w[k].z), not_finite<T>(w[k].w)};
               if (!(m[0] | m[1] | m[2] | m[3])) continue;
               found = true;
@@ -624,18 +628,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       const float inv = 1.f / l;
       const bool mend = *(volatile int*)&fix[r % kFixes] == r + 1;
       if (live && ok && half == 0) store_sum(a, it, tok, it.head0 + my_head, ref, l);
-#pragma unroll 1
-      for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
-        float o[32];
-        tmem_ld32(tw + i, o);
-        tmem_wait_ld_();
-        store_row<T, D>(a, it, tok, it.head0 + my_head, i, o, inv, live && ok, mend, stage[warp]);
-        __syncwarp();
-      }
+      float o[D / 2];
+#pragma unroll
+      for (int i = 0; i < D / 2; i += 32) tmem_ld32(tw + half * (D / 2) + i, o + i);
+      tmem_wait_ld_();
       fence_before_sync();
       __syncwarp();
       // only where another item follows: see arrive_at
       if (lane == 0 && ok && x >= 0) arrive_at(peer_addr(s_addr(&bars.o_empty), 0));
+#pragma unroll
+      for (int i = 0; i < D / 2; i += 32)
+        store_row<T, D>(a, it, tok, it.head0 + my_head, half * (D / 2) + i, o + i, inv, live && ok, mend, stage[warp]);
+      __syncwarp();
       bar_meet(1 + q4);  // shared_sum may be written again
     }
   }
