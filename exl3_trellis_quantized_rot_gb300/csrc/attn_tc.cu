@@ -377,36 +377,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
 
   if (warp == kCopyWarp) {
-    // ---- copies: this CTA's rows of Q, its 64 keys of K, its dim/2 columns of V
+    // ---- copies: this CTA's rows of Q, its 64 keys of K, its dim/2 columns of V,
+    // in the order in which the MMAs free the memory for them: K runs SB - 1 tiles
+    // ahead of V, and an item's first K ahead of its Q
     auto lead = [&](uint64_t* bar) { return peer_addr(s_addr(bar), 0); };
-    int edges = 0, g = 0;
+    int edges = 0, gk = 0, gv = 0;
     bool ok = true;
-    Pages here = pages_of(a), ahead = here;
+    Pages pk = pages_of(a), pv = pk;  // of the next tile of K, of V
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
-      look_up(a, ahead, it.first, lane);
-      if (!(ok = wait_warp(c, &bars.q_empty, (r & 1) ^ 1))) break;
+      auto send_k = [&](int j) {
+        const int st = gk % ST;
+        const Pages here = pk;
+        look_up(a, pk, it.first + j + 1, lane);
+        ok = ok && wait_warp(c, &bars.k_empty[st], ((gk / ST) & 1) ^ 1);
+        if (!ok) return;
+        const uint32_t bar = lead(&bars.k_full[st]);
+        if (lane == 0) expect_tx_at(bar, G::kKV);
+        __syncwarp();
+        copy_k<D>(a, it, here, j, (int)rank, sk + st * G::kKV, bar, lane);
+        gk++;
+      };
+      auto send_v = [&](int j) {
+        const int st = gv % ST;
+        const Pages here = pv;
+        look_up(a, pv, it.first + j + 1, lane);
+        ok = ok && wait_warp(c, &bars.v_empty[st], ((gv / ST) & 1) ^ 1);
+        if (!ok) return;
+        const bool edge = (it.first + j + 1) * kTileKeys > it.hidden;
+        const uint32_t bar = edge ? peer_addr(s_addr(&bars.v_edge[edges % kEdgeBars]), rank) : lead(&bars.v_full[st]);
+        edges += edge;
+        if (lane == 0) expect_tx_at(bar, G::kKV);
+        __syncwarp();
+        copy_v<D>(a, it, here, j, (int)rank, sv + st * G::kKV, bar, lane);
+        gv++;
+      };
+      look_up(a, pk, it.first, lane);
+      pv = pk;
+      for (int j = 0; j < SB - 1 && j < it.tiles; j++) send_k(j);
+      ok = ok && wait_warp(c, &bars.q_empty, (r & 1) ^ 1);
+      if (!ok) break;
       if (lane == 0) {
         expect_tx_at(lead(&bars.q_full), a.tokens * a.per_tile * D * 2);
         for (int ch = 0; ch < D / 64; ch++)
           tma_load_5d_pair(sq + ch * 16384, &a.qmap, 0, it.head0, it.row0 + (int)rank * a.tokens, ch, 0, lead(&bars.q_full));
       }
-      for (int j = 0; j < it.tiles; j++, g++) {
-        const int st = g % ST;
-        const uint32_t par = ((g / ST) & 1) ^ 1;
-        here = ahead;
-        look_up(a, ahead, it.first + j + 1, lane);
-        if (!(ok = wait_warp(c, &bars.k_empty[st], par))) break;
-        uint32_t bar = lead(&bars.k_full[st]);
-        if (lane == 0) expect_tx_at(bar, G::kKV);
-        __syncwarp();
-        copy_k<D>(a, it, here, j, (int)rank, sk + st * G::kKV, bar, lane);
-        if (!(ok = wait_warp(c, &bars.v_empty[st], par))) break;
-        bar = (it.first + j + 1) * kTileKeys > it.hidden ? peer_addr(s_addr(&bars.v_edge[edges++ % kEdgeBars]), rank)
-                                                         : lead(&bars.v_full[st]);
-        if (lane == 0) expect_tx_at(bar, G::kKV);
-        __syncwarp();
-        copy_v<D>(a, it, here, j, (int)rank, sv + st * G::kKV, bar, lane);
+      __syncwarp();
+      for (int j = 0; ok && j < it.tiles; j++) {
+        if (j + SB - 1 < it.tiles) send_k(j + SB - 1);
+        send_v(j);
       }
     }
   } else if (warp == kMmaWarp) {
