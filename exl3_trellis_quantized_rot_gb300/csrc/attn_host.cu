@@ -461,6 +461,8 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   if (batch * a.group > 32 && shared >= 256) {
     a.per_tile = heads_per_tile(a.group);
     a.tokens = 128 / a.per_tile;
+    const int most = 2 * a.tokens, tiles = (batch + most - 1) / most;
+    a.tokens = (batch + 2 * tiles - 1) / (2 * tiles);  // the sequences spread evenly over the tiles' CTAs
     a.pre_splits = prefix_splits(batch, h->heads_q, h->heads_kv, shared);
     const int mt = (batch + 2 * a.tokens - 1) / (2 * a.tokens), box = c->page_size < 64 ? c->page_size : 64;
     a.items = a.heads_kv * (a.group / a.per_tile) * mt * a.pre_splits;

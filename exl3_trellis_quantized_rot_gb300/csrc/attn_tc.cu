@@ -214,20 +214,34 @@ __device__ __forceinline__ int sees(const DecodeAttnArgs& a, const Item& it, int
 }
 
 // The copies of K's 64 keys and V's 128 keys of a tile, by a warp. Each lane holds
-// the page of one block of 16 of the tile's keys, asked for a tile ahead.
+// the page of one block of 16 keys: four tiles' blocks at a time, and the next
+// four's are on their way.
 struct Pages {
   const int* table;  // the shared prefix's: sequence 0's
-  int page;
+  int tile;          // first of the four
+  int page, next;
 };
-__device__ __forceinline__ Pages pages_of(const PromptArgs&) { return {nullptr, 0}; }
+__device__ __forceinline__ void look_up(const PromptArgs&, Pages&, int, int) {}
+__device__ __forceinline__ int page_ahead(const DecodeAttnArgs& a, const Pages& pg, int tile, int lane) {
+  const int p = (tile * kTileKeys + lane * 16) >> a.page_shift;
+  return p < a.width ? __ldg(pg.table + p) : -1;
+}
+// Makes the window hold `tile`: called for each tile in order, and at an item's first.
+__device__ __forceinline__ void look_up(const DecodeAttnArgs& a, Pages& pg, int tile, int lane) {
+  if (tile == pg.tile + 4) {
+    pg.page = pg.next;
+  } else if (tile < pg.tile || tile > pg.tile + 4) {
+    pg.page = page_ahead(a, pg, tile, lane);
+  } else {
+    return;
+  }
+  pg.tile = tile;
+  pg.next = page_ahead(a, pg, tile + 4, lane);
+}
+__device__ __forceinline__ Pages pages_of(const PromptArgs&) { return {}; }
 __device__ __forceinline__ Pages pages_of(const DecodeAttnArgs& a) {
   const int s = a.seqs[0];
-  return {a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width, -1};
-}
-__device__ __forceinline__ void look_up(const PromptArgs&, Pages&, int, int) {}
-__device__ __forceinline__ void look_up(const DecodeAttnArgs& a, Pages& pg, int tile, int lane) {
-  const int p = (tile * kTileKeys + (lane & 7) * 16) >> a.page_shift;
-  pg.page = p < a.width ? __ldg(pg.table + p) : -1;
+  return {a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width, INT_MIN / 2, -1, -1};
 }
 template <int D>
 __device__ __forceinline__ void copy_k(const PromptArgs& a, const Item& it, const Pages&, int j, int rank, uint32_t dst,
@@ -249,7 +263,7 @@ __device__ __forceinline__ void copy_k(const DecodeAttnArgs& a, const Item& it, 
 #pragma unroll
   for (int x0 = 0; x0 < 4 * (D / 64); x0 += 32) {
     const int x = x0 + lane, b = x / (D / 64), ch = x % (D / 64), key = 64 * rank + (b << shift);
-    const int pid = __shfl_sync(~0u, page, (key >> 4) & 7);
+    const int pid = __shfl_sync(~0u, page, (it.first + j - pg.tile) * 8 + ((key >> 4) & 7));
     if (x < (64 >> shift) * (D / 64))
       tma_load_5d_pair(dst + ch * 8192 + (b << shift) * 128, &a.kt, 0, (key0 + key) & (a.page_size - 1), ch, it.kvh, pid, bar);
   }
@@ -262,7 +276,7 @@ __device__ __forceinline__ void copy_v(const DecodeAttnArgs& a, const Item& it, 
 #pragma unroll
   for (int x0 = 0; x0 < 8 * (D / 128); x0 += 32) {
     const int x = x0 + lane, b = x / (D / 128), ch = x % (D / 128), key = b << shift;
-    const int pid = __shfl_sync(~0u, page, (key >> 4) & 7);
+    const int pid = __shfl_sync(~0u, page, (it.first + j - pg.tile) * 8 + ((key >> 4) & 7));
     if (x < (128 >> shift) * (D / 128))
       tma_load_5d_pair(dst + ch * 16384 + (b << shift) * 128, &a.vt, 0, (key0 + key) & (a.page_size - 1), rank * (D / 128) + ch,
                        it.kvh, pid, bar);
@@ -383,25 +397,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     auto lead = [&](uint64_t* bar) { return peer_addr(s_addr(bar), 0); };
     int edges = 0, gk = 0, gv = 0;
     bool ok = true;
-    Pages pk = pages_of(a), pv = pk;  // of the next tile of K, of V
+    Pages pk = pages_of(a), pv = pk;
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
       auto send_k = [&](int j) {
         const int st = gk % ST;
-        const Pages here = pk;
-        look_up(a, pk, it.first + j + 1, lane);
+        look_up(a, pk, it.first + j, lane);
         ok = ok && wait_warp(c, &bars.k_empty[st], ((gk / ST) & 1) ^ 1);
         if (!ok) return;
         const uint32_t bar = lead(&bars.k_full[st]);
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_k<D>(a, it, here, j, (int)rank, sk + st * G::kKV, bar, lane);
+        copy_k<D>(a, it, pk, j, (int)rank, sk + st * G::kKV, bar, lane);
         gk++;
       };
       auto send_v = [&](int j) {
         const int st = gv % ST;
-        const Pages here = pv;
-        look_up(a, pv, it.first + j + 1, lane);
+        look_up(a, pv, it.first + j, lane);
         ok = ok && wait_warp(c, &bars.v_empty[st], ((gv / ST) & 1) ^ 1);
         if (!ok) return;
         const bool edge = (it.first + j + 1) * kTileKeys > it.hidden;
@@ -409,11 +421,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         edges += edge;
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_v<D>(a, it, here, j, (int)rank, sv + st * G::kKV, bar, lane);
+        copy_v<D>(a, it, pv, j, (int)rank, sv + st * G::kKV, bar, lane);
         gv++;
       };
-      look_up(a, pk, it.first, lane);
-      pv = pk;
       for (int j = 0; j < SB - 1 && j < it.tiles; j++) send_k(j);
       ok = ok && wait_warp(c, &bars.q_empty, (r & 1) ^ 1);
       if (!ok) break;
@@ -554,6 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     if (x >= 0) it = item_of(a, x);
     for (int r = 0; x >= 0; r++, it = next) {
       const bool live = my_tok < a.tokens && it.row0 + tok < it.end_row;
+      const bool some = __any_sync(~0u, live);  // the same in both warps: where no row is a token's, there is nothing to compute
       const int hi = live ? sees(a, it, tok) : INT_MAX;  // keys the row sees; a row that is no token's is not stored
       float ref = -INFINITY, l = 0.f;
       float s[64];
@@ -564,6 +575,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       };
       for (int j = 0; j < it.tiles; j++, g++) {
         ok = wait_warp(c, &bars.s_full[g % SB], (g / SB) & 1) && ok;
+        if (!some) {
+          if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.p_full[g % SB]), 0));
+          continue;
+        }
         fence_after_sync();
         scores_of(g);
         tmem_wait_ld_();

@@ -3,9 +3,10 @@
 //   m' = max(m, max_j s_j),  p_j = 2^(s_j - m'),  l' = l 2^(m - m') + sum_j p_j,
 //   o' = o 2^(m - m') + sum_j p_j v_j,            s_j = scale log2(e) q . k_j,
 // one pass over the keys; the row's result is o / l. A warp owns its rows, its
-// slices and its own ring of shared-memory stages, so warps never wait for
-// one another. Partial results (o, m, l) of several warps are joined by
-// decode_join_kernel in slot order.
+// slices and its own ring of shared-memory stages, so the four of a CTA never
+// wait for one another; a fifth warp asks for their slices, one lane a ring, and
+// runs on into the next segment while the last one's result is stored. Partial
+// results (o, m, l) of several warps are joined by decode_join_kernel in slot order.
 //
 // A slice is 16 KB of K and V of one K/V head (16 keys of 256, 32 of 128),
 // fetched by two to four tensor copies of 16 tokens each with the 128-byte
@@ -20,8 +21,10 @@
 namespace tfx {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;  // that compute; one more asks for their slices
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kStages = 3;
+constexpr int kFewest = 2;  // slices a warp takes at least
 
 template <int D>
 struct Slice {
@@ -80,6 +83,8 @@ struct Rows {
       q[i][2] = r0 ? *reinterpret_cast<const uint32_t*>(r0 + c + 8) : 0u;
       q[i][3] = r1 ? *reinterpret_cast<const uint32_t*>(r1 + c + 8) : 0u;
     }
+  }
+  __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int i = 0; i < D / 8; i++)
 #pragma unroll
@@ -89,69 +94,126 @@ struct Rows {
   }
 };
 
-// The ring of one warp: stages of one slice each, refilled by lane 0.
+// The ring of one warp: stages of one slice each.
 struct Ring {
   uint8_t* buf;
-  uint64_t* full;
-  int it = 0;  // slices consumed so far: stage it % kStages, phase it / kStages
+  uint64_t *full, *empty;
+  int it = 0;  // slices so far: stage it % kStages, phase it / kStages
 };
 
-// Where the tokens are: token t of a paged sequence is in page table[t / page_size];
-// without a table the tokens are rows base, base + 1, ... of one long "page".
-struct Keys {
-  const CUtensorMap *k, *v;
+// A run of slices of one group: 16 rows of one K/V head against keys of one sequence.
+struct Segment {
+  bool prefix;
+  int s0, s1;    // slices, from the sequence's first token
+  int head;      // K/V head
+  int seq;       // of the batch; -1: the shared prefix, through the first one's table
+  int row0;      // first row of the tile: of the batch's rows (prefix) or of the group's heads
+  int rows;
+  long long group;  // number of the group in its list
   const int* table;
-  int page_shift, pages, width;
-  int base, head;
 };
 
+struct Walk {
+  long long pre_total, total;
+  int own, sp, tiles, ptiles;
+};
 template <int D>
-__device__ __forceinline__ void fetch(const Keys& ks, Ring& rg, int stage, int token, int entry) {
-  uint8_t* dst = rg.buf + stage * Slice<D>::kStage;
-  uint64_t* bar = rg.full + stage;
-  mbar_expect_tx(bar, Slice<D>::kStage);
-#pragma unroll
-  for (int b = 0; b < Slice<D>::kKeys / 16; b++) {
-    int page = 0, at = ks.base + token + 16 * b;
-    if (ks.table) {
-      const int p = (token + 16 * b) >> ks.page_shift;
-      // a page can end inside a slice of 32 keys: its second half has an entry of its own
-      page = b == 0 ? entry : p < ks.width ? __ldg(ks.table + p) : -1;
-      page = page >= 0 && page < ks.pages ? page : -1;  // -1 is out of the map's range: zeros
-      at = (token + 16 * b) & ((1 << ks.page_shift) - 1);
+__device__ __forceinline__ Walk walk_of(const DecodeAttnArgs& a, int own) {
+  constexpr int KS = Slice<D>::kKeys;
+  Walk w;
+  w.own = own;
+  w.sp = a.pre_splits ? 0 : (a.shared + KS - 1) / KS;
+  w.tiles = (a.group + 15) / 16;
+  w.ptiles = (a.batch * a.group + 15) / 16;
+  w.pre_total = (long long)a.heads_kv * w.ptiles * w.sp;
+  w.total = w.pre_total + (long long)a.heads_kv * w.tiles * own;
+  return w;
+}
+
+// The segment that begins with slice x of those before `end`.
+template <int D>
+__device__ __forceinline__ Segment segment_at(const DecodeAttnArgs& a, const Walk& w, const int* starts, long long x,
+                                              long long end) {
+  Segment g;
+  g.prefix = x < w.pre_total;
+  if (g.prefix) {
+    const int grp = (int)(x / w.sp), s = a.seqs[0];
+    g.group = grp;
+    g.s0 = (int)(x % w.sp);
+    g.s1 = (int)min((long long)w.sp, g.s0 + (end - x));
+    g.head = grp / w.ptiles;
+    g.seq = -1;
+    g.row0 = grp % w.ptiles * 16;
+    g.rows = min(16, a.batch * a.group - g.row0);
+    g.table = a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width;
+  } else {
+    const long long y = x - w.pre_total;
+    const int hr = (int)(y / w.own), z = (int)(y % w.own);
+    int lo = 0, hi = a.batch - 1;  // the sequence that slice z belongs to
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid + 1] > z) hi = mid; else lo = mid + 1;
     }
-    tma_load_5d(dst + b * Slice<D>::kBlock, ks.k, 0, at, 0, ks.head, page, bar);
-    tma_load_5d(dst + Slice<D>::kHalf + b * Slice<D>::kBlock, ks.v, 0, at, 0, ks.head, page, bar);
+    const int off = a.shared / Slice<D>::kKeys;
+    g.seq = lo;
+    g.group = (long long)hr * a.batch + lo;
+    g.s0 = z - starts[lo] + off;
+    g.s1 = (int)min((long long)(starts[lo + 1] - starts[lo] + off), g.s0 + (end - x));
+    g.head = hr / w.tiles;
+    g.row0 = hr % w.tiles * 16;
+    g.rows = min(16, a.group - g.row0);
+    g.table = a.tables + (long long)a.seqs[lo] * a.width;  // it has slices, so its slot is in range
   }
+  return g;
+}
+
+// One lane: the slices [x, end) into a ring, in order.
+template <int D>
+__device__ __forceinline__ bool feed(const DecodeAttnArgs& a, const Walk& w, const int* starts, Ring& rg, long long x,
+                                     long long end) {
+  constexpr int KS = Slice<D>::kKeys;
+  auto page_at = [&](const int* table, int token) {
+    const int p = token >> a.page_shift;
+    return p < a.width ? __ldg(table + p) : -1;
+  };
+  while (x < end) {
+    const Segment g = segment_at<D>(a, w, starts, x, end);
+    int next = page_at(g.table, g.s0 * KS);
+    for (int s = g.s0; s < g.s1; s++) {
+      const int page0 = next, st = rg.it % kStages;
+      if (s + 1 < g.s1) next = page_at(g.table, (s + 1) * KS);
+      if (!mbar_wait_bounded(rg.empty + st, ((rg.it / kStages) & 1) ^ 1, a.spin)) return false;
+      uint8_t* dst = rg.buf + st * Slice<D>::kStage;
+      uint64_t* bar = rg.full + st;
+      mbar_expect_tx(bar, Slice<D>::kStage);
+#pragma unroll
+      for (int b = 0; b < KS / 16; b++) {
+        const int token = s * KS + 16 * b;
+        // a page of 16 ends inside a slice of 32 keys: its second half has an entry of its own
+        const int p = b == 0 ? page0 : page_at(g.table, token);
+        const int page = (unsigned)p < (unsigned)a.pages ? p : -1;  // -1 is out of the map's range: zeros
+        const int at = token & (a.page_size - 1);
+        tma_load_5d(dst + b * Slice<D>::kBlock, &a.k, 0, at, 0, g.head, page, bar);
+        tma_load_5d(dst + Slice<D>::kHalf + b * Slice<D>::kBlock, &a.v, 0, at, 0, g.head, page, bar);
+      }
+      rg.it++;
+    }
+    x += g.s1 - g.s0;
+  }
+  return true;
 }
 
 // The rows against slices [s0, s1) of the keys lo <= key < hi. False: a wait gave up.
 template <typename T, int D>
-__device__ __forceinline__ bool attend(Rows<T, D>& R, const Keys& ks, Ring& rg, int s0, int s1, int lo, float scale,
-                                       int lane, long long spin) {
-  constexpr int KS = Slice<D>::kKeys;
-  const int g = lane >> 2, t = lane & 3, mi = lane >> 3, mr = lane & 7;
+__device__ __forceinline__ bool attend(Rows<T, D>& R, Ring& rg, int s0, int s1, int lo, float scale, int lane,
+                                       long long spin) {
+  constexpr int KS = Slice<D>::kKeys, NB = KS / 16;
+  const int t = lane & 3, mi = lane >> 3, mr = lane & 7;
   int hmin = min(R.hi[0], R.hi[1]), hmax = max(R.hi[0], R.hi[1]);
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
     hmin = min(hmin, __shfl_xor_sync(~0u, hmin, d));
     hmax = max(hmax, __shfl_xor_sync(~0u, hmax, d));
-  }
-  // page-table entries of the slices ahead, one per lane
-  int tb = -1, held = 0;
-  auto entry_of = [&](int token) -> int {
-    if (!ks.table) return 0;
-    const int p = token >> ks.page_shift;
-    if (tb < 0 || p >= tb + 32) {
-      tb = p;
-      held = p + lane < ks.width ? __ldg(ks.table + p + lane) : -1;
-    }
-    return __shfl_sync(~0u, held, p - tb);
-  };
-  const int it0 = rg.it;
-  for (int i = 0; i < kStages && s0 + i < s1; i++) {
-    const int e = entry_of((s0 + i) * KS);
-    if (lane == 0) fetch<D>(ks, rg, (it0 + i) % kStages, (s0 + i) * KS, e);
   }
   for (int s = s0; s < s1; s++) {
     const int st = rg.it % kStages;
@@ -167,9 +229,10 @@ __device__ __forceinline__ bool attend(Rows<T, D>& R, const Keys& ks, Ring& rg, 
           for (int c = lane; c < D / 8; c += 32)
             *reinterpret_cast<uint4*>(vb + (r >> 4) * Slice<D>::kBlock + (c >> 3) * 2048 + (r & 15) * 128 +
                                       (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+      fence_async_smem();  // ordinary stores to memory that a later copy writes
       __syncwarp();
     }
-    // S = Q K^T; two chains per tile of 8 keys
+    // S = Q K^T; two chains per tile of 8 keys, each step's K a step ahead
     float sc[KS / 8][4];
     {
       float s2[KS / 8][4];
@@ -178,20 +241,22 @@ __device__ __forceinline__ bool attend(Rows<T, D>& R, const Keys& ks, Ring& rg, 
 #pragma unroll
         for (int c = 0; c < 4; c++) sc[j][c] = s2[j][c] = 0.f;
       const int key = (mi >> 1) * 8 + mr;
-#pragma unroll
-      for (int i = 0; i < D / 16; i++) {
+      uint32_t f[2][NB][4];
+      auto load = [&](int i) {
         const int c = i * 2 + (mi & 1);  // 16-byte column of 8 values
 #pragma unroll
-        for (int b = 0; b < KS / 16; b++) {
-          uint32_t f[4];
-          ldsm4(f, s_addr(kb) + b * Slice<D>::kBlock + (c >> 3) * 2048 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
-          if (i & 1) {
-            mma<T>(s2[2 * b], R.q[i], f[0], f[1]);
-            mma<T>(s2[2 * b + 1], R.q[i], f[2], f[3]);
-          } else {
-            mma<T>(sc[2 * b], R.q[i], f[0], f[1]);
-            mma<T>(sc[2 * b + 1], R.q[i], f[2], f[3]);
-          }
+        for (int b = 0; b < NB; b++)
+          ldsm4(f[i & 1][b], s_addr(kb) + b * Slice<D>::kBlock + (c >> 3) * 2048 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+      };
+      load(0);
+#pragma unroll
+      for (int i = 0; i < D / 16; i++) {
+        if (i + 1 < D / 16) load(i + 1);
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+          const uint32_t(&x)[4] = f[i & 1][b];
+          mma<T>(i & 1 ? s2[2 * b] : sc[2 * b], R.q[i], x[0], x[1]);
+          mma<T>(i & 1 ? s2[2 * b + 1] : sc[2 * b + 1], R.q[i], x[2], x[3]);
         }
       }
 #pragma unroll
@@ -231,9 +296,9 @@ __device__ __forceinline__ bool attend(Rows<T, D>& R, const Keys& ks, Ring& rg, 
 #pragma unroll
         for (int c = 0; c < 4; c++) R.o[i][c] *= keep[c >> 1];
     }
-    uint32_t p[KS / 16][4];
+    uint32_t p[NB][4];
 #pragma unroll
-    for (int b = 0; b < KS / 16; b++)
+    for (int b = 0; b < NB; b++)
 #pragma unroll
       for (int j = 0; j < 2; j++) {
         float e[4];
@@ -247,22 +312,28 @@ __device__ __forceinline__ bool attend(Rows<T, D>& R, const Keys& ks, Ring& rg, 
         p[b][2 * j + 1] = pack2<T>(e[2], e[3]);
       }
     const int vkey = (mi & 1) * 8 + mr;
+    {
+      uint32_t f[2][NB][4];
+      auto load = [&](int i) {
+        const int c = i * 2 + (mi >> 1);
 #pragma unroll
-    for (int b = 0; b < KS / 16; b++)
+        for (int b = 0; b < NB; b++)
+          ldsm4t(f[i & 1][b],
+                 s_addr(vb) + b * Slice<D>::kBlock + (c >> 3) * 2048 + vkey * 128 + (((c & 7) ^ (vkey & 7)) << 4));
+      };
+      load(0);
 #pragma unroll
       for (int i = 0; i < D / 16; i++) {
-        const int c = i * 2 + (mi >> 1);
-        uint32_t f[4];
-        ldsm4t(f, s_addr(vb) + b * Slice<D>::kBlock + (c >> 3) * 2048 + vkey * 128 + (((c & 7) ^ (vkey & 7)) << 4));
-        mma<T>(R.o[2 * i], p[b], f[0], f[1]);
-        mma<T>(R.o[2 * i + 1], p[b], f[2], f[3]);
+        if (i + 1 < D / 16) load(i + 1);
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+          mma<T>(R.o[2 * i], p[b], f[i & 1][b][0], f[i & 1][b][1]);
+          mma<T>(R.o[2 * i + 1], p[b], f[i & 1][b][2], f[i & 1][b][3]);
+        }
       }
-    fence_async_smem();  // zeroed rows are ordinary stores to memory that the next copy writes
-    __syncwarp();
-    if (s + kStages < s1) {
-      const int e = entry_of((s + kStages) * KS);
-      if (lane == 0) fetch<D>(ks, rg, st, (s + kStages) * KS, e);
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(rg.empty + st);
     rg.it++;
   }
 #pragma unroll
@@ -273,150 +344,126 @@ __device__ __forceinline__ bool attend(Rows<T, D>& R, const Keys& ks, Ring& rg, 
   return true;
 }
 
-// Shared memory of this warp and its barriers; every thread of the CTA calls it.
-template <int D>
-__device__ __forceinline__ Ring make_ring(uint8_t* dyn, uint64_t (*full)[kStages], int warp, int lane) {
-  uint8_t* base = dyn + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
-  if (lane == 0) {
-    for (int i = 0; i < kStages; i++) mbar_init(&full[warp][i], 1);
-    fence_mbar_init();
-  }
-  __syncthreads();
-  Ring r;
-  r.buf = base + warp * kStages * Slice<D>::kStage;
-  r.full = full[warp];
-  return r;
-}
-
 // After a wait that gave up: the error word, and time for the copies in flight to land.
-__device__ __forceinline__ void gave_up(int* err, int lane) {
-  if (lane == 0) atomicExch(err, 1);
+__device__ __forceinline__ void gave_up(int* err) {
+  atomicExch(err, 1);
   const long long t0 = clock64();
-  while (clock64() - t0 < 2000000) __nanosleep(1000);
+  while (clock64() - t0 < 2000000) {
+  }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_warp_kernel(const __grid_constant__ DecodeAttnArgs a) {
+__global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_constant__ DecodeAttnArgs a) {
   constexpr int KS = Slice<D>::kKeys;
   extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t full[kWarps][kStages];
+  __shared__ uint64_t full[kWarps][kStages], empty[kWarps][kStages];
   __shared__ int starts[TFX_ATTN_MAX_BATCH + 1];
   __shared__ int wsum[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * kStages; i++) {
+      mbar_init(&full[0][0] + i, 1);
+      mbar_init(&empty[0][0] + i, 1);
+    }
+    fence_mbar_init();
+    starts[0] = 0;
+  }
   // after the tensor-core kernel, this one starts where that leaves room: they
   // share no memory that is written, and that one began after all that came before
   if (!a.pre_splits) griddep_wait();
-  Ring rg = make_ring<D>(dyn, full, warp, lane);
   // own slices before each sequence
   int carry = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kWarps * 32) {
     const int i = b0 + threadIdx.x;
-    const int len = i < a.batch ? seq_len(a, i) : 0;
-    const int mine = len > a.shared ? (len + KS - 1) / KS - a.shared / KS : 0;
-    int x = mine;
+    const int len = warp < kWarps && i < a.batch ? seq_len(a, i) : 0;
+    int x = len > a.shared ? (len + KS - 1) / KS - a.shared / KS : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(~0u, x, d);
       if (lane >= d) x += y;
     }
-    if (lane == 31) wsum[warp] = x;
+    if (lane == 31 && warp < kWarps) wsum[warp] = x;
     __syncthreads();
     int before = carry, all = carry;
     for (int w = 0; w < kWarps; w++) {
       if (w < warp) before += wsum[w];
       all += wsum[w];
     }
-    if (i < a.batch) starts[i + 1] = before + x;
+    if (warp < kWarps && i < a.batch) starts[i + 1] = before + x;
     carry = all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) starts[0] = 0;
-  __syncthreads();
-  const int own = starts[a.batch];
-  const int tiles = (a.group + 15) / 16, ptiles = (a.batch * a.group + 15) / 16;
-  const int sp = a.pre_splits ? 0 : (a.shared + KS - 1) / KS;
-  const long long pre_total = (long long)a.heads_kv * ptiles * sp;
-  const long long total = pre_total + (long long)a.heads_kv * tiles * own;
-  const long long per = max((total + a.warps - 1) / a.warps, 4LL);
+  const Walk w = walk_of<D>(a, carry);
+  const long long per = max((w.total + a.warps - 1) / a.warps, (long long)kFewest);
   if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i <= a.batch; i += kWarps * 32) a.starts[i] = starts[i];
+    for (int i = threadIdx.x; i <= a.batch; i += kThreads) a.starts[i] = starts[i];
     if (threadIdx.x == 0) a.starts[a.batch + 1] = (int)per;
   }
   griddep_launch();
-  const int w = blockIdx.x * kWarps + warp;
-  long long x = w * per;
-  const long long end = min(x + per, total);
-  const T* q = reinterpret_cast<const T*>(a.q);
-  while (x < end) {
+  uint8_t* base = dyn + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
+  auto ring_of = [&](int r) {
+    Ring rg;
+    rg.buf = base + r * kStages * Slice<D>::kStage;
+    rg.full = full[r];
+    rg.empty = empty[r];
+    return rg;
+  };
+  bool ok = true;
+  if (warp == kWarps) {
+    if (lane < kWarps) {
+      Ring rg = ring_of(lane);
+      const long long x = ((long long)lane * gridDim.x + blockIdx.x) * per;
+      ok = feed<D>(a, w, starts, rg, x, min(x + per, w.total));
+    }
+  } else {
+    Ring rg = ring_of(warp);
+    // neighbouring runs go to neighbouring CTAs: few runs still use every SM
+    const int me = warp * gridDim.x + blockIdx.x;
+    long long x = me * per;
+    const long long end = min(x + per, w.total);
+    const T* q = reinterpret_cast<const T*>(a.q);
     Rows<T, D> R;
-    const T* rp[2] = {nullptr, nullptr};
-    Keys ks = {&a.k, &a.v, nullptr, a.page_shift, a.pages, a.width, 0, 0};
-    int s0, s1, lo, rows;
-    float* po;
-    float2* pml;
-    if (x < pre_total) {
-      const int grp = (int)(x / sp), tile = grp % ptiles;
-      s0 = (int)(x % sp);
-      s1 = (int)min((long long)sp, s0 + (end - x));
-      lo = 0;
-      ks.head = grp / ptiles;
-      const int s = a.seqs[0];
-      ks.table = a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width;
-      rows = min(16, a.batch * a.group - tile * 16);
+    Segment g;
+    auto begin = [&]() {  // the segment at x: its rows of q are asked for
+      g = segment_at<D>(a, w, starts, x, end);
+      const T* rp[2];
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const int r = tile * 16 + (lane >> 2) + 8 * h;
-        const bool in = r < a.batch * a.group;
-        const int i = in ? r / a.group : 0;
-        rp[h] = in ? q + (long long)i * a.ldq + (long long)(ks.head * a.group + r % a.group) * D : nullptr;
-        R.hi[h] = in ? min(a.shared, seq_len(a, i)) : 0;
+        const int r = (lane >> 2) + 8 * h;
+        const bool in = r < g.rows;
+        const int row = in ? g.row0 + r : g.row0, i = g.prefix ? row / a.group : g.seq;
+        const int head = g.head * a.group + (g.prefix ? row % a.group : row);
+        rp[h] = in ? q + (long long)i * a.ldq + (long long)head * D : nullptr;
+        const int len = seq_len(a, i);
+        R.hi[h] = !g.prefix ? len : in ? min(a.shared, len) : 0;
       }
-      po = a.pre_o + ((long long)w + grp) * 16 * D;
-      pml = a.pre_ml + ((long long)w + grp) * 16;
-    } else {
-      const long long y = x - pre_total;
-      const int hr = (int)(y / own), z = (int)(y % own), tile = hr % tiles;
-      int lo_i = 0, hi_i = a.batch - 1;  // the sequence that slice z belongs to
-      while (lo_i < hi_i) {
-        const int mid = (lo_i + hi_i) >> 1;
-        if (starts[mid + 1] > z) hi_i = mid; else lo_i = mid + 1;
-      }
-      const int i = lo_i, off = a.shared / KS;
-      s0 = z - starts[i] + off;
-      s1 = (int)min((long long)(starts[i + 1] - starts[i] + off), s0 + (end - x));
-      lo = a.shared;
-      ks.head = hr / tiles;
-      ks.table = a.tables + (long long)a.seqs[i] * a.width;
-      rows = min(16, a.group - tile * 16);
-      const int len = seq_len(a, i);
+      R.load(rp[0], rp[1], lane);
+    };
+    if (x < end) begin();
+    while (ok && x < end) {
+      R.reset();
+      ok = attend<T, D>(R, rg, g.s0, g.s1, g.prefix ? 0 : a.shared, a.scale_log2, lane, a.spin);
+      if (!ok) break;
+      const long long slot = me + g.group;
+      float* po = g.prefix ? a.pre_o + slot * 16 * D : a.own_o + slot * a.own_rows * D;
+      float2* pml = g.prefix ? a.pre_ml + slot * 16 : a.own_ml + slot * a.own_rows;
+      const int rows = g.rows;
+      x += g.s1 - g.s0;
+      if (x < end) begin();  // the next segment's q is on its way while this one's result is stored
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const int r = tile * 16 + (lane >> 2) + 8 * h;
-        const bool in = r < a.group;
-        rp[h] = in ? q + (long long)i * a.ldq + (long long)(ks.head * a.group + r) * D : nullptr;
-        R.hi[h] = len;
+        const int r = (lane >> 2) + 8 * h;
+        if (r >= rows) continue;
+        if ((lane & 3) == 0) pml[r] = make_float2(R.m[h], R.l[h]);
+#pragma unroll
+        for (int i = 0; i < D / 8; i++)
+          *reinterpret_cast<float2*>(po + (long long)r * D + i * 8 + 2 * (lane & 3)) =
+              make_float2(R.o[i][2 * h], R.o[i][2 * h + 1]);
       }
-      const long long slot = (long long)w + (long long)hr * a.batch + i;
-      po = a.own_o + slot * a.own_rows * D;
-      pml = a.own_ml + slot * a.own_rows;
+      __syncwarp();
     }
-    R.load(rp[0], rp[1], lane);
-    if (!attend<T, D>(R, ks, rg, s0, s1, lo, a.scale_log2, lane, a.spin)) {
-      gave_up(a.err, lane);
-      return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const int r = (lane >> 2) + 8 * h;
-      if (r >= rows) continue;
-      if ((lane & 3) == 0) pml[r] = make_float2(R.m[h], R.l[h]);
-#pragma unroll
-      for (int i = 0; i < D / 8; i++)
-        *reinterpret_cast<float2*>(po + (long long)r * D + i * 8 + 2 * (lane & 3)) =
-            make_float2(R.o[i][2 * h], R.o[i][2 * h + 1]);
-    }
-    x += s1 - s0;
   }
+  if (!ok) gave_up(a.err);
   if (a.pre_splits) griddep_wait();  // this grid's end says to the next that both are done
 }
 
@@ -424,55 +471,72 @@ __global__ void __launch_bounds__(kWarps * 32) decode_warp_kernel(const __grid_c
 // in slot order. Each warp joins every fourth one, then the four are joined.
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_constant__ DecodeAttnArgs a) {
-  constexpr int KS = Slice<D>::kKeys;
   constexpr int V = D / 32;  // values of a row per lane, as V/4 runs of 4
+  constexpr int kBatch = 4;  // partial results in flight a warp
   __shared__ float so[kWarps][D];
   __shared__ float2 sml[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   const int i = blockIdx.x / a.heads_q, head = blockIdx.x % a.heads_q;
   const int kvh = head / a.group, gh = head % a.group;
-  const int tiles = (a.group + 15) / 16, ptiles = (a.batch * a.group + 15) / 16;
-  const int sp = a.pre_splits ? 0 : (a.shared + KS - 1) / KS, own = a.starts[a.batch];
+  const int len = seq_len(a, i), from = a.starts[i], n = a.starts[i + 1] - from;
+  const Walk w = walk_of<D>(a, a.starts[a.batch]);
   const long long per = a.starts[a.batch + 1];
-  const long long pre_total = (long long)a.heads_kv * ptiles * sp;
   float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
   for (int c = 0; c < V; c++) o[c] = 0.f;
-  auto take = [&](const float* po, float2 ml) {
-    const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2_fast(m - ref), g = exp2_fast(ml.x - ref);
-    l = l * f + ml.y * g;
+  // rows row0, row0 + step, ... (count of them) of a list of partial results
+  auto take = [&](const float* po, const float2* pml, long long row0, long long step, int count) {
+    for (int z0 = warp; z0 < count; z0 += kWarps * kBatch) {
+      float2 ml[kBatch];
+      float4 x[kBatch][V / 4];
 #pragma unroll
-    for (int c = 0; c < V / 4; c++) {
-      const float4 x = *reinterpret_cast<const float4*>(po + c * 128 + lane * 4);
-      o[c * 4] = o[c * 4] * f + x.x * g;
-      o[c * 4 + 1] = o[c * 4 + 1] * f + x.y * g;
-      o[c * 4 + 2] = o[c * 4 + 2] * f + x.z * g;
-      o[c * 4 + 3] = o[c * 4 + 3] * f + x.w * g;
+      for (int k = 0; k < kBatch; k++) {
+        const int z = z0 + k * kWarps;
+        const long long row = row0 + step * (z < count ? z : z0);
+        ml[k] = z < count ? pml[row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int c = 0; c < V / 4; c++) x[k][c] = *reinterpret_cast<const float4*>(po + row * D + c * 128 + lane * 4);
+      }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) mn = fmaxf(mn, ml[k].x);
+      const float ref = mn == -INFINITY ? 0.f : mn, f = exp2_fast(m - ref);
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < V; c++) o[c] *= f;
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) {
+        if (z0 + k * kWarps >= count) break;
+        const float g = exp2_fast(ml[k].x - ref);
+        l += ml[k].y * g;
+#pragma unroll
+        for (int c = 0; c < V / 4; c++) {
+          o[c * 4] += x[k][c].x * g;
+          o[c * 4 + 1] += x[k][c].y * g;
+          o[c * 4 + 2] += x[k][c].z * g;
+          o[c * 4 + 3] += x[k][c].w * g;
+        }
+      }
+      m = mn;
     }
-    m = mn;
   };
-  for (int z = warp; z < a.pre_splits; z += kWarps) {
-    const long long row = (long long)z * a.batch * a.heads_q + blockIdx.x;
-    take(a.pre_o + row * D, a.pre_ml[row]);
+  // the runs that hold a part of slices [x0, x0 + count)
+  auto runs = [&](long long x0, int count, long long* first) {
+    *first = x0 / per;
+    return (int)((x0 + count - 1) / per - *first) + 1;
+  };
+  take(a.pre_o, a.pre_ml, blockIdx.x, (long long)a.batch * a.heads_q, a.pre_splits);
+  long long first;
+  if (w.sp) {
+    const int r = i * a.group + gh, grp = kvh * w.ptiles + r / 16;
+    const int k = runs((long long)grp * w.sp, w.sp, &first);
+    take(a.pre_o, a.pre_ml, (first + grp) * 16 + r % 16, 16, k);
   }
-  if (sp) {
-    const int r = i * a.group + gh, grp = kvh * ptiles + r / 16;
-    const long long x0 = (long long)grp * sp, x1 = x0 + sp;
-    for (long long w = x0 / per + warp; w <= (x1 - 1) / per; w += kWarps) {
-      const long long row = (w + grp) * 16 + r % 16;
-      take(a.pre_o + row * D, a.pre_ml[row]);
-    }
-  }
-  const int n = a.starts[i + 1] - a.starts[i];
   if (n) {
-    const int hr = kvh * tiles + gh / 16;
-    const long long x0 = pre_total + (long long)hr * own + a.starts[i], x1 = x0 + n;
-    for (long long w = x0 / per + warp; w <= (x1 - 1) / per; w += kWarps) {
-      const long long row = (w + (long long)hr * a.batch + i) * a.own_rows + gh % 16;
-      take(a.own_o + row * D, a.own_ml[row]);
-    }
+    const int hr = kvh * w.tiles + gh / 16;
+    const int k = runs(w.pre_total + (long long)hr * w.own + from, n, &first);
+    take(a.own_o, a.own_ml, (first + (long long)hr * a.batch + i) * a.own_rows + gh % 16, a.own_rows, k);
   }
   griddep_launch();
 #pragma unroll
@@ -480,24 +544,24 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
   if (lane == 0) sml[warp] = make_float2(m, l);
   __syncthreads();
   float mn = -INFINITY, sum = 0.f, f[kWarps];
-  for (int w = 0; w < kWarps; w++) mn = fmaxf(mn, sml[w].x);
+  for (int k = 0; k < kWarps; k++) mn = fmaxf(mn, sml[k].x);
   const float ref = mn == -INFINITY ? 0.f : mn;
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) {
-    f[w] = exp2_fast(sml[w].x - ref);
-    sum += sml[w].y * f[w];
+  for (int k = 0; k < kWarps; k++) {
+    f[k] = exp2_fast(sml[k].x - ref);
+    sum += sml[k].y * f[k];
   }
-  const bool none = seq_len(a, i) == 0;  // a sequence without tokens: zeros
   const float inv = 1.f / sum;
   T* out = reinterpret_cast<T*>(a.out) + (long long)i * a.ldo + (long long)head * D;
   for (int c = threadIdx.x * 2; c < D; c += kWarps * 64) {
     float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-      x += so[w][c] * f[w];
-      y += so[w][c + 1] * f[w];
+    for (int k = 0; k < kWarps; k++) {
+      x += so[k][c] * f[k];
+      y += so[k][c + 1] * f[k];
     }
-    *reinterpret_cast<uint32_t*>(out + c) = none ? 0u : pack2<T>(x * inv, y * inv);
+    // a sequence without tokens: zeros
+    *reinterpret_cast<uint32_t*>(out + c) = len == 0 ? 0u : pack2<T>(x * inv, y * inv);
   }
 }
 
@@ -506,7 +570,7 @@ int decode_of(const DecodeAttnArgs& a, cudaStream_t s) {
   const void* fn = (const void*)decode_warp_kernel<T, D>;
   int rc = opt_in_smem(fn, warp_smem<D>());
   if (rc) return rc;
-  rc = launch_kernel(fn, dim3((unsigned)(a.warps / kWarps)), dim3(kWarps * 32), warp_smem<D>(), s,
+  rc = launch_kernel(fn, dim3((unsigned)(a.warps / kWarps)), dim3(kThreads), warp_smem<D>(), s,
                      const_cast<DecodeAttnArgs*>(&a), a.pre_splits > 0, 1);
   if (rc) return rc;
   return launch_kernel((const void*)decode_join_kernel<T, D>, dim3((unsigned)(a.batch * a.heads_q)), dim3(kWarps * 32), 0,
