@@ -9,6 +9,7 @@ every step runs in the kernels of ``libtfx_exl3.so``. Names follow the C ABI:
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import sys
 
 try:
@@ -61,7 +62,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if torch else
 
 
 def _lib():
-    return _pkg.lib()
+    return _pkg._lib or _pkg.lib()
+
+
+@functools.lru_cache(maxsize=64)
+def _heads(hq: int, hkv: int, dim: int, act: int, scale):
+    """The C descriptor of a head layout (a model has a few); read-only once made."""
+    return C.byref(HeadsStruct(hq, hkv, dim, act, dim ** -0.5 if scale is None else scale))
 
 
 def _check(rc: int) -> None:
@@ -71,9 +78,7 @@ def _check(rc: int) -> None:
 
 def _stream(stream, device: int) -> int:
     """A stream's handle; by default torch's current one on the device."""
-    if stream is None:
-        return _raw_stream(device)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    return _raw_stream(device) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _act(dtype) -> int:
@@ -125,14 +130,18 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
     if last > min(T, Tk, Tv):
         raise ValueError(f"offsets end at {last}, past the rows of q, k or v")
     if out is None:
-        out = torch.empty((T, hq, dim), dtype=dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ldo, pout = hq * dim, out.data_ptr()
         if first > 0 or last < T:
             out.zero_()
-    To, ldo, pout = _rows("out", out, hq, dim, dtype, dev)
-    if To < last:
-        raise ValueError(f"out has {To} rows, offsets end at {last}")
-    h = HeadsStruct(hq, hkv, dim, _act(dtype), dim ** -0.5 if scale is None else scale)
-    _check(_lib().tfx_attn_prompt(C.byref(h), pq, ldq, pk, ldk, pv, ldv, po, n - 1, pout, ldo, _stream(stream, dev)))
+    else:
+        To, ldo, pout = _rows("out", out, hq, dim, dtype, dev)
+        if To < last:
+            raise ValueError(f"out has {To} rows, offsets end at {last}")
+    rc = _lib().tfx_attn_prompt(_heads(hq, hkv, dim, _act(dtype), scale), pq, ldq, pk, ldk, pv, ldv, po, n - 1, pout, ldo,
+                                _stream(stream, dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -158,7 +167,8 @@ class Cache:
             book[4 + slots + pages:] = -1
         elif book.numel() != ints:
             raise ValueError(f"book of {book.numel()} values, {ints} are wanted")
-        self.device, self.dtype, self.heads_kv, self.dim = k.get_device(), k.dtype, heads, dim
+        self.device, self.dtype, self.heads_kv, self.dim, self.act = k.get_device(), k.dtype, heads, dim, self.s.act
+        self.ref = C.byref(self.s)
         self.s.book = _ints("book", book, self.device)[1]
         self.k, self.v, self.book = k, v, book
 
@@ -178,9 +188,6 @@ class Cache:
         """The book's status bits (CACHE_FULL, CACHE_BAD, CACHE_TABLE_FULL); waits for the GPU."""
         return int(self.book[0])
 
-    def ref(self):
-        return C.byref(self.s)
-
     def __del__(self):
         try:
             if self.s.priv and _pkg._lib is not None:
@@ -191,11 +198,11 @@ class Cache:
 
 def cache_reserve(c: Cache, max_batch: int, heads: int, stream=None) -> None:
     """Scratch for attn_decode over up to max_batch sequences of `heads` query heads, and for the page calls."""
-    _check(_lib().tfx_cache_reserve(c.ref(), max_batch, heads, _stream(stream, c.device)))
+    _check(_lib().tfx_cache_reserve(c.ref, max_batch, heads, _stream(stream, c.device)))
 
 
 def cache_release(c: Cache) -> None:
-    _check(_lib().tfx_cache_release(c.ref()))
+    _check(_lib().tfx_cache_release(c.ref))
 
 
 def cache_extend(c: Cache, seqs, offsets, stream=None) -> None:
@@ -204,7 +211,7 @@ def cache_extend(c: Cache, seqs, offsets, stream=None) -> None:
     m, po = _ints("offsets", offsets, c.device)
     if m != n + 1:
         raise ValueError(f"{m} offsets for {n} sequences")
-    _check(_lib().tfx_cache_extend(c.ref(), ps, po, n, _stream(stream, c.device)))
+    _check(_lib().tfx_cache_extend(c.ref, ps, po, n, _stream(stream, c.device)))
 
 
 def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=None) -> None:
@@ -217,7 +224,7 @@ def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=Non
         raise ValueError(f"{n} rows of k, {m} of v")
     if offsets is not None and seqs is not None and offsets.numel() != seqs.numel() + 1:
         raise ValueError(f"{offsets.numel()} offsets for {seqs.numel()} sequences")
-    _check(_lib().tfx_cache_append(c.ref(), layer, pk, ldk, pv, ldv, n, _stream(stream, c.device)))
+    _check(_lib().tfx_cache_append(c.ref, layer, pk, ldk, pv, ldv, n, _stream(stream, c.device)))
 
 
 def _pair(c: Cache, src, dst) -> tuple:
@@ -230,23 +237,23 @@ def _pair(c: Cache, src, dst) -> tuple:
 
 def cache_fork(c: Cache, src, dst, stream=None) -> None:
     """Slot dst[i] becomes a copy of sequence src[i]: full pages shared, a partly filled last one copied."""
-    _check(_lib().tfx_cache_fork(c.ref(), *_pair(c, src, dst), _stream(stream, c.device)))
+    _check(_lib().tfx_cache_fork(c.ref, *_pair(c, src, dst), _stream(stream, c.device)))
 
 
 def cache_free(c: Cache, seqs, stream=None) -> None:
     """The sequences give their pages back."""
     n, ps = _ints("seqs", seqs, c.device)
-    _check(_lib().tfx_cache_free(c.ref(), ps, n, _stream(stream, c.device)))
+    _check(_lib().tfx_cache_free(c.ref, ps, n, _stream(stream, c.device)))
 
 
 def cache_compact(c: Cache, stream=None) -> None:
     """Moves the used pages to the front of the pool; book[1] is the number moved."""
-    _check(_lib().tfx_cache_compact(c.ref(), _stream(stream, c.device)))
+    _check(_lib().tfx_cache_compact(c.ref, _stream(stream, c.device)))
 
 
 def cache_copy(c: Cache, src, dst, stream=None) -> None:
     """Contents of page src[i] to page dst[i], all layers."""
-    _check(_lib().tfx_cache_copy(c.ref(), *_pair(c, src, dst), _stream(stream, c.device)))
+    _check(_lib().tfx_cache_copy(c.ref, *_pair(c, src, dst), _stream(stream, c.device)))
 
 
 def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | None = None, out=None, stream=None):
@@ -261,12 +268,16 @@ def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | N
     if n != b:
         raise ValueError(f"{n} sequences for {b} rows of q")
     if out is None:
-        out = torch.empty((b, hq, dim), dtype=c.dtype, device=q.device)
-    bo, ldo, po = _rows("out", out, hq, dim, c.dtype, dev)
-    if bo != b:
-        raise ValueError(f"out has {bo} rows, q {b}")
-    h = HeadsStruct(hq, c.heads_kv, dim, c.s.act, dim ** -0.5 if scale is None else scale)
-    _check(_lib().tfx_attn_decode(c.ref(), layer, C.byref(h), pq, ldq, ps, b, shared, po, ldo, _stream(stream, dev)))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ldo, po = hq * dim, out.data_ptr()
+    else:
+        bo, ldo, po = _rows("out", out, hq, dim, c.dtype, dev)
+        if bo != b:
+            raise ValueError(f"out has {bo} rows, q {b}")
+    rc = _lib().tfx_attn_decode(c.ref, layer, _heads(hq, c.heads_kv, dim, c.act, scale), pq, ldq, ps, b, shared, po, ldo,
+                                _stream(stream, dev))
+    if rc:
+        _check(rc)
     return out
 
 
