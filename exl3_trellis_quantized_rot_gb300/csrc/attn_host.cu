@@ -213,7 +213,7 @@ int64_t prefix_rows(int batch, int heads_q, int heads_kv) {
 
 // Decode scratch for `batch` sequences: byte offsets of its parts.
 struct DecodeScratch {
-  size_t starts, own_ml, pre_ml, own_o, pre_o, bytes;
+  size_t runs, own_ml, pre_ml, own_o, pre_o, bytes;
 };
 DecodeScratch decode_scratch(int batch, int heads_q, int heads_kv, int dim, int warps) {
   const int64_t group = heads_q / heads_kv, tiles = (group + kRowTile - 1) / kRowTile;
@@ -225,8 +225,8 @@ DecodeScratch decode_scratch(int batch, int heads_q, int heads_kv, int dim, int 
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
   DecodeScratch d;
   int64_t at = 0;
-  d.starts = at;
-  at += up((batch + 2) * 4LL);
+  d.runs = at;
+  at += up(heads_kv * (ptiles + tiles * batch) * 8);
   d.own_ml = at;
   at += up(own * 8);
   d.pre_ml = at;
@@ -475,7 +475,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   const DecodeScratch d = decode_scratch(batch, h->heads_q, c->heads_kv, c->dim, a.warps);
   if (d.bytes > pv->part_bytes)
     return fail_with(TFX_ENOTRESERVED, "%d sequences of %d heads take more scratch than was reserved", batch, h->heads_q);
-  a.starts = reinterpret_cast<int*>(pv->part + d.starts);
+  a.runs = reinterpret_cast<int2*>(pv->part + d.runs);
   a.own_ml = reinterpret_cast<float2*>(pv->part + d.own_ml);
   a.pre_ml = reinterpret_cast<float2*>(pv->part + d.pre_ml);
   a.own_o = reinterpret_cast<float*>(pv->part + d.own_o);

@@ -57,7 +57,7 @@ struct DecodeAttnArgs {
   int per_tile, tokens, pre_splits, items;  // tensor-core kernel
   int warps;          // NW
   int own_rows;       // rows of an own slot: min(16, group)
-  int* starts;        // [batch + 1] own slices before sequence i; then per
+  int2* runs;         // [prefix groups + own groups]: the first warp that has a part of a group, and how many have
   float* own_o;       // [NW + groups][own_rows][dim]
   float2* own_ml;     // [NW + groups][own_rows]: (reference of the exponents, sum)
   float* pre_o;       // [NW + prefix groups][16][dim], or [pre_splits][batch][heads_q][dim]

@@ -395,9 +395,16 @@ __global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_cons
   }
   const Walk w = walk_of<D>(a, carry);
   const long long per = max((w.total + a.warps - 1) / a.warps, (long long)kFewest);
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i <= a.batch; i += kThreads) a.starts[i] = starts[i];
-    if (threadIdx.x == 0) a.starts[a.batch + 1] = (int)per;
+  // for the join: the runs that hold a part of each group
+  {
+    const int pre = a.heads_kv * w.ptiles * (w.sp > 0), own = a.heads_kv * w.tiles * a.batch;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < pre + own; i += gridDim.x * kThreads) {
+      const int y = i - pre, hr = y / a.batch, seq = y - hr * a.batch;
+      const long long x0 = i < pre ? (long long)i * w.sp : w.pre_total + (long long)hr * w.own + starts[seq];
+      const int n = i < pre ? w.sp : starts[seq + 1] - starts[seq];
+      const int first = (int)(x0 / per);
+      a.runs[i] = make_int2(first, n ? (int)((x0 + n - 1) / per) - first + 1 : 0);
+    }
   }
   griddep_launch();
   uint8_t* base = dyn + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
@@ -478,10 +485,13 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   const int i = blockIdx.x / a.heads_q, head = blockIdx.x % a.heads_q;
-  const int kvh = head / a.group, gh = head % a.group;
-  const int len = seq_len(a, i), from = a.starts[i], n = a.starts[i + 1] - from;
-  const Walk w = walk_of<D>(a, a.starts[a.batch]);
-  const long long per = a.starts[a.batch + 1];
+  const int kvh = head / a.group, gh = head % a.group, r = i * a.group + gh;
+  const int tiles = (a.group + 15) / 16, ptiles = (a.batch * a.group + 15) / 16;
+  const int hr = kvh * tiles + gh / 16, grp = kvh * ptiles + r / 16;
+  const bool pre = a.shared > 0 && !a.pre_splits;
+  const int2 own = a.runs[(pre ? a.heads_kv * ptiles : 0) + hr * a.batch + i];
+  const int2 first = pre ? a.runs[grp] : make_int2(0, 0);
+  const int len = seq_len(a, i);
   float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
   for (int c = 0; c < V; c++) o[c] = 0.f;
@@ -521,23 +531,9 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
       m = mn;
     }
   };
-  // the runs that hold a part of slices [x0, x0 + count)
-  auto runs = [&](long long x0, int count, long long* first) {
-    *first = x0 / per;
-    return (int)((x0 + count - 1) / per - *first) + 1;
-  };
   take(a.pre_o, a.pre_ml, blockIdx.x, (long long)a.batch * a.heads_q, a.pre_splits);
-  long long first;
-  if (w.sp) {
-    const int r = i * a.group + gh, grp = kvh * w.ptiles + r / 16;
-    const int k = runs((long long)grp * w.sp, w.sp, &first);
-    take(a.pre_o, a.pre_ml, (first + grp) * 16 + r % 16, 16, k);
-  }
-  if (n) {
-    const int hr = kvh * w.tiles + gh / 16;
-    const int k = runs(w.pre_total + (long long)hr * w.own + from, n, &first);
-    take(a.own_o, a.own_ml, (first + (long long)hr * a.batch + i) * a.own_rows + gh % 16, a.own_rows, k);
-  }
+  take(a.pre_o, a.pre_ml, (long long)(first.x + grp) * 16 + r % 16, 16, first.y);
+  take(a.own_o, a.own_ml, ((long long)own.x + (long long)hr * a.batch + i) * a.own_rows + gh % 16, a.own_rows, own.y);
   griddep_launch();
 #pragma unroll
   for (int c = 0; c < V; c++) so[warp][(c >> 2) * 128 + lane * 4 + (c & 3)] = o[c];
