@@ -22,7 +22,7 @@
 // probabilities P(j-1) V(j-1) has read before it.
 //
 // Warps of a CTA: 0..7 softmax and results; 8 issues the MMAs (in the even CTA);
-// 9 asks for K, V and Q; 10 and 11 look after V where a tile has keys that some
+// 9 asks for K and Q, 10 for V; 11 looks after V where a tile has keys that some
 // row must not see: 0 * inf and 0 * NaN are NaN, so V's rows past the sequence
 // become zeros, and later tokens' values that are not finite too; the rows that
 // do see the latter get them when the result is stored.
@@ -46,7 +46,7 @@ namespace tfx {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kEdgeWarp = 10;  // 0..7 softmax, 10 and 11 edges
+constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kEdgeWarp = 11;  // 0..7 softmax
 constexpr int kTileKeys = 128;
 constexpr float kSlack = 8.f;  // log2 by which a row's maximum may pass its reference
 constexpr int kEdgeBars = 4, kFixes = 8;
@@ -63,7 +63,7 @@ struct Geom {
 struct Barriers {
   uint64_t q_full, q_empty;
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t v_edge[kEdgeBars];  // V tiles that warps 10 and 11 look at before the MMAs may
+  uint64_t v_edge[kEdgeBars];  // V tiles that warp 11 looks at before the MMAs may
   uint64_t s_full[3];          // scores are in tensor memory
   uint64_t p_full[3];          // probabilities of both CTAs are
   // P V of a tile is added. One a score buffer, like the two above: a parity tells
@@ -376,6 +376,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s_addr(&tmem_slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  // the first pages are looked up while the pair comes together
+  Pages pg = {};
+  const int x0 = nth(a, 0);
+  if ((warp == kKWarp || warp == kVWarp) && x0 >= 0) {
+    pg = pages_of(a);
+    look_up(a, pg, item_of(a, x0).first, lane);
+  }
   // rows of Q that no copy writes
   for (int x = a.tokens * a.per_tile * 8 + threadIdx.x; x < 128 * 8; x += kThreads)
     for (int ch = 0; ch < D / 64; ch++)
@@ -390,52 +397,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   // registers: 384 x 168 at launch; 256 x 208 + 128 x 80 = 63,488 of those 64,512 from here on
   if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
 
-  if (warp == kCopyWarp) {
-    // ---- copies: this CTA's rows of Q, its 64 keys of K, its dim/2 columns of V,
-    // in the order in which the MMAs free the memory for them: K runs SB - 1 tiles
-    // ahead of V, and an item's first K ahead of its Q
-    auto lead = [&](uint64_t* bar) { return peer_addr(s_addr(bar), 0); };
-    int edges = 0, gk = 0, gv = 0;
+  auto lead = [&](uint64_t* bar) { return peer_addr(s_addr(bar), 0); };
+  if (warp == kKWarp) {
+    // ---- copies: this CTA's 64 keys of K and its rows of Q; an item's first K
+    // need not wait until the last one's Q has been read
+    int g = 0;
     bool ok = true;
-    Pages pk = pages_of(a), pv = pk;
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
-      auto send_k = [&](int j) {
-        const int st = gk % ST;
-        look_up(a, pk, it.first + j, lane);
-        ok = ok && wait_warp(c, &bars.k_empty[st], ((gk / ST) & 1) ^ 1);
-        if (!ok) return;
+      for (int j = 0; ok && j < it.tiles; j++, g++) {
+        const int st = g % ST;
+        look_up(a, pg, it.first + j, lane);
+        if (!(ok = wait_warp(c, &bars.k_empty[st], ((g / ST) & 1) ^ 1))) break;
         const uint32_t bar = lead(&bars.k_full[st]);
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_k<D>(a, it, pk, j, (int)rank, sk + st * G::kKV, bar, lane);
-        gk++;
-      };
-      auto send_v = [&](int j) {
-        const int st = gv % ST;
-        look_up(a, pv, it.first + j, lane);
-        ok = ok && wait_warp(c, &bars.v_empty[st], ((gv / ST) & 1) ^ 1);
-        if (!ok) return;
+        copy_k<D>(a, it, pg, j, (int)rank, sk + st * G::kKV, bar, lane);
+        if (j > 0) continue;
+        if (!(ok = wait_warp(c, &bars.q_empty, (r & 1) ^ 1))) break;
+        if (lane == 0) {
+          expect_tx_at(lead(&bars.q_full), a.tokens * a.per_tile * D * 2);
+          for (int ch = 0; ch < D / 64; ch++)
+            tma_load_5d_pair(sq + ch * 16384, &a.qmap, 0, it.head0, it.row0 + (int)rank * a.tokens, ch, 0, lead(&bars.q_full));
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == kVWarp) {
+    // ---- copies: its dim/2 columns of V
+    int g = 0, edges = 0;
+    bool ok = true;
+    for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
+      const Item it = item_of(a, x);
+      for (int j = 0; j < it.tiles; j++, g++) {
+        const int st = g % ST;
+        look_up(a, pg, it.first + j, lane);
+        if (!(ok = wait_warp(c, &bars.v_empty[st], ((g / ST) & 1) ^ 1))) break;
         const bool edge = (it.first + j + 1) * kTileKeys > it.hidden;
         const uint32_t bar = edge ? peer_addr(s_addr(&bars.v_edge[edges % kEdgeBars]), rank) : lead(&bars.v_full[st]);
         edges += edge;
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_v<D>(a, it, pv, j, (int)rank, sv + st * G::kKV, bar, lane);
-        gv++;
-      };
-      for (int j = 0; j < SB - 1 && j < it.tiles; j++) send_k(j);
-      ok = ok && wait_warp(c, &bars.q_empty, (r & 1) ^ 1);
-      if (!ok) break;
-      if (lane == 0) {
-        expect_tx_at(lead(&bars.q_full), a.tokens * a.per_tile * D * 2);
-        for (int ch = 0; ch < D / 64; ch++)
-          tma_load_5d_pair(sq + ch * 16384, &a.qmap, 0, it.head0, it.row0 + (int)rank * a.tokens, ch, 0, lead(&bars.q_full));
-      }
-      __syncwarp();
-      for (int j = 0; ok && j < it.tiles; j++) {
-        if (j + SB - 1 < it.tiles) send_k(j + SB - 1);
-        send_v(j);
+        copy_v<D>(a, it, pg, j, (int)rank, sv + st * G::kKV, bar, lane);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -491,35 +494,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   } else if (warp >= kEdgeWarp) {
     // ---- V tiles with keys that some row must not see
     int edges = 0, g = 0;
+    bool ok = true;
     for (int r = 0, x; (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
       for (int j = 0; j < it.tiles; j++, g++) {
         const int key0 = (it.first + j) * kTileKeys;
         if (key0 + kTileKeys <= it.hidden) continue;
         const int st = g % ST;
-        // both warps meet at the barrier below for every tile, also after a timeout;
-        // then nothing is handed on: v_full may still be in an earlier tile's
-        // phase, which takes that tile's two arrivals and no more
-        const bool ok = wait_warp(c, &bars.v_edge[edges % kEdgeBars], (edges / kEdgeBars) & 1);
+        // after a timeout nothing is handed on: v_full may still be in an earlier
+        // tile's phase, which takes that tile's two arrivals and no more
+        ok = ok && wait_warp(c, &bars.v_edge[edges % kEdgeBars], (edges / kEdgeBars) & 1);
         edges++;
         const int from = max(it.hidden - key0, 0);
         constexpr int kPieces = D / 16;  // 16-byte pieces of a row in this CTA
         bool found = false;
         const int till = min((it.seen - key0 + 15) & ~15, kTileKeys);  // the product takes 16 keys at a time, and no more
         const int all = ok ? (till - from) * kPieces : 0;
-        for (int y0 = threadIdx.x - kEdgeWarp * 32; y0 < all; y0 += 256) {
+        for (int y0 = lane; y0 < all; y0 += 128) {
           uint4 w[4];
           uint32_t at[4];
 #pragma unroll
           for (int k = 0; k < 4; k++) {
-            const int y = y0 + 64 * k, row = from + y / kPieces, p = y % kPieces;
+            const int y = y0 + 32 * k, row = from + y / kPieces, p = y % kPieces;
             at[k] = sv + st * G::kKV + (p >> 3) * (kTileKeys * 128) + row * 128 + (p & 7) * 16;
             if (y < all)
               asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w) : "r"(at[k]));
           }
 #pragma unroll
           for (int k = 0; k < 4; k++) {
-            const int y = y0 + 64 * k;
+            const int y = y0 + 32 * k;
             if (y >= all) continue;
             if (key0 + from + y / kPieces < it.seen) {
               const uint32_t m[4] = {not_finite<T>(w[k].x), not_finite<T>(w[k].y), not_finite<T>(w[k].z), not_finite<T>(w[k].w)};
@@ -543,8 +546,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
         fence_async_smem();
-        asm volatile("bar.sync 5, 64;" ::: "memory");
-        if (threadIdx.x == kEdgeWarp * 32 && ok && !*c.abort_flag) arrive_at(peer_addr(s_addr(&bars.v_full[st]), 0));
+        __syncwarp();
+        if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.v_full[st]), 0));
       }
     }
   } else {
@@ -559,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     int g = 0;
     bool ok = true;
     const int tok = (int)rank * a.tokens + my_tok;
-    int x = nth(a, 0);
+    int x = x0;
     Item it, next = {};
     if (x >= 0) it = item_of(a, x);
     for (int r = 0; x >= 0; r++, it = next) {
