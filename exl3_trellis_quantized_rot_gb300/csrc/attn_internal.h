@@ -19,6 +19,7 @@ constexpr int kAttnMaxSeqs = 512;  // sequences of one prompt launch (longer lis
 // keys) to the first: level by level, at each the sequences that have it.
 // before[s] is the number of tiles that come before level count[s] - 1.
 struct PromptArgs {
+  static constexpr bool kFewRows = false;
   CUtensorMap qmap, k, v;
   const void* vbase;
   void* out;
@@ -43,6 +44,7 @@ struct PromptArgs {
 // Warp w takes the slices [w*per, (w+1)*per); a run of them inside one group is
 // a segment with its own partial result, in slot w + (number of the group).
 struct DecodeAttnArgs {
+  static constexpr bool kFewRows = true;
   CUtensorMap k, v;           // boxes of 16 tokens, all of a head's values
   CUtensorMap qmap, kt, vt;   // tensor-core kernel: tiles of Q; boxes of up to 64 tokens of 64 values
   const void* q;

@@ -567,7 +567,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     if (x >= 0) it = item_of(a, x);
     for (int r = 0; x >= 0; r++, it = next) {
       const bool live = my_tok < a.tokens && it.row0 + tok < it.end_row;
-      const bool some = __any_sync(~0u, live);  // the same in both warps: where no row is a token's, there is nothing to compute
+      // A decode batch may leave whole warps without a row: they only hand on. (The
+      // same in both warps. Prompts fill their tiles; the test alone cost 4 % there.)
+      const bool some = !A::kFewRows || __any_sync(~0u, live);
       const int hi = live ? sees(a, it, tok) : INT_MAX;  // keys the row sees; a row that is no token's is not stored
       float ref = -INFINITY, l = 0.f;
       float s[64];
