@@ -79,27 +79,26 @@ struct Ctx {
   long long spin;
 };
 
-__device__ __forceinline__ bool wait(const Ctx& c, uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (true) {
-    for (int i = 0; i < 16; i++)
-      if (mbar_poll(bar, parity)) return true;
-    if (*c.abort_flag) return false;
-    if (clock64() - t0 > c.spin) {
-      *c.abort_flag = 1;
-      atomicExch(c.err, 1);
-      return false;
-    }
-  }
-}
-// For a whole warp. One lane does the waiting proper, so that the lanes are
-// together again for the warp-wide instructions that follow, after a timeout too.
+// The whole warp waits, its lanes together, as the warp-wide instructions that
+// follow want them: after a timeout too. Warps that have time to spare sleep NAP
+// ns between polls and leave issue slots and the shared-memory pipe to the softmax
+// warps beside them (48/8 heads of 128: 299 -> 288 us).
+template <int NAP>
 __device__ __forceinline__ bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
   if (__all_sync(~0u, mbar_poll(bar, parity))) return true;
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait(c, bar, parity);
-  ok = __shfl_sync(~0u, ok, 0);
-  return ok != 0;
+  const long long t0 = clock64();
+  while (true) {
+    for (int i = 0; i < 8; i++) {
+      if (NAP) __nanosleep(NAP);
+      if (__all_sync(~0u, mbar_poll(bar, parity))) return true;
+    }
+    const bool late = clock64() - t0 > c.spin;
+    if (late && (threadIdx.x & 31) == 0) {
+      *c.abort_flag = 1;
+      atomicExch(c.err, 1);
+    }
+    if (__any_sync(~0u, late || *c.abort_flag)) return false;
+  }
 }
 
 // The two warps that share rows meet at their named barrier.
@@ -408,13 +407,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       for (int j = 0; ok && j < it.tiles; j++, g++) {
         const int st = g % ST;
         look_up(a, pg, it.first + j, lane);
-        if (!(ok = wait_warp(c, &bars.k_empty[st], ((g / ST) & 1) ^ 1))) break;
+        if (!(ok = wait_warp<30>(c, &bars.k_empty[st], ((g / ST) & 1) ^ 1))) break;
         const uint32_t bar = lead(&bars.k_full[st]);
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
         copy_k<D>(a, it, pg, j, (int)rank, sk + st * G::kKV, bar, lane);
         if (j > 0) continue;
-        if (!(ok = wait_warp(c, &bars.q_empty, (r & 1) ^ 1))) break;
+        if (!(ok = wait_warp<30>(c, &bars.q_empty, (r & 1) ^ 1))) break;
         if (lane == 0) {
           expect_tx_at(lead(&bars.q_full), a.tokens * a.per_tile * D * 2);
           for (int ch = 0; ch < D / 64; ch++)
@@ -432,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       for (int j = 0; j < it.tiles; j++, g++) {
         const int st = g % ST;
         look_up(a, pg, it.first + j, lane);
-        if (!(ok = wait_warp(c, &bars.v_empty[st], ((g / ST) & 1) ^ 1))) break;
+        if (!(ok = wait_warp<30>(c, &bars.v_empty[st], ((g / ST) & 1) ^ 1))) break;
         const bool edge = (it.first + j + 1) * kTileKeys > it.hidden;
         const uint32_t bar = edge ? peer_addr(s_addr(&bars.v_edge[edges % kEdgeBars]), rank) : lead(&bars.v_full[st]);
         edges += edge;
@@ -450,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       bool ok = true;
       auto scores = [&](int y, bool last) -> bool {
         const int st = y % ST;
-        if (!wait_warp(c, &bars.k_full[st], (y / ST) & 1)) return false;
+        if (!wait_warp<10>(c, &bars.k_full[st], (y / ST) & 1)) return false;
         fence_after_sync();
         const uint64_t qd = operand(sq, kmaj), kd = operand(sk + st * G::kKV, kmaj);
         const uint32_t d = tm + D + (y % SB) * 128;
@@ -468,14 +467,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
         const Item it = item_of(a, x);
         const int n = it.tiles, last_steps = (min(it.seen - (it.first + n - 1) * kTileKeys, kTileKeys) + 15) >> 4;
-        if (!(ok = wait_warp(c, &bars.q_full, r & 1))) break;
+        if (!(ok = wait_warp<10>(c, &bars.q_full, r & 1))) break;
         int ahead = 0;  // scores of the item's tiles issued: up to SB - 1 more than the products with V
         for (int j = 0; j < n; j++, g++) {
           for (; ok && ahead < n && ahead < j + SB; ahead++) ok = scores(g - j + ahead, ahead + 1 == n);
           if (!ok) break;
           const int st = g % ST;
-          if (!(ok = wait_warp(c, &bars.v_full[st], (g / ST) & 1) && wait_warp(c, &bars.p_full[g % SB], (g / SB) & 1))) break;
-          if (j == 0 && r > 0 && !(ok = wait_warp(c, &bars.o_empty, (r - 1) & 1))) break;
+          if (!(ok = wait_warp<10>(c, &bars.v_full[st], (g / ST) & 1) && wait_warp<10>(c, &bars.p_full[g % SB], (g / SB) & 1))) break;
+          if (j == 0 && r > 0 && !(ok = wait_warp<10>(c, &bars.o_empty, (r - 1) & 1))) break;
           fence_after_sync();
           const uint64_t vd = operand(sv + st * G::kKV, vmaj);
           const uint32_t p = tm + D + (g % SB) * 128;
@@ -503,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         const int st = g % ST;
         // after a timeout nothing is handed on: v_full may still be in an earlier
         // tile's phase, which takes that tile's two arrivals and no more
-        ok = ok && wait_warp(c, &bars.v_edge[edges % kEdgeBars], (edges / kEdgeBars) & 1);
+        ok = ok && wait_warp<300>(c, &bars.v_edge[edges % kEdgeBars], (edges / kEdgeBars) & 1);
         edges++;
         const int from = max(it.hidden - key0, 0);
         constexpr int kPieces = D / 16;  // 16-byte pieces of a row in this CTA
@@ -579,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         tmem_ld32(t + 32, s + 32);
       };
       for (int j = 0; j < it.tiles; j++, g++) {
-        ok = wait_warp(c, &bars.s_full[g % SB], (g / SB) & 1) && ok;
+        ok = wait_warp<0>(c, &bars.s_full[g % SB], (g / SB) & 1) && ok;
         if (!some) {
           if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.p_full[g % SB]), 0));
           continue;
@@ -611,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
           if (move) ref = want;
           l *= f;
           if (j > 0) {
-            ok = wait_warp(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
+            ok = wait_warp<0>(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
             fence_after_sync();
             const uint64_t ff = pair_of(f, f);
 #pragma unroll 1
@@ -662,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       if (x >= 0) next = item_of(a, x);
       bar_meet(1 + q4);
       l += shared_sum[half ^ 1][row];
-      ok = wait_warp(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
+      ok = wait_warp<0>(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
       fence_after_sync();
       const float inv = 1.f / l;
       const bool mend = *(volatile int*)&fix[r % kFixes] == r + 1;
