@@ -186,5 +186,19 @@ __device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int i) {
   if (s < 0 || s >= a.slots) return 0;
   return min(max(a.lens[s], 0), (int)min((long long)a.width << a.page_shift, (long long)INT_MAX));
 }
+// The page table that the shared prefix is read through: the first sequence's that
+// holds all of it (the first one's, where the batch is what it says), else the longest's.
+__device__ __forceinline__ const int* prefix_table(const DecodeAttnArgs& a) {
+  int best = 0, most = -1;
+  for (int i = 0; i < a.batch && most < a.shared; i++) {
+    const int len = seq_len(a, i);
+    if (len > most) {
+      most = len;
+      best = i;
+    }
+  }
+  const int s = a.seqs[best];
+  return a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width;
+}
 
 }  // namespace tfx

@@ -216,7 +216,7 @@ __device__ __forceinline__ int sees(const DecodeAttnArgs& a, const Item& it, int
 // the page of one block of 16 keys: four tiles' blocks at a time, and the next
 // four's are on their way.
 struct Pages {
-  const int* table;  // the shared prefix's: sequence 0's
+  const int* table;  // the shared prefix's
   int tile;          // first of the four
   int page, next;
 };
@@ -239,8 +239,7 @@ __device__ __forceinline__ void look_up(const DecodeAttnArgs& a, Pages& pg, int 
 }
 __device__ __forceinline__ Pages pages_of(const PromptArgs&) { return {}; }
 __device__ __forceinline__ Pages pages_of(const DecodeAttnArgs& a) {
-  const int s = a.seqs[0];
-  return {a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width, INT_MIN / 2, -1, -1};
+  return {prefix_table(a), INT_MIN / 2, -1, -1};
 }
 template <int D>
 __device__ __forceinline__ void copy_k(const PromptArgs& a, const Item& it, const Pages&, int j, int rank, uint32_t dst,

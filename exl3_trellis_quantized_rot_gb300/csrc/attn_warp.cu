@@ -106,7 +106,7 @@ struct Segment {
   bool prefix;
   int s0, s1;    // slices, from the sequence's first token
   int head;      // K/V head
-  int seq;       // of the batch; -1: the shared prefix, through the first one's table
+  int seq;       // of the batch; -1: the shared prefix
   int row0;      // first row of the tile: of the batch's rows (prefix) or of the group's heads
   int rows;
   long long group;  // number of the group in its list
@@ -137,7 +137,7 @@ __device__ __forceinline__ Segment segment_at(const DecodeAttnArgs& a, const Wal
   Segment g;
   g.prefix = x < w.pre_total;
   if (g.prefix) {
-    const int grp = (int)(x / w.sp), s = a.seqs[0];
+    const int grp = (int)(x / w.sp);
     g.group = grp;
     g.s0 = (int)(x % w.sp);
     g.s1 = (int)min((long long)w.sp, g.s0 + (end - x));
@@ -145,7 +145,7 @@ __device__ __forceinline__ Segment segment_at(const DecodeAttnArgs& a, const Wal
     g.seq = -1;
     g.row0 = grp % w.ptiles * 16;
     g.rows = min(16, a.batch * a.group - g.row0);
-    g.table = a.tables + (long long)(s >= 0 && s < a.slots ? s : 0) * a.width;
+    g.table = prefix_table(a);
   } else {
     const long long y = x - w.pre_total;
     const int hr = (int)(y / w.own), z = (int)(y % w.own);

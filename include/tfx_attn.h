@@ -118,9 +118,10 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * `layer`: for sequence s = seqs[i] (device), row i of q (heads_q*dim values,
  * ldq elements apart) attends to all tokens s holds, its newest included.
  * shared: the first `shared` tokens are the same in every sequence of the
- * batch (they come from one fork): they are read once, through the table of
- * seqs[0], for the whole batch; 0 where nothing is shared. A sequence shorter
- * than that attends to as many of them as its length says. A sequence that
+ * batch (they come from one fork): they are read once, through the table of the
+ * first sequence that holds them all, for the whole batch; 0 where nothing is
+ * shared. A sequence shorter than that attends to as many of them as its length
+ * says (what it does not hold of them must then be finite). A sequence that
  * holds no token, or a slot out of range, gives zeros. h->heads_kv, dim and act
  * are the cache's. Same arithmetic as tfx_attn_prompt, with partial results of
  * FP32 joined in a fixed order. */

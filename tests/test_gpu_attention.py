@@ -284,6 +284,22 @@ def test_decode_of_uneven_batches(shared):
     assert not out[4:].any()
 
 
+@pytest.mark.parametrize("copies", [1, 6])
+def test_decode_reads_the_prefix_through_a_sequence_that_holds_it(copies):
+    """The batch begins with an empty sequence, a slot out of range and a short one."""
+    c = make_cache([5, 9, 70, 33], 400, 16, 4, 256, F16)
+    c.lens[0], c.lens[1] = 0, 90
+    c.tables[0] = -1
+    c.tables[1, 6:] = -1
+    tfx.cache_reserve(c, 30, 24)
+    seqs = torch.tensor([0, 99, 1, 2, 3] * copies, dtype=torch.int32, device="cuda")
+    q = normal((len(seqs), 24, 256), F16, 9)
+    out = tfx.attn_decode(c, 0, q, seqs, shared=400)
+    keep = [i for i, s in enumerate(seqs.tolist()) if s != 99]
+    check_decode(out[keep], c, 0, q[keep], seqs[keep])
+    assert not out[1::5].any()
+
+
 def test_decode_shared_prefix_agrees_with_none():
     c = make_cache([100, 37, 1, 290] * 5, 2000, 16, 4, 256, BF16)
     tfx.cache_reserve(c, 20, 24)
