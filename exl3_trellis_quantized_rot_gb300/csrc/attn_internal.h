@@ -112,6 +112,10 @@ tfx_exl3_driver driver_hooks();
 bool driver_is_runtime();
 long long spin_limit();
 int multiprocessors();
+// Whether launches may carry the programmatic dependency (tfx_exl3_set_pdl: not
+// where it is off). Every attention and cache kernel waits for the launches before
+// it (griddepcontrol.wait) ahead of its first access to memory that they may use.
+bool dependent_launches();
 int launch_kernel(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t s, void* arg, bool pdl, int cluster);
 int opt_in_smem(const void* fn, size_t smem);
 int fail_with(int code, const char* fmt, ...);

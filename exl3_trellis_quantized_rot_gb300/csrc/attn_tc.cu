@@ -378,6 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   Pages pg = {};
   const int x0 = nth(a, 0);
   if ((warp == kKWarp || warp == kVWarp) && x0 >= 0) {
+    griddep_wait();
     pg = pages_of(a);
     look_up(a, pg, item_of(a, x0).first, lane);
   }
@@ -391,6 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   cluster_sync();
   fence_after_sync();
   const uint32_t tm = *(volatile uint32_t*)&tmem_slot;
+  griddep_wait();
   griddep_launch();  // what follows waits for this grid before it reads what it wrote
   // registers: 384 x 168 at launch; 256 x 208 + 128 x 80 = 63,488 of those 64,512 from here on
   if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -702,7 +704,8 @@ int launch_of(const A& a, cudaStream_t s) {
   const int rc = opt_in_smem(fn, Geom<D>::kSmem);
   if (rc) return rc;
   const int pairs = std::min(a.items, multiprocessors() / 2);
-  return launch_kernel(fn, dim3(2u * (unsigned)pairs), dim3(kThreads), Geom<D>::kSmem, s, const_cast<A*>(&a), false, 1);
+  return launch_kernel(fn, dim3(2u * (unsigned)pairs), dim3(kThreads), Geom<D>::kSmem, s, const_cast<A*>(&a),
+                       dependent_launches(), 1);
 }
 template <typename A>
 int launch_any(const A& a, int act, int dim, cudaStream_t s) {

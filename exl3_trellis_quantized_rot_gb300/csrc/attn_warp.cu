@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_cons
     starts[0] = 0;
   }
   // after the tensor-core kernel, this one starts where that leaves room: they
-  // share no memory that is written, and that one began after all that came before
+  // share no memory that is written, and that one lets this one start only when
+  // all that came before has ended
   if (!a.pre_splits) griddep_wait();
   // own slices before each sequence
   int carry = 0;
@@ -567,10 +568,10 @@ int decode_of(const DecodeAttnArgs& a, cudaStream_t s) {
   int rc = opt_in_smem(fn, warp_smem<D>());
   if (rc) return rc;
   rc = launch_kernel(fn, dim3((unsigned)(a.warps / kWarps)), dim3(kThreads), warp_smem<D>(), s,
-                     const_cast<DecodeAttnArgs*>(&a), a.pre_splits > 0, 1);
+                     const_cast<DecodeAttnArgs*>(&a), dependent_launches(), 1);
   if (rc) return rc;
   return launch_kernel((const void*)decode_join_kernel<T, D>, dim3((unsigned)(a.batch * a.heads_q)), dim3(kWarps * 32), 0,
-                       s, const_cast<DecodeAttnArgs*>(&a), true, 1);
+                       s, const_cast<DecodeAttnArgs*>(&a), dependent_launches(), 1);
 }
 
 }  // namespace

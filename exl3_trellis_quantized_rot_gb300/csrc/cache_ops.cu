@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kBookThreads) extend_kernel(const __grid_const
 // One CTA per token: its K row and its V row.
 __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ AppendArgs a) {
   griddep_wait();
+  griddep_launch();
   const int t = blockIdx.x;
   if (t >= *a.count) return;
   const int to = a.row_slot[t];
@@ -293,6 +294,7 @@ __global__ void __launch_bounds__(kBookThreads) compact_book_kernel(const __grid
 __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ BookArgs a) {
   __shared__ int len;
   griddep_wait();
+  griddep_launch();
   const int s = a.list0[blockIdx.x];
   if (s < 0 || s >= a.slots) {
     if (threadIdx.x == 0) atomicOr(&a.book[0], TFX_CACHE_BAD);
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ BookA
 // a fork's shared pages, or the renumbering after a compact.
 __global__ void __launch_bounds__(kCopyThreads) move_kernel(const __grid_constant__ MoveArgs a) {
   griddep_wait();
+  griddep_launch();
   const long long tid = (long long)blockIdx.x * kCopyThreads + threadIdx.x, nt = (long long)gridDim.x * kCopyThreads;
   if (a.tables == kTablesFork) {
     for (long long x = tid; x < (long long)a.n * a.width; x += nt) {
@@ -364,24 +367,26 @@ __global__ void __launch_bounds__(kCopyThreads) move_kernel(const __grid_constan
 }  // namespace
 
 int launch_extend(const BookArgs& a, cudaStream_t s) {
-  return launch_kernel((const void*)extend_kernel, dim3(1), dim3(kBookThreads), 0, s, const_cast<BookArgs*>(&a), false, 1);
+  return launch_kernel((const void*)extend_kernel, dim3(1), dim3(kBookThreads), 0, s, const_cast<BookArgs*>(&a),
+                       dependent_launches(), 1);
 }
 int launch_append(const AppendArgs& a, int rows, cudaStream_t s) {
   return launch_kernel((const void*)append_kernel, dim3((unsigned)rows), dim3(128), 0, s, const_cast<AppendArgs*>(&a),
-                       true, 1);
+                       dependent_launches(), 1);
 }
 int launch_free(const BookArgs& a, cudaStream_t s) {
-  return launch_kernel((const void*)free_kernel, dim3((unsigned)a.n), dim3(256), 0, s, const_cast<BookArgs*>(&a), false, 1);
+  return launch_kernel((const void*)free_kernel, dim3((unsigned)a.n), dim3(256), 0, s, const_cast<BookArgs*>(&a),
+                       dependent_launches(), 1);
 }
 int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStream_t s) {
   if (book) {
     const int rc = launch_kernel(compact ? (const void*)compact_book_kernel : (const void*)fork_book_kernel, dim3(1),
-                                 dim3(kBookThreads), 0, s, const_cast<BookArgs*>(book), false, 1);
+                                 dim3(kBookThreads), 0, s, const_cast<BookArgs*>(book), dependent_launches(), 1);
     if (rc) return rc;
   }
   const unsigned ctas = (unsigned)multiprocessors() * 8;  // eight CTAs of 256 threads fill an SM
   return launch_kernel((const void*)move_kernel, dim3(ctas), dim3(kCopyThreads), 0, s, const_cast<MoveArgs*>(&m),
-                       book != nullptr, 1);
+                       dependent_launches(), 1);
 }
 
 }  // namespace tfx

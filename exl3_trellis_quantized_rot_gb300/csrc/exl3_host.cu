@@ -1100,6 +1100,7 @@ tfx_exl3_driver driver_hooks() { return drv(); }
 bool driver_is_runtime() { return drv().alloc == rt_alloc; }
 long long spin_limit() { return g_spin.load(std::memory_order_relaxed); }
 int multiprocessors() { return sm_count(); }
+bool dependent_launches() { return g_pdl.load(std::memory_order_relaxed) != 0; }
 int launch_kernel(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t s, void* arg, bool pdl, int cluster) {
   return launch(fn, grid, block, smem, s, arg, pdl, cluster);
 }
