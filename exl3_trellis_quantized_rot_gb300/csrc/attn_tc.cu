@@ -72,6 +72,19 @@ struct Barriers {
   uint64_t o_empty;            // both CTAs have read an item's result
 };
 
+// Where a warp is in a ring of N barriers, and the parity it waits for there.
+template <int N>
+struct Turn {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 struct Ctx {
   Barriers* b;
   volatile int* abort_flag;
@@ -401,18 +414,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   if (warp == kKWarp) {
     // ---- copies: this CTA's 64 keys of K and its rows of Q; an item's first K
     // need not wait until the last one's Q has been read
-    int g = 0;
+    Turn<ST> t;
     bool ok = true;
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
-      for (int j = 0; ok && j < it.tiles; j++, g++) {
-        const int st = g % ST;
+      for (int j = 0; ok && j < it.tiles; j++) {
         look_up(a, pg, it.first + j, lane);
-        if (!(ok = wait_warp<30>(c, &bars.k_empty[st], ((g / ST) & 1) ^ 1))) break;
-        const uint32_t bar = lead(&bars.k_full[st]);
+        if (!(ok = wait_warp<30>(c, &bars.k_empty[t.i], t.parity ^ 1))) break;
+        const uint32_t bar = lead(&bars.k_full[t.i]);
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_k<D>(a, it, pg, j, (int)rank, sk + st * G::kKV, bar, lane);
+        copy_k<D>(a, it, pg, j, (int)rank, sk + t.i * G::kKV, bar, lane);
+        t.next();
         if (j > 0) continue;
         if (!(ok = wait_warp<30>(c, &bars.q_empty, (r & 1) ^ 1))) break;
         if (lane == 0) {
@@ -425,20 +438,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     }
   } else if (warp == kVWarp) {
     // ---- copies: its dim/2 columns of V
-    int g = 0, edges = 0;
+    Turn<ST> t;
+    int edges = 0;
     bool ok = true;
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
-      for (int j = 0; j < it.tiles; j++, g++) {
-        const int st = g % ST;
+      for (int j = 0; j < it.tiles; j++, t.next()) {
         look_up(a, pg, it.first + j, lane);
-        if (!(ok = wait_warp<30>(c, &bars.v_empty[st], ((g / ST) & 1) ^ 1))) break;
+        if (!(ok = wait_warp<30>(c, &bars.v_empty[t.i], t.parity ^ 1))) break;
         const bool edge = (it.first + j + 1) * kTileKeys > it.hidden;
-        const uint32_t bar = edge ? peer_addr(s_addr(&bars.v_edge[edges % kEdgeBars]), rank) : lead(&bars.v_full[st]);
+        const uint32_t bar = edge ? peer_addr(s_addr(&bars.v_edge[edges % kEdgeBars]), rank) : lead(&bars.v_full[t.i]);
         edges += edge;
         if (lane == 0) expect_tx_at(bar, G::kKV);
         __syncwarp();
-        copy_v<D>(a, it, pg, j, (int)rank, sv + st * G::kKV, bar, lane);
+        copy_v<D>(a, it, pg, j, (int)rank, sv + t.i * G::kKV, bar, lane);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -446,23 +459,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     if (rank == 0) {
       constexpr uint32_t is = idesc<T>(kTileKeys, false), ip = idesc<T>(D, true);
       constexpr uint64_t kmaj = operand_bits(16), vmaj = operand_bits(kTileKeys * 128);
-      int g = 0;
+      const uint64_t qd = operand(sq, kmaj), kd0 = operand(sk, kmaj), vd0 = operand(sv, vmaj);
+      Turn<ST> kt, vt;  // K and V stages
+      Turn<SB> st, pt;  // score buffers, of the scores and of the products with V
       bool ok = true;
-      auto scores = [&](int y, bool last) -> bool {
-        const int st = y % ST;
-        if (!wait_warp<10>(c, &bars.k_full[st], (y / ST) & 1)) return false;
+      auto scores = [&](bool last) -> bool {
+        if (!wait_warp<10>(c, &bars.k_full[kt.i], kt.parity)) return false;
         fence_after_sync();
-        const uint64_t qd = operand(sq, kmaj), kd = operand(sk + st * G::kKV, kmaj);
-        const uint32_t d = tm + D + (y % SB) * 128;
+        const uint64_t kd = kd0 + kt.i * (G::kKV >> 4);
+        const uint32_t d = tm + D + st.i * 128;
         if (elected()) {
 #pragma unroll
           for (int k = 0; k < D / 16; k++)
             mma2_ss(d, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), kd + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), is, k > 0);
-          commit2(&bars.s_full[y % SB]);
-          commit2(&bars.k_empty[st]);
+          commit2(&bars.s_full[st.i]);
+          commit2(&bars.k_empty[kt.i]);
           if (last) commit2(&bars.q_empty);
         }
         __syncwarp();
+        kt.next();
+        st.next();
         return true;
       };
       for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
@@ -470,37 +486,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         const int n = it.tiles, last_steps = (min(it.seen - (it.first + n - 1) * kTileKeys, kTileKeys) + 15) >> 4;
         if (!(ok = wait_warp<10>(c, &bars.q_full, r & 1))) break;
         int ahead = 0;  // scores of the item's tiles issued: up to SB - 1 more than the products with V
-        for (int j = 0; j < n; j++, g++) {
-          for (; ok && ahead < n && ahead < j + SB; ahead++) ok = scores(g - j + ahead, ahead + 1 == n);
-          if (!ok) break;
-          const int st = g % ST;
-          if (!(ok = wait_warp<10>(c, &bars.v_full[st], (g / ST) & 1) && wait_warp<10>(c, &bars.p_full[g % SB], (g / SB) & 1))) break;
+        for (int j = 0; j < n; j++) {
+          for (; ok && ahead < n && ahead < j + SB; ahead++) ok = scores(ahead + 1 == n);
+          if (!ok || !(ok = wait_warp<10>(c, &bars.p_full[pt.i], pt.parity) && wait_warp<10>(c, &bars.v_full[vt.i], vt.parity))) break;
           if (j == 0 && r > 0 && !(ok = wait_warp<10>(c, &bars.o_empty, (r - 1) & 1))) break;
           fence_after_sync();
-          const uint64_t vd = operand(sv + st * G::kKV, vmaj);
-          const uint32_t p = tm + D + (g % SB) * 128;
+          const uint64_t vd = vd0 + vt.i * (G::kKV >> 4);
+          const uint32_t p = tm + D + pt.i * 128;
           if (elected()) {
             const int steps = j + 1 < n ? kTileKeys / 16 : last_steps;
 #pragma unroll
             for (int k = 0; k < kTileKeys / 16; k++)
               if (k < steps) mma2_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
-            commit2(&bars.v_empty[st]);
-            commit2(&bars.pv_done[g % SB]);
+            commit2(&bars.v_empty[vt.i]);
+            commit2(&bars.pv_done[pt.i]);
           }
           __syncwarp();
+          vt.next();
+          pt.next();
         }
       }
     }
   } else if (warp >= kEdgeWarp) {
     // ---- V tiles with keys that some row must not see
-    int edges = 0, g = 0;
+    Turn<ST> t;
+    int edges = 0;
     bool ok = true;
     for (int r = 0, x; (x = nth(a, r)) >= 0; r++) {
       const Item it = item_of(a, x);
-      for (int j = 0; j < it.tiles; j++, g++) {
+      for (int j = 0; j < it.tiles; j++, t.next()) {
         const int key0 = (it.first + j) * kTileKeys;
         if (key0 + kTileKeys <= it.hidden) continue;
-        const int st = g % ST;
+        const int st = t.i;
         // after a timeout nothing is handed on: v_full may still be in an earlier
         // tile's phase, which takes that tile's two arrivals and no more
         ok = ok && wait_warp<300>(c, &bars.v_edge[edges % kEdgeBars], (edges / kEdgeBars) & 1);
@@ -559,7 +576,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     const uint32_t tw = tm + ((uint32_t)q4 << 21);
     const float cs = a.scale_log2;
     const int my_tok = row / a.per_tile, my_head = row % a.per_tile;
-    int g = 0;
+    Turn<SB> t, before;  // this tile's score buffer, and the one before it
+    int even = 0;
+    const uint32_t p_full = peer_addr(s_addr(&bars.p_full[0]), 0);
     bool ok = true;
     const int tok = (int)rank * a.tokens + my_tok;
     int x = x0;
@@ -572,20 +591,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       const bool some = !A::kFewRows || __any_sync(~0u, live);
       const int hi = live ? sees(a, it, tok) : INT_MAX;  // keys the row sees; a row that is no token's is not stored
       float ref = -INFINITY, l = 0.f;
-      float s[64];
-      auto scores_of = [&](int y) {  // asks for this warp's columns of a tile's scores
-        const uint32_t t = tw + D + (y % SB) * 128 + half * 64;
-        tmem_ld32(t, s);
-        tmem_ld32(t + 32, s + 32);
-      };
-      for (int j = 0; j < it.tiles; j++, g++) {
-        ok = wait_warp<0>(c, &bars.s_full[g % SB], (g / SB) & 1) && ok;
+      for (int j = 0; j < it.tiles; j++, before = t, t.next(), even ^= 1) {
+        ok = wait_warp<0>(c, &bars.s_full[t.i], t.parity) && ok;
         if (!some) {
-          if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.p_full[g % SB]), 0));
+          if (lane == 0 && ok) arrive_at(p_full + 8 * t.i);
           continue;
         }
         fence_after_sync();
-        scores_of(g);
+        const uint32_t buf = tw + D + t.i * 128;
+        float s[64];
+        tmem_ld32(buf + half * 64, s);
+        tmem_ld32(buf + half * 64 + 32, s + 32);
         tmem_wait_ld_();
         const int left = hi - (it.first + j) * kTileKeys - half * 64;
         if (__any_sync(~0u, left < 64)) {
@@ -602,16 +618,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
 #pragma unroll
         for (int k = 0; k < 4; k++) mx[k] = fmaxf(mx[k], s[60 + k]);
         const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        shared_max[g & 1][half][row] = mine;
+        shared_max[even][half][row] = mine;
         bar_meet(1 + q4);  // also: both warps hold their scores, whose columns the probabilities overwrite
-        const float want = fmaxf(mine, shared_max[g & 1][half ^ 1][row]) * cs - Exponent<T>::kShift;
+        const float want = fmaxf(mine, shared_max[even][half ^ 1][row]) * cs - Exponent<T>::kShift;
         const bool move = want > ref + kSlack;  // never for a row that sees nothing; always for its first keys
         if (__any_sync(~0u, move)) {
           const float f = move ? exp2_fast(ref - want) : 1.f;
           if (move) ref = want;
           l *= f;
           if (j > 0) {
-            ok = wait_warp<0>(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
+            ok = wait_warp<0>(c, &bars.pv_done[before.i], before.parity) && ok;
             fence_after_sync();
             const uint64_t ff = pair_of(f, f);
 #pragma unroll 1
@@ -634,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         const float off = ref == -INFINITY ? 0.f : -ref;
         const uint64_t c2 = pair_of(cs, cs), o2 = pair_of(off, off);
         uint64_t sum2[2] = {0, 0};
-        const uint32_t tp = tw + D + (g % SB) * 128 + half * 32;
+        const uint32_t tp = buf + half * 32;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           uint32_t p[16];
@@ -652,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         tmem_wait_st_();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.p_full[g % SB]), 0));
+        if (lane == 0 && ok) arrive_at(p_full + 8 * t.i);
         float y0, y1;
         parts_of(add2(sum2[0], sum2[1]), y0, y1);
         l += y0 + y1;
@@ -662,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       if (x >= 0) next = item_of(a, x);
       bar_meet(1 + q4);
       l += shared_sum[half ^ 1][row];
-      ok = wait_warp<0>(c, &bars.pv_done[(g - 1) % SB], ((g - 1) / SB) & 1) && ok;
+      ok = wait_warp<0>(c, &bars.pv_done[before.i], before.parity) && ok;
       fence_after_sync();
       const float inv = 1.f / l;
       const bool mend = *(volatile int*)&fix[r % kFixes] == r + 1;
