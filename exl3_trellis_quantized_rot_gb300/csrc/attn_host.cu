@@ -275,7 +275,9 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
   a.err = error_word();
   a.spin = tfx::spin_limit();
   if (!a.err) return fail_with(TFX_ECUDA, "no device error word");
-  const int tile = 2 * a.tokens, per_token_tile = a.heads_kv * (a.group / a.per_tile);
+  a.sub = a.group / a.per_tile;
+  a.hg = a.heads_kv * a.sub;
+  const int tile = 2 * a.tokens, per_token_tile = a.hg;
   for (int i = 0; i < n;) {
     struct Seq {
       int begin, len;
@@ -464,8 +466,11 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
     const int most = 2 * a.tokens, tiles = (batch + most - 1) / most;
     a.tokens = (batch + 2 * tiles - 1) / (2 * tiles);  // the sequences spread evenly over the tiles' CTAs
     a.pre_splits = prefix_splits(batch, h->heads_q, h->heads_kv, shared);
-    const int mt = (batch + 2 * a.tokens - 1) / (2 * a.tokens), box = c->page_size < 64 ? c->page_size : 64;
-    a.items = a.heads_kv * (a.group / a.per_tile) * mt * a.pre_splits;
+    a.sub = a.group / a.per_tile;
+    a.hg = a.heads_kv * a.sub;
+    a.mt = (batch + 2 * a.tokens - 1) / (2 * a.tokens);
+    a.items = a.hg * a.mt * a.pre_splits;
+    const int box = c->page_size < 64 ? c->page_size : 64;
     if ((rc = make_q_map(&a.qmap, q, c->act, c->dim, h->heads_q, batch, ldq, a.per_tile, a.tokens))) return rc;
     if ((rc = make_map(&a.kt, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), box, 1))) return rc;
     if ((rc = make_map(&a.vt, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), box, 1))) return rc;

@@ -26,6 +26,7 @@ struct PromptArgs {
   long long ldv, ldo;
   float scale_log2;  // scale * log2(e)
   int heads_kv, group, per_tile, tokens;
+  int sub, hg;  // tiles of a group's heads; of all heads
   int n, items;
   int* err;
   long long spin;
@@ -56,7 +57,8 @@ struct DecodeAttnArgs {
   float scale_log2;
   int heads_q, heads_kv, group, batch, shared;
   int page_size, page_shift, pages, slots, width;
-  int per_tile, tokens, pre_splits, items;  // tensor-core kernel
+  // tensor-core kernel: as above, and tiles of the batch's rows
+  int per_tile, tokens, sub, hg, mt, pre_splits, items;
   int warps;          // NW
   int own_rows;       // rows of an own slot: min(16, group)
   int2* runs;         // [prefix groups + own groups]: the first warp that has a part of a group, and how many have

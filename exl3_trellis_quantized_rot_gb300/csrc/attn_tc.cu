@@ -172,7 +172,7 @@ struct Item {
 };
 
 __device__ __forceinline__ Item item_of(const PromptArgs& a, int x) {
-  const int sub = a.group / a.per_tile, hg = a.heads_kv * sub, i = x / hg, h = x % hg;
+  const int i = x / a.hg, h = x - i * a.hg, sub = a.sub;
   int lo = 0, hi = a.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -195,15 +195,17 @@ __device__ __forceinline__ Item item_of(const PromptArgs& a, int x) {
 }
 
 __device__ __forceinline__ Item item_of(const DecodeAttnArgs& a, int x) {
-  const int sub = a.group / a.per_tile, hg = a.heads_kv * sub, h = x % hg, y = x / hg;
-  const int mt = (a.batch + 2 * a.tokens - 1) / (2 * a.tokens), all = (a.shared + kTileKeys - 1) / kTileKeys;
+  const int y = x / a.hg, h = x - y * a.hg, sub = a.sub;
+  const unsigned all = (unsigned)(a.shared + kTileKeys - 1) / kTileKeys, splits = (unsigned)a.pre_splits;
   Item it;
-  it.split = y / mt;
-  it.row0 = y % mt * 2 * a.tokens;
+  it.split = y / a.mt;
+  it.row0 = (y - it.split * a.mt) * 2 * a.tokens;
   it.end_row = a.batch;
   it.key_row = it.t0 = 0;
-  it.first = (int)((long long)all * it.split / a.pre_splits);
-  it.tiles = (int)((long long)all * (it.split + 1) / a.pre_splits) - it.first;
+  // the tiles evenly: the first all % splits shares have one more
+  const unsigned each = all / splits, more = all - each * splits, n = (unsigned)it.split;
+  it.first = (int)(each * n + min(n, more));
+  it.tiles = (int)(each + (n < more));
   it.seen = it.hidden = a.shared;
   it.kvh = h / sub;
   it.head0 = it.kvh * a.group + h % sub * a.per_tile;
@@ -250,9 +252,19 @@ __device__ __forceinline__ void look_up(const DecodeAttnArgs& a, Pages& pg, int 
   pg.tile = tile;
   pg.next = page_ahead(a, pg, tile + 4, lane);
 }
-__device__ __forceinline__ Pages pages_of(const PromptArgs&) { return {}; }
-__device__ __forceinline__ Pages pages_of(const DecodeAttnArgs& a) {
-  return {prefix_table(a), INT_MIN / 2, -1, -1};
+__device__ __forceinline__ void first_pages(const PromptArgs&, Pages&, int, int) {}
+__device__ __forceinline__ void first_pages(const DecodeAttnArgs& a, Pages& pg, int tile, int lane) {
+  // the first sequence's, asked for beside its length; another's if that says so
+  const int s = a.seqs[0];
+  pg.table = a.tables + (long long)((unsigned)s < (unsigned)a.slots ? s : 0) * a.width;
+  pg.page = page_ahead(a, pg, tile, lane);
+  pg.next = page_ahead(a, pg, tile + 4, lane);
+  if (seq_len(a, 0) < a.shared) {
+    pg.table = prefix_table(a);
+    pg.page = page_ahead(a, pg, tile, lane);
+    pg.next = page_ahead(a, pg, tile + 4, lane);
+  }
+  pg.tile = tile;
 }
 template <int D>
 __device__ __forceinline__ void copy_k(const PromptArgs& a, const Item& it, const Pages&, int j, int rank, uint32_t dst,
@@ -390,10 +402,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   // the first pages are looked up while the pair comes together
   Pages pg = {};
   const int x0 = nth(a, 0);
+  Item it0 = {};
+  if (x0 >= 0) it0 = item_of(a, x0);
   if ((warp == kKWarp || warp == kVWarp) && x0 >= 0) {
     griddep_wait();
-    pg = pages_of(a);
-    look_up(a, pg, item_of(a, x0).first, lane);
+    first_pages(a, pg, it0.first, lane);
   }
   // rows of Q that no copy writes
   for (int x = a.tokens * a.per_tile * 8 + threadIdx.x; x < 128 * 8; x += kThreads)
@@ -417,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     Turn<ST> t;
     bool ok = true;
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
-      const Item it = item_of(a, x);
+      const Item it = r ? item_of(a, x) : it0;
       for (int j = 0; ok && j < it.tiles; j++) {
         look_up(a, pg, it.first + j, lane);
         if (!(ok = wait_warp<30>(c, &bars.k_empty[t.i], t.parity ^ 1))) break;
@@ -442,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     int edges = 0;
     bool ok = true;
     for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
-      const Item it = item_of(a, x);
+      const Item it = r ? item_of(a, x) : it0;
       for (int j = 0; j < it.tiles; j++, t.next()) {
         look_up(a, pg, it.first + j, lane);
         if (!(ok = wait_warp<30>(c, &bars.v_empty[t.i], t.parity ^ 1))) break;
@@ -482,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         return true;
       };
       for (int r = 0, x; ok && (x = nth(a, r)) >= 0; r++) {
-        const Item it = item_of(a, x);
+        const Item it = r ? item_of(a, x) : it0;
         const int n = it.tiles, last_steps = (min(it.seen - (it.first + n - 1) * kTileKeys, kTileKeys) + 15) >> 4;
         if (!(ok = wait_warp<10>(c, &bars.q_full, r & 1))) break;
         int ahead = 0;  // scores of the item's tiles issued: up to SB - 1 more than the products with V
@@ -513,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     int edges = 0;
     bool ok = true;
     for (int r = 0, x; (x = nth(a, r)) >= 0; r++) {
-      const Item it = item_of(a, x);
+      const Item it = r ? item_of(a, x) : it0;
       for (int j = 0; j < it.tiles; j++, t.next()) {
         const int key0 = (it.first + j) * kTileKeys;
         if (key0 + kTileKeys <= it.hidden) continue;
@@ -582,8 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
     bool ok = true;
     const int tok = (int)rank * a.tokens + my_tok;
     int x = x0;
-    Item it, next = {};
-    if (x >= 0) it = item_of(a, x);
+    Item it = it0, next = {};
     for (int r = 0; x >= 0; r++, it = next) {
       const bool live = my_tok < a.tokens && it.row0 + tok < it.end_row;
       // A decode batch may leave whole warps without a row: they only hand on. (The

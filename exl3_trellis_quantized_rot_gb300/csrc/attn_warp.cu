@@ -480,61 +480,64 @@ __global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_cons
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_constant__ DecodeAttnArgs a) {
   constexpr int V = D / 32;  // values of a row per lane, as V/4 runs of 4
-  constexpr int kBatch = 4;  // partial results in flight a warp
+  constexpr int kBatch = 6;  // partial results in flight a warp
   __shared__ float so[kWarps][D];
   __shared__ float2 sml[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
-  const int i = blockIdx.x / a.heads_q, head = blockIdx.x % a.heads_q;
+  const int i = blockIdx.x / a.heads_q, head = blockIdx.x - i * a.heads_q;
   const int kvh = head / a.group, gh = head % a.group, r = i * a.group + gh;
   const int tiles = (a.group + 15) / 16, ptiles = (a.batch * a.group + 15) / 16;
   const int hr = kvh * tiles + gh / 16, grp = kvh * ptiles + r / 16;
   const bool pre = a.shared > 0 && !a.pre_splits;
+  const int len = seq_len(a, i);  // nothing since the launch before the last one writes lengths
+  griddep_wait();
   const int2 own = a.runs[(pre ? a.heads_kv * ptiles : 0) + hr * a.batch + i];
   const int2 first = pre ? a.runs[grp] : make_int2(0, 0);
-  const int len = seq_len(a, i);
   float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
   for (int c = 0; c < V; c++) o[c] = 0.f;
-  // rows row0, row0 + step, ... (count of them) of a list of partial results
-  auto take = [&](const float* po, const float2* pml, long long row0, long long step, int count) {
-    for (int z0 = warp; z0 < count; z0 += kWarps * kBatch) {
-      float2 ml[kBatch];
-      float4 x[kBatch][V / 4];
+  // the row's partial results: shares of the prefix, runs of the prefix, runs of its own tokens
+  const int shares = a.pre_splits, all = shares + first.y + own.y;
+  const long long pre0 = (long long)(first.x + grp) * 16 + r % 16;
+  const long long own0 = ((long long)own.x + (long long)hr * a.batch + i) * a.own_rows + gh % 16;
+  for (int z0 = warp; z0 < all; z0 += kWarps * kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch][V / 4];
 #pragma unroll
-      for (int k = 0; k < kBatch; k++) {
-        const int z = z0 + k * kWarps;
-        const long long row = row0 + step * (z < count ? z : z0);
-        ml[k] = z < count ? pml[row] : make_float2(-INFINITY, 0.f);
+    for (int k = 0; k < kBatch; k++) {
+      const int z = min(z0 + k * kWarps, all - 1), y = z - shares;
+      const bool mine = y >= first.y;
+      const long long row = y < 0    ? (long long)z * a.batch * a.heads_q + blockIdx.x
+                            : mine ? own0 + (long long)(y - first.y) * a.own_rows
+                                   : pre0 + y * 16;
+      ml[k] = (mine ? a.own_ml : a.pre_ml)[row];
+      const float* po = (mine ? a.own_o : a.pre_o) + row * D + lane * 4;
 #pragma unroll
-        for (int c = 0; c < V / 4; c++) x[k][c] = *reinterpret_cast<const float4*>(po + row * D + c * 128 + lane * 4);
-      }
-      float mn = m;
-#pragma unroll
-      for (int k = 0; k < kBatch; k++) mn = fmaxf(mn, ml[k].x);
-      const float ref = mn == -INFINITY ? 0.f : mn, f = exp2_fast(m - ref);
-      l *= f;
-#pragma unroll
-      for (int c = 0; c < V; c++) o[c] *= f;
-#pragma unroll
-      for (int k = 0; k < kBatch; k++) {
-        if (z0 + k * kWarps >= count) break;
-        const float g = exp2_fast(ml[k].x - ref);
-        l += ml[k].y * g;
-#pragma unroll
-        for (int c = 0; c < V / 4; c++) {
-          o[c * 4] += x[k][c].x * g;
-          o[c * 4 + 1] += x[k][c].y * g;
-          o[c * 4 + 2] += x[k][c].z * g;
-          o[c * 4 + 3] += x[k][c].w * g;
-        }
-      }
-      m = mn;
+      for (int c = 0; c < V / 4; c++) x[k][c] = *reinterpret_cast<const float4*>(po + c * 128);
+      if (z0 + k * kWarps >= all) ml[k] = make_float2(-INFINITY, 0.f);  // past the end: no weight
     }
-  };
-  take(a.pre_o, a.pre_ml, blockIdx.x, (long long)a.batch * a.heads_q, a.pre_splits);
-  take(a.pre_o, a.pre_ml, (long long)(first.x + grp) * 16 + r % 16, 16, first.y);
-  take(a.own_o, a.own_ml, ((long long)own.x + (long long)hr * a.batch + i) * a.own_rows + gh % 16, a.own_rows, own.y);
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; k++) mn = fmaxf(mn, ml[k].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, f = exp2_fast(m - ref);
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < V; c++) o[c] *= f;
+#pragma unroll
+    for (int k = 0; k < kBatch; k++) {
+      if (z0 + k * kWarps >= all) break;
+      const float g = exp2_fast(ml[k].x - ref);
+      l += ml[k].y * g;
+#pragma unroll
+      for (int c = 0; c < V / 4; c++) {
+        o[c * 4] += x[k][c].x * g;
+        o[c * 4 + 1] += x[k][c].y * g;
+        o[c * 4 + 2] += x[k][c].z * g;
+        o[c * 4 + 3] += x[k][c].w * g;
+      }
+    }
+    m = mn;
+  }
   griddep_launch();
 #pragma unroll
   for (int c = 0; c < V; c++) so[warp][(c >> 2) * 128 + lane * 4 + (c & 3)] = o[c];
