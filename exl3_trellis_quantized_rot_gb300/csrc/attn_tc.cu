@@ -346,12 +346,26 @@ __device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, i
 }
 template <typename T, int D>
 __device__ __forceinline__ void store_row(const DecodeAttnArgs& a, const Item& it, int tok, int head, int col, float* o,
-                                          float, bool live, bool, uint4*) {
-  if (!live) return;
-  float* po = a.pre_o + (((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head) * D + col;
+                                          float, bool live, bool, uint4* stage) {
+  // through shared memory, 16 rows at a time: eight lanes store a row's 128 bytes
+  float* po = live ? a.pre_o + (((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head) * D + col : nullptr;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < 8; k++)
-    *reinterpret_cast<float4*>(po + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+  for (int h = 0; h < 2; h++) {
+    if ((lane >> 4) == h)
+#pragma unroll
+      for (int k = 0; k < 8; k++)
+        stage[(lane & 15) * 8 + (k ^ (lane & 7))] = make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                                                               __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int r = k * 4 + (lane >> 3), p = lane & 7;
+      float* to = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(po), h * 16 + r));
+      if (to) *reinterpret_cast<uint4*>(to + p * 4) = stage[r * 8 + (p ^ (r & 7))];
+    }
+    __syncwarp();
+  }
 }
 __device__ __forceinline__ void store_sum(const PromptArgs&, const Item&, int, int, float, float) {}
 __device__ __forceinline__ void store_sum(const DecodeAttnArgs& a, const Item& it, int tok, int head, float ref, float l) {
