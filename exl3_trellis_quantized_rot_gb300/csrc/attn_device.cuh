@@ -91,6 +91,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Both CTAs come together, and nothing more: barriers are made visible by their own
+// fence, and a release here waits for every store under way (about 1,300 cycles
+// at a kernel's end, measured).
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // This CTA's shared address `a` in the CTA of the given rank.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
   uint32_t r;

@@ -306,66 +306,85 @@ __device__ __forceinline__ void copy_v(const DecodeAttnArgs& a, const Item& it, 
   }
 }
 
-// 32 columns of a row's result, from column `col` on: o is the accumulator's, inv = 1 / sum. All lanes call it.
-template <typename T, int D>
-__device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, int tok, int head, int col, float* o,
+// N columns of a row's result, from column `col` on: o is the accumulator's, inv = 1
+// / sum. All lanes call it. 32 columns at a time go through shared memory, so that
+// neighbouring lanes store neighbouring pieces of a row: as 16 bytes of 32 rows an
+// instruction they took longer.
+template <typename T, int D, int N>
+__device__ __forceinline__ void store_row(const PromptArgs& a, const Item& it, int tok, int head, int col, float (&o)[N],
                                           float inv, bool live, bool mend, uint4* stage) {
   if (mend && live) {  // values that were taken out of V: this row's own
     const T* v = reinterpret_cast<const T*>(a.vbase) + (long long)it.key_row * a.ldv + (long long)it.kvh * D + col;
     for (int key = it.hidden; key <= it.t0 + tok; key++) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(v + (long long)key * a.ldv);
 #pragma unroll
-      for (int k = 0; k < 16; k++) {
+      for (int k = 0; k < N / 2; k++) {
         const uint32_t x = w[k], m = not_finite<T>(x);
         if (m & 0x8000u) o[2 * k] += value_of<T>(x, 0);
         if (m & 0x80000000u) o[2 * k + 1] += value_of<T>(x, 1);
       }
     }
   }
-  // a row's 64 bytes, to be stored by four lanes: 8 rows an instruction instead of 32
-  uint4 w[4];
-#pragma unroll
-  for (int k = 0; k < 4; k++) {
-    w[k].x = pack2<T>(o[8 * k] * inv, o[8 * k + 1] * inv);
-    w[k].y = pack2<T>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-    w[k].z = pack2<T>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-    w[k].w = pack2<T>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
-  }
+  const int lane = threadIdx.x & 31, p = lane & 3;
   T* out = live ? reinterpret_cast<T*>(a.out) + (long long)(it.row0 + tok) * a.ldo + (long long)head * D + col : nullptr;
-  const int lane = threadIdx.x & 31;
+  T* to[4];  // the rows that this lane stores a piece of: four lanes a row's 64 bytes
 #pragma unroll
-  for (int k = 0; k < 4; k++) stage[lane * 4 + (k ^ ((lane >> 1) & 3))] = w[k];  // 8 lanes' pieces in 8 different columns of banks
-  __syncwarp();
+  for (int k = 0; k < 4; k++)
+    to[k] = reinterpret_cast<T*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(out), k * 8 + (lane >> 2)));
 #pragma unroll
-  for (int k = 0; k < 4; k++) {
-    const int r = k * 8 + (lane >> 2), p = lane & 3;
-    T* to = reinterpret_cast<T*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(out), r));
-    if (to) *reinterpret_cast<uint4*>(to + p * 8) = stage[r * 4 + (p ^ ((r >> 1) & 3))];
-  }
-  __syncwarp();
-}
-template <typename T, int D>
-__device__ __forceinline__ void store_row(const DecodeAttnArgs& a, const Item& it, int tok, int head, int col, float* o,
-                                          float, bool live, bool, uint4* stage) {
-  // through shared memory, 16 rows at a time: eight lanes store a row's 128 bytes
-  float* po = live ? a.pre_o + (((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head) * D + col : nullptr;
-  const int lane = threadIdx.x & 31;
+  for (int c = 0; c < N; c += 32) {
 #pragma unroll
-  for (int h = 0; h < 2; h++) {
-    if ((lane >> 4) == h)
-#pragma unroll
-      for (int k = 0; k < 8; k++)
-        stage[(lane & 15) * 8 + (k ^ (lane & 7))] = make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
-                                                               __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const int r = k * 4 + (lane >> 3), p = lane & 7;
-      float* to = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(po), h * 16 + r));
-      if (to) *reinterpret_cast<uint4*>(to + p * 4) = stage[r * 8 + (p ^ (r & 7))];
+    for (int k = 0; k < 4; k++) {  // 8 lanes' pieces in 8 different columns of banks
+      const float* x = o + c + 8 * k;
+      stage[lane * 4 + (k ^ ((lane >> 1) & 3))] = make_uint4(pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv),
+                                                             pack2<T>(x[4] * inv, x[5] * inv), pack2<T>(x[6] * inv, x[7] * inv));
     }
     __syncwarp();
+    uint4 w[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int r = k * 8 + (lane >> 2);
+      w[k] = stage[r * 4 + (p ^ ((r >> 1) & 3))];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+      if (to[k]) *reinterpret_cast<uint4*>(to[k] + c + p * 8) = w[k];
   }
+}
+// A share of the prefix: the sums as they are, 16 rows at a time, eight lanes a row's 128 bytes.
+template <typename T, int D, int N>
+__device__ __forceinline__ void store_row(const DecodeAttnArgs& a, const Item& it, int tok, int head, int col, float (&o)[N],
+                                          float, bool live, bool, uint4* stage) {
+  const int lane = threadIdx.x & 31, p = lane & 7;
+  float* po = live ? a.pre_o + (((long long)it.split * a.batch + it.row0 + tok) * a.heads_q + head) * D + col : nullptr;
+  float* to[8];
+#pragma unroll
+  for (int k = 0; k < 8; k++)
+    to[k] = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(po), k * 4 + (lane >> 3)));
+#pragma unroll
+  for (int c = 0; c < N; c += 32)
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      if ((lane >> 4) == h)
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const float* x = o + c + 4 * k;
+          stage[(lane & 15) * 8 + (k ^ (lane & 7))] =
+              make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        }
+      __syncwarp();
+      uint4 w[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const int r = k * 4 + (lane >> 3);
+        w[k] = stage[r * 8 + (p ^ (r & 7))];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        if (to[h * 4 + k]) *reinterpret_cast<uint4*>(to[h * 4 + k] + c + p * 4) = w[k];
+    }
 }
 __device__ __forceinline__ void store_sum(const PromptArgs&, const Item&, int, int, float, float) {}
 __device__ __forceinline__ void store_sum(const DecodeAttnArgs& a, const Item& it, int tok, int head, float ref, float l) {
@@ -429,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   fence_async_smem();
   fence_before_sync();
   __syncthreads();
-  cluster_sync();
+  pair_sync();
   fence_after_sync();
   const uint32_t tm = *(volatile uint32_t*)&tmem_slot;
   griddep_wait();
@@ -717,9 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       __syncwarp();
       // only where another item follows: see arrive_at
       if (lane == 0 && ok && x >= 0) arrive_at(peer_addr(s_addr(&bars.o_empty), 0));
-#pragma unroll
-      for (int i = 0; i < D / 2; i += 32)
-        store_row<T, D>(a, it, tok, it.head0 + my_head, half * (D / 2) + i, o + i, inv, live && ok, mend, stage[warp]);
+      store_row<T, D>(a, it, tok, it.head0 + my_head, half * (D / 2), o, inv, live && ok, mend, stage[warp]);
       __syncwarp();
       bar_meet(1 + q4);  // shared_sum may be written again
     }
@@ -733,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   }
   fence_before_sync();
   __syncthreads();
-  cluster_sync();
+  pair_sync();
   if (warp == kMmaWarp) {
     fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
