@@ -15,11 +15,19 @@
 // each byte of K and V is fetched from L2 once for 256 rows, and the two SMs'
 // shared memories deliver half of it each.
 //
-// Tensor memory (512 columns): O 0..dim-1, two score buffers of 128 columns
-// from 256 on. A buffer's first 64 columns take the probabilities (two 16-bit
-// values a column), the A operand of P V. Order of the MMAs, one issuing
-// thread: S0, [S1, P0 V0], [S2, P1 V1], ...: S(j+1) goes to the buffer whose
-// probabilities P(j-1) V(j-1) has read before it.
+// Tensor memory (512 columns): O in 0..dim-1, then B score buffers of 128 columns,
+// two at dim 256, three at 128. A buffer's first 64 columns take the probabilities
+// (two 16-bit values a column), the A operand of P V. Order of the MMAs, from one
+// warp: S0 .. S(B-1), P0 V0, SB, P1 V1, S(B+1), ...: S(j+B) goes to the buffer whose
+// probabilities P(j) V(j) has read before it.
+//
+// What bounds it (GB300): at dim 256 the tensor pipe, 2,063 cycles a tile of 256
+// rows x 128 keys against the MMAs' 2,048 (16,384 tokens of 24/4 heads: 1.8 ms,
+// 1,840 TFLOP/s). At dim 128 the softmax warps, about 1,425 cycles a tile against
+// 1,024: their exponentials take 800 (the unit's own rate allows 512), the rest is
+// the way from scores to maximum and back, which two warps of a scheduler walk
+// together. Tried there and slower: four warps of 32 columns a row, two warps
+// taking turns at whole tiles.
 //
 // Warps of a CTA: 0..7 softmax and results; 8 issues the MMAs (in the even CTA);
 // 9 asks for K and Q, 10 for V; 11 looks after V where a tile has keys that some
@@ -647,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         float s[64];
         tmem_ld32(buf + half * 64, s);
         tmem_ld32(buf + half * 64 + 32, s + 32);
-        tmem_wait_ld_();
+        tmem_loaded();
         const int left = hi - (it.first + j) * kTileKeys - half * 64;
         if (__any_sync(~0u, left < 64)) {
           asm volatile("");  // keeps this a branch: as 64 selects in every tile it took a third of the time
@@ -679,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
             for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
               float o[32];
               tmem_ld32(tw + i, o);
-              tmem_wait_ld_();
+              tmem_loaded();
               uint32_t u[32];
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
@@ -710,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
           }
           tmem_st16u(tp + h * 16, p);
         }
-        tmem_wait_st_();
+        tmem_stored();
         fence_before_sync();
         __syncwarp();
         if (lane == 0 && ok) arrive_at(p_full + 8 * t.i);
@@ -731,7 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
       float o[D / 2];
 #pragma unroll
       for (int i = 0; i < D / 2; i += 32) tmem_ld32(tw + half * (D / 2) + i, o + i);
-      tmem_wait_ld_();
+      tmem_loaded();
       fence_before_sync();
       __syncwarp();
       // only where another item follows: see arrive_at

