@@ -23,11 +23,14 @@
 //
 // What bounds it (GB300): at dim 256 the tensor pipe, 2,063 cycles a tile of 256
 // rows x 128 keys against the MMAs' 2,048 (16,384 tokens of 24/4 heads: 1.8 ms,
-// 1,840 TFLOP/s). At dim 128 the softmax warps, about 1,425 cycles a tile against
-// 1,024: their exponentials take 800 (the unit's own rate allows 512), the rest is
-// the way from scores to maximum and back, which two warps of a scheduler walk
-// together. Tried there and slower: four warps of 32 columns a row, two warps
-// taking turns at whole tiles.
+// 1,840 TFLOP/s). At dim 128 two chains of nearly one length: the softmax, about 1,425
+// cycles a tile (its exponentials take 800, where the unit's rate allows 512; the rest is
+// the way from scores to maximum and back, which two warps of a scheduler walk together),
+// and the MMAs, about 1,300 where their rate allows 1,024. With either one's work halved
+// the other still takes nearly the whole time. Tried there and slower: four warps of 32
+// columns a row, two warps taking turns at whole tiles, two sets of warps taking turns.
+// Between two items about 5,000 cycles at dim 256: the last product 900, the store of 64
+// KB beside the next item's copies 3,500, the first softmax 1,700.
 //
 // Warps of a CTA: 0..7 softmax and results; 8 issues the MMAs (in the even CTA);
 // 9 asks for K and Q, 10 for V; 11 looks after V where a tile has keys that some
