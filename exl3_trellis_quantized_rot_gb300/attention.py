@@ -58,6 +58,7 @@ def declare(L: C.CDLL) -> None:
 
 
 _act_of = {torch.float16: 0, torch.bfloat16: 1} if torch else {}  # TFX_F16, TFX_BF16
+_int32 = torch.int32 if torch else None
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if torch else None  # absent without CUDA
 
 
@@ -105,7 +106,7 @@ def _rows(name: str, t, heads: int, dim: int, dtype, device: int) -> tuple:
 
 def _ints(name: str, t, device: int) -> tuple:
     """(length, address) of a contiguous int32 vector; device -1 is the CPU."""
-    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
+    if t.dtype is not _int32 or t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 vector on {'the CPU' if device < 0 else f'CUDA device {device}'} is wanted")
     return t.numel(), t.data_ptr()
 
@@ -116,21 +117,30 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
     int32 tensor on the CPU, sequence i is rows offsets[i]:offsets[i+1].
     scale: 1/sqrt(dim) by default. Returns out (rows outside the sequences of
     an out that is made here are zero)."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q, k and v are (rows, heads, dim)")
-    _, hq, dim = q.shape
-    hkv, dtype, dev = k.shape[1], q.dtype, q.get_device()
-    T, ldq, pq = _rows("q", q, hq, dim, dtype, dev)
-    Tk, ldk, pk = _rows("k", k, hkv, dim, dtype, dev)
-    Tv, ldv, pv = _rows("v", v, hkv, dim, dtype, dev)
+    try:
+        (T, hq, dim), (Tk, hkv, dk), (Tv, hv, dv) = q.shape, k.shape, v.shape
+        (ldq, sq, eq), (ldk, sk, ek), (ldv, sv, ev) = q.stride(), k.stride(), v.stride()
+    except ValueError:
+        raise ValueError("q, k and v are (rows, heads, dim)") from None
+    dtype, dev = q.dtype, q.get_device()
+    # _rows' conditions all at once (short prompts wait for this code); what does not
+    # meet them is looked at one by one: refused with the reason, or odd strides of a
+    # dimension of one
+    if (dim == dk == dv == sq == sk == sv and hv == hkv and eq == ek == ev == 1 and T > 1 and Tk > 1 and Tv > 1
+            and k.dtype is dtype and v.dtype is dtype and k.get_device() == dev == v.get_device() and dev >= 0):
+        pq, pk, pv = q.data_ptr(), k.data_ptr(), v.data_ptr()
+    else:
+        T, ldq, pq = _rows("q", q, hq, dim, dtype, dev)
+        Tk, ldk, pk = _rows("k", k, hkv, dim, dtype, dev)
+        Tv, ldv, pv = _rows("v", v, hkv, dim, dtype, dev)
     n, po = _ints("offsets", offsets, -1)
     if n < 1:
         raise ValueError("offsets holds at least one value")
     first, last = C.c_int32.from_address(po).value, C.c_int32.from_address(po + 4 * (n - 1)).value
-    if last > min(T, Tk, Tv):
+    if last > T or last > Tk or last > Tv:
         raise ValueError(f"offsets end at {last}, past the rows of q, k or v")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty((T, hq, dim), dtype=dtype, device=q.device)
         ldo, pout = hq * dim, out.data_ptr()
         if first > 0 or last < T:
             out.zero_()
@@ -138,8 +148,9 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
         To, ldo, pout = _rows("out", out, hq, dim, dtype, dev)
         if To < last:
             raise ValueError(f"out has {To} rows, offsets end at {last}")
-    rc = _lib().tfx_attn_prompt(_heads(hq, hkv, dim, _act(dtype), scale), pq, ldq, pk, ldk, pv, ldv, po, n - 1, pout, ldo,
-                                _stream(stream, dev))
+    rc = (_pkg._lib or _pkg.lib()).tfx_attn_prompt(
+        _heads(hq, hkv, dim, _act(dtype), scale), pq, ldq, pk, ldk, pv, ldv, po, n - 1, pout, ldo,
+        _raw_stream(dev) if stream is None else _stream(stream, dev))
     if rc:
         _check(rc)
     return out
@@ -218,13 +229,28 @@ def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=Non
     """K and V (rows, kv_heads, dim) of one layer's new tokens, into the room that
     the last cache_extend made. seqs and offsets are that call's and may be left
     out: where each row goes was settled there."""
-    n, ldk, pk = _rows("k", k, c.heads_kv, c.dim, c.dtype, c.device)
-    m, ldv, pv = _rows("v", v, c.heads_kv, c.dim, c.dtype, c.device)
-    if n != m:
-        raise ValueError(f"{n} rows of k, {m} of v")
+    heads, dim, dtype, dev = c.heads_kv, c.dim, c.dtype, c.device
+    try:
+        (n, hk, dk), (m, hv, dv), (ldk, sk, ek), (ldv, sv, ev) = k.shape, v.shape, k.stride(), v.stride()
+    except ValueError:
+        raise ValueError(f"k and v are (rows, {heads}, {dim})") from None
+    # as in attn_prompt: _rows' conditions all at once
+    if (n == m and hk == hv == heads and dim == dk == dv == sk == sv and ek == ev == 1
+            and k.dtype is dtype and v.dtype is dtype and k.get_device() == dev == v.get_device() and dev >= 0):
+        if n <= 1:  # a single row's pitch is not used
+            ldk = ldv = heads * dim
+        pk, pv = k.data_ptr(), v.data_ptr()
+    else:
+        n, ldk, pk = _rows("k", k, heads, dim, dtype, dev)
+        m, ldv, pv = _rows("v", v, heads, dim, dtype, dev)
+        if n != m:
+            raise ValueError(f"{n} rows of k, {m} of v")
     if offsets is not None and seqs is not None and offsets.numel() != seqs.numel() + 1:
         raise ValueError(f"{offsets.numel()} offsets for {seqs.numel()} sequences")
-    _check(_lib().tfx_cache_append(c.ref, layer, pk, ldk, pv, ldv, n, _stream(stream, c.device)))
+    rc = (_pkg._lib or _pkg.lib()).tfx_cache_append(c.ref, layer, pk, ldk, pv, ldv, n,
+                                                    _raw_stream(dev) if stream is None else _stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def _pair(c: Cache, src, dst) -> tuple:
@@ -260,22 +286,30 @@ def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | N
     """Attention of one new token of each sequence seqs[i] over the cache's tokens
     (tfx_attn_decode). q: (batch, heads, dim); the first `shared` tokens, the same
     in all of them, are read once. Returns out."""
-    if q.dim() != 3:
-        raise ValueError("q is (batch, heads, dim)")
-    hq, dim, dev = q.shape[1], c.dim, c.device
-    b, ldq, pq = _rows("q", q, hq, dim, c.dtype, dev)
+    try:
+        (b, hq, dq), (ldq, sq, eq) = q.shape, q.stride()
+    except ValueError:
+        raise ValueError("q is (batch, heads, dim)") from None
+    dim, dtype, dev = c.dim, c.dtype, c.device
+    # as in attn_prompt: _rows' conditions all at once
+    if dim == dq == sq and eq == 1 and q.dtype is dtype and q.get_device() == dev and dev >= 0:
+        if b <= 1:
+            ldq = hq * dim
+        pq = q.data_ptr()
+    else:
+        b, ldq, pq = _rows("q", q, hq, dim, dtype, dev)
     n, ps = _ints("seqs", seqs, dev)
     if n != b:
         raise ValueError(f"{n} sequences for {b} rows of q")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty((b, hq, dim), dtype=dtype, device=q.device)
         ldo, po = hq * dim, out.data_ptr()
     else:
-        bo, ldo, po = _rows("out", out, hq, dim, c.dtype, dev)
+        bo, ldo, po = _rows("out", out, hq, dim, dtype, dev)
         if bo != b:
             raise ValueError(f"out has {bo} rows, q {b}")
-    rc = _lib().tfx_attn_decode(c.ref, layer, _heads(hq, c.heads_kv, dim, c.act, scale), pq, ldq, ps, b, shared, po, ldo,
-                                _stream(stream, dev))
+    rc = (_pkg._lib or _pkg.lib()).tfx_attn_decode(c.ref, layer, _heads(hq, c.heads_kv, dim, c.act, scale), pq, ldq, ps, b,
+                                                   shared, po, ldo, _raw_stream(dev) if stream is None else _stream(stream, dev))
     if rc:
         _check(rc)
     return out
