@@ -224,7 +224,8 @@ __device__ __forceinline__ bool attend(Rows<T, D>& R, Ring& rg, int s0, int s1, 
   }
   for (int s = s0; s < s1; s++) {
     const int st = rg.it % kStages;
-    if (!mbar_wait_bounded(rg.full + st, (rg.it / kStages) & 1, spin)) return false;
+    // the warp gives up together: what follows wants all its lanes
+    if (!__all_sync(~0u, mbar_wait_bounded(rg.full + st, (rg.it / kStages) & 1, spin))) return false;
     uint8_t* kb = rg.buf + st * Slice<D>::kStage;
     uint8_t* vb = kb + Slice<D>::kHalf;
     const int k0 = s * KS;

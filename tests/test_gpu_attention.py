@@ -372,3 +372,24 @@ def test_bounded_waits_report():
     assert tfx.attn_error() == 0
     assert torch.equal(tfx.attn_prompt(q, k, v, off), want[0])
     assert torch.equal(tfx.attn_decode(c, 0, qd, seqs, shared=640), want[1])
+
+
+@pytest.mark.parametrize("hq,hkv,dim,page,shared,lens", [(24, 4, 256, 16, 0, [700, 1, 333]), (8, 2, 128, 16, 200, [90, 2, 1500]),
+                                                         (2, 2, 256, 64, 3000, [40] * 8)])
+def test_bounded_waits_of_single_warps(hq, hkv, dim, page, shared, lens):
+    """Limits at which some lanes' polls succeed and others' do not: a warp gives up as a
+    whole, so a call either says that it gave up or is right, and the next call is right."""
+    c = make_cache(lens, shared, page, hkv, dim, F16)
+    tfx.cache_reserve(c, len(lens), hq)
+    q, seqs = normal((len(lens), hq, dim), F16, 4), torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    want = tfx.attn_decode(c, 0, q, seqs, shared=shared)
+    check_decode(want, c, 0, q, seqs)
+    for limit in (1, 300, 700, 1500, 3000):
+        tfx.set_spin_limit(limit)
+        try:
+            got = tfx.attn_decode(c, 0, q, seqs, shared=shared)
+            assert tfx.attn_error() == 1 or torch.equal(got, want)
+        finally:
+            tfx.set_spin_limit(0)
+        assert torch.equal(tfx.attn_decode(c, 0, q, seqs, shared=shared), want)
+        assert tfx.attn_error() == 0
