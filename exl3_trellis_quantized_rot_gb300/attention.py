@@ -23,8 +23,8 @@ CACHE_FULL, CACHE_BAD, CACHE_TABLE_FULL = 1, 2, 4
 MAX_BATCH = 4096
 
 ABI_SYMBOLS = ("tfx_attn_prompt", "tfx_attn_decode", "tfx_attn_debug_error", "tfx_cache_book_ints", "tfx_cache_reserve",
-               "tfx_cache_release", "tfx_cache_extend", "tfx_cache_append", "tfx_cache_fork", "tfx_cache_free",
-               "tfx_cache_compact", "tfx_cache_copy")
+               "tfx_cache_release", "tfx_cache_extend", "tfx_cache_append", "tfx_cache_append_listed", "tfx_cache_fork",
+               "tfx_cache_free", "tfx_cache_compact", "tfx_cache_copy")
 
 
 class HeadsStruct(C.Structure):
@@ -48,6 +48,7 @@ def declare(L: C.CDLL) -> None:
     L.tfx_cache_release.argtypes = [K]
     L.tfx_cache_extend.argtypes = [K, vp, vp, i, vp]
     L.tfx_cache_append.argtypes = [K, i, vp, l64, vp, l64, i, vp]
+    L.tfx_cache_append_listed.argtypes = [K, i, vp, l64, vp, l64, i, vp, vp, i, vp]
     L.tfx_cache_fork.argtypes = [K, vp, vp, i, vp]
     L.tfx_cache_free.argtypes = [K, vp, i, vp]
     L.tfx_cache_compact.argtypes = [K, vp]
@@ -227,8 +228,8 @@ def cache_extend(c: Cache, seqs, offsets, stream=None) -> None:
 
 def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=None) -> None:
     """K and V (rows, kv_heads, dim) of one layer's new tokens, into the room that
-    the last cache_extend made. seqs and offsets are that call's and may be left
-    out: where each row goes was settled there."""
+    cache_extend made. seqs and offsets (int32 vectors on the cache's device) are that
+    call's, or some entries of it; left out, the last cache_extend's."""
     heads, dim, dtype, dev = c.heads_kv, c.dim, c.dtype, c.device
     try:
         (n, hk, dk), (m, hv, dv), (ldk, sk, ek), (ldv, sv, ev) = k.shape, v.shape, k.stride(), v.stride()
@@ -245,10 +246,17 @@ def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=Non
         m, ldv, pv = _rows("v", v, heads, dim, dtype, dev)
         if n != m:
             raise ValueError(f"{n} rows of k, {m} of v")
-    if offsets is not None and seqs is not None and offsets.numel() != seqs.numel() + 1:
-        raise ValueError(f"{offsets.numel()} offsets for {seqs.numel()} sequences")
-    rc = (_pkg._lib or _pkg.lib()).tfx_cache_append(c.ref, layer, pk, ldk, pv, ldv, n,
-                                                    _raw_stream(dev) if stream is None else _stream(stream, dev))
+    on = _raw_stream(dev) if stream is None else _stream(stream, dev)
+    if seqs is None and offsets is None:
+        rc = (_pkg._lib or _pkg.lib()).tfx_cache_append(c.ref, layer, pk, ldk, pv, ldv, n, on)
+    elif seqs is None or offsets is None:
+        raise ValueError("seqs and offsets go together")
+    else:
+        ns, ps = _ints("seqs", seqs, dev)
+        no, po = _ints("offsets", offsets, dev)
+        if no != ns + 1:
+            raise ValueError(f"{no} offsets for {ns} sequences")
+        rc = (_pkg._lib or _pkg.lib()).tfx_cache_append_listed(c.ref, layer, pk, ldk, pv, ldv, n, ps, po, ns, on)
     if rc:
         _check(rc)
 

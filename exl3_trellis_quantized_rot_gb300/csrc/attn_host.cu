@@ -143,9 +143,11 @@ int* refs_of(const tfx_cache* c) { return lens_of(c) + c->slots; }
 int* tables_of(const tfx_cache* c) { return refs_of(c) + c->pages; }
 int64_t page_values(const tfx_cache* c) { return (int64_t)c->page_size * c->heads_kv * c->dim; }
 
-// Page-call scratch: four lists of `pages` ints, one of `slots`-or-`pages`
-// entries (a call lists at most that many), token slots, a counter.
+// Page-call scratch: a counter and the list length that an append uses, what
+// extends leave for the appends (a mark and a list entry of each slot), and five
+// lists of `slots`-or-`pages` entries (a call lists at most that many).
 int64_t list_cap(const tfx_cache* c) { return c->slots > c->pages ? c->slots : c->pages; }
+size_t page_scratch_ints(const tfx_cache* c) { return 4 + 4 * (size_t)c->slots + 1 + 5 * (size_t)list_cap(c); }
 
 tfx::BookArgs book_args(const tfx_cache* c, const int32_t* l0, const int32_t* l1, int n) {
   const CachePriv* pv = static_cast<const CachePriv*>(c->priv);
@@ -165,12 +167,15 @@ tfx::BookArgs book_args(const tfx_cache* c, const int32_t* l0, const int32_t* l1
   const int64_t cap = list_cap(c);
   int* p = pv->pages;
   a.count = p;
-  a.free_list = p + 4;
+  a.grown.n = p + 1;
+  a.grown.mark = reinterpret_cast<int2*>(p + 4);
+  a.grown.seqs = p + 4 + 2 * (int64_t)c->slots;
+  a.grown.offsets = a.grown.seqs + c->slots;
+  a.free_list = a.grown.offsets + c->slots + 1;
   a.move_src = a.free_list + cap;
   a.move_dst = a.move_src + cap;
   a.map = a.move_dst + cap;
   a.start = a.map + cap;
-  a.row_slot = a.start + cap;
   return a;
 }
 
@@ -318,8 +323,14 @@ int tfx_cache_reserve(tfx_cache* c, int max_batch, int heads_q, cudaStream_t str
     if (!pv) return fail_with(TFX_ECUDA, "no host memory");
     c->priv = pv;
   }
-  const size_t ints = 4 + 5 * (size_t)list_cap(c) + (size_t)c->pages * c->page_size;
-  if ((rc = grow(reinterpret_cast<void**>(&pv->pages), &pv->pages_bytes, ints * 4, stream))) return rc;
+  const size_t had = pv->pages_bytes;
+  if ((rc = grow(reinterpret_cast<void**>(&pv->pages), &pv->pages_bytes, page_scratch_ints(c) * 4, stream))) return rc;
+  if (pv->pages_bytes > had && tfx::driver_hooks().memset0(pv->pages, pv->pages_bytes, stream) != 0) {  // no slot has a mark
+    tfx::driver_hooks().free(pv->pages, stream);
+    pv->pages = nullptr;
+    pv->pages_bytes = 0;
+    return fail_with(TFX_ECUDA, "clearing %zu bytes failed", page_scratch_ints(c) * 4);
+  }
   const int b = max_batch > pv->max_batch ? max_batch : pv->max_batch, hq = heads_q > pv->heads_q ? heads_q : pv->heads_q;
   size_t part = 0;  // the most that a batch up to b takes (fewer sequences can mean more shares of the prefix)
   for (int i = 1; i <= b; i++) {
@@ -353,8 +364,8 @@ int tfx_cache_extend(tfx_cache* c, const int32_t* seqs, const int32_t* offsets, 
   return tfx::launch_extend(book_args(c, seqs, offsets, n), stream);
 }
 
-int tfx_cache_append(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
-                     cudaStream_t stream) {
+static int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
+                       const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream) {
   int rc = check_cache(c);
   if (rc) return rc;
   if (layer < 0 || layer >= c->layers) return fail_with(TFX_EINVAL, "layer %d of %d", layer, c->layers);
@@ -374,9 +385,30 @@ int tfx_cache_append(tfx_cache* c, int layer, const void* k, int64_t ldk, const 
   a.ldk = ldk / 8;
   a.ldv = ldv / 8;
   a.row = c->heads_kv * c->dim / 8;
-  a.row_slot = b.row_slot;
-  a.count = b.count;
+  a.seqs = seqs;
+  a.offsets = offsets;
+  a.n = n;
+  a.book = c->book;
+  a.table = b.tables;
+  a.slots = c->slots;
+  a.width = c->width;
+  a.pages = c->pages;
+  a.page_size = c->page_size;
+  a.grown = b.grown;
   return tfx::launch_append(a, rows, stream);
+}
+
+int tfx_cache_append(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
+                     cudaStream_t stream) {
+  return append_rows(c, layer, k, ldk, v, ldv, rows, nullptr, nullptr, 0, stream);
+}
+
+int tfx_cache_append_listed(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
+                            const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream) {
+  const int rc = check_list(c, n, seqs, offsets);
+  if (rc) return rc;
+  if (n > c->slots) return fail_with(TFX_EINVAL, "%d sequences, %d slots", n, c->slots);
+  return append_rows(c, layer, k, ldk, v, ldv, n ? rows : 0, seqs, offsets, n, stream);
 }
 
 int tfx_cache_fork(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {

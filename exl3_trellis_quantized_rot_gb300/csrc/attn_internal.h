@@ -70,15 +70,24 @@ struct DecodeAttnArgs {
   long long spin;
 };
 
+// What appends need to know of the extends before them. Only an extend writes it,
+// except that a slot which is freed, or becomes a fork, loses its mark.
+struct Grown {
+  int2* mark;    // of each slot: the position its last new tokens begin at, and how many they are; y 0: none, -1: refused
+  int* n;        // the last extend's lists
+  int* seqs;     // [slots]
+  int* offsets;  // [slots + 1]
+};
+
 // One-CTA book kernels of the page operations.
 struct BookArgs {
   int *book, *lens, *refs, *tables;
   const int *list0, *list1;  // seqs / sources; offsets / targets
   int n, slots, width, pages, page_size, row_cap;
-  // scratch: free pages in order; moves; where a page is after a compact; per
-  // list entry its length before the call (-1: left alone); token slot of each
-  // new row; moves or rows counted
-  int *free_list, *move_src, *move_dst, *map, *start, *row_slot, *count;
+  // scratch: free pages in order; moves; where a page is after a compact; the
+  // length that each fork takes over (-1: left alone); moves counted
+  int *free_list, *move_src, *move_dst, *map, *start, *count;
+  Grown grown;
 };
 
 struct AppendArgs {
@@ -86,7 +95,12 @@ struct AppendArgs {
   void *k, *v;         // the layer's pages
   long long ldk, ldv;  // 16-byte words
   int row;             // 16-byte words of a token's K (or V)
-  const int *row_slot, *count;
+  const int *seqs, *offsets;  // null: the last extend's, in `grown`
+  int n;
+  int* book;
+  const int* table;
+  int slots, width, pages, page_size;
+  Grown grown;
 };
 
 enum Tables { kTablesNone = 0, kTablesFork = 1, kTablesCompact = 2 };

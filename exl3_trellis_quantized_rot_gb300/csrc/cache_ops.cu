@@ -130,44 +130,61 @@ __global__ void __launch_bounds__(kBookThreads) extend_kernel(const __grid_const
         }
         a.lens[s] = old + add;
       }
-      a.start[i] = bad ? -1 : old;
+      // for the appends; a slot that asks for nothing keeps what it has
+      if (s >= 0 && s < a.slots && (bad || add)) a.grown.mark[s] = bad ? make_int2(0, -1) : make_int2(old, add);
+      a.grown.seqs[i] = s;
+      a.grown.offsets[i] = a.list1[i];
     }
     if (bad) atomicOr(&status, bad);
     carry += all;
   }
   __syncthreads();
-  // where each new row goes
-  const int rows = a.n ? max(0, min(a.list1[a.n], a.row_cap)) : 0;
-  for (int t = threadIdx.x; t < rows; t += kBookThreads) {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (a.list1[mid + 1] > t) hi = mid; else lo = mid + 1;
-    }
-    const int j = t - a.list1[lo], old = a.start[lo];
-    int to = -1;
-    if (old >= 0 && j >= 0) {
-      const int pos = old + j;
-      const int p = a.tables[(long long)a.list0[lo] * a.width + pos / a.page_size];
-      if (p >= 0 && p < a.pages) to = p * a.page_size + pos % a.page_size;
-    }
-    a.row_slot[t] = to;
-  }
   if (threadIdx.x == 0) {
-    *a.count = rows;
+    *a.grown.n = a.n;
+    a.grown.offsets[a.n] = a.n ? a.list1[a.n] : 0;
     if (status) a.book[0] |= status;
   }
   griddep_launch();
 }
 
-// One CTA per token: its K row and its V row.
+// The entry of a list of n > 0 (offsets not decreasing) that row t is of, by a warp:
+// 32 entries a step. Whether the row is in it at all is the caller's to look at.
+__device__ __forceinline__ int entry_of(const int* offsets, int n, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32, x = lane * step;
+    const int k = max(__popc(__ballot_sync(~0u, x < len && offsets[lo + x] <= t)) - 1, 0);
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  return lo;
+}
+
+// One CTA per token: its K row and its V row. Where they go follows from the lists,
+// the marks that extends left and the tables as they are now, so that other calls may come
+// between an extend and its appends.
 __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ AppendArgs a) {
   griddep_wait();
   griddep_launch();
   const int t = blockIdx.x;
-  if (t >= *a.count) return;
-  const int to = a.row_slot[t];
-  if (to < 0) return;
+  const int n = a.seqs ? a.n : *a.grown.n;
+  const int* offsets = a.seqs ? a.offsets : a.grown.offsets;
+  if (n < 1) return;
+  const int i = entry_of(offsets, n, t);
+  const int begin = offsets[i], end = offsets[i + 1], s = (a.seqs ? a.seqs : a.grown.seqs)[i];
+  if (t < begin || t >= end) return;
+  const int2 mark = (unsigned)s < (unsigned)a.slots ? a.grown.mark[s] : make_int2(0, 0);
+  if (mark.y < 0) return;  // refused by its extend, which said so
+  int page = -1;
+  const int pos = mark.x + (t - begin);
+  if (mark.y == end - begin && pos / a.page_size < a.width)
+    page = a.table[(long long)s * a.width + pos / a.page_size];
+  if (page < 0 || page >= a.pages) {
+    if (threadIdx.x == 0) atomicOr(&a.book[0], TFX_CACHE_BAD);
+    return;
+  }
+  const int to = page * a.page_size + pos % a.page_size;
   const uint4* ks = reinterpret_cast<const uint4*>(a.k_new) + (long long)t * a.ldk;
   const uint4* vs = reinterpret_cast<const uint4*>(a.v_new) + (long long)t * a.ldv;
   uint4* kd = reinterpret_cast<uint4*>(a.k) + (long long)to * a.row;
@@ -228,6 +245,7 @@ __global__ void __launch_bounds__(kBookThreads) fork_book_kernel(const __grid_co
           if (from < 0 || from >= a.pages) from = -1;
         }
         a.lens[d] = len;
+        a.grown.mark[d] = make_int2(0, 0);
       }
       a.move_src[i] = from;
       a.move_dst[i] = to;
@@ -300,7 +318,10 @@ __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ BookA
     if (threadIdx.x == 0) atomicOr(&a.book[0], TFX_CACHE_BAD);
     return;
   }
-  if (threadIdx.x == 0) len = atomicExch(&a.lens[s], 0);
+  if (threadIdx.x == 0) {
+    len = atomicExch(&a.lens[s], 0);
+    a.grown.mark[s] = make_int2(0, 0);
+  }
   __syncthreads();
   int* row = a.tables + (long long)s * a.width;
   const int n = (int)min((long long)a.width, ((long long)len + a.page_size - 1) / a.page_size);

@@ -90,11 +90,21 @@ int tfx_cache_extend(tfx_cache* c, const int32_t* seqs, const int32_t* offsets, 
 
 /* The new tokens' K and V of one layer, after the extend that made room for
  * them: row t of k and v (heads_kv*dim values, ldk / ldv elements apart, both
- * multiples of 8) is the token that the last tfx_cache_extend's offsets give
+ * multiples of 8) is the token that the lists of the last tfx_cache_extend give
  * row t. Rows of sequences that extend left as they were, and rows past its last
- * offset, are not stored. */
+ * offset, are not stored. Other calls may come in between (a compact too); a row
+ * whose slot has since been freed, forked onto, or extended by another number of
+ * tokens is not stored and leaves TFX_CACHE_BAD. A fork copies the tokens of a
+ * partly filled page as they are: fork a sequence after its appends. */
 int tfx_cache_append(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
                      cudaStream_t stream);
+
+/* The same with lists of its own (device; n as in tfx_cache_extend): where
+ * several extends have made room, the lists of the one that these rows are for, or
+ * some of its entries. Row t of sequence seqs[i] is one of the tokens that the last
+ * extend of that sequence made room for, which must be offsets[i+1] - offsets[i]. */
+int tfx_cache_append_listed(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
+                            const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream);
 
 /* dst[i] becomes a copy of sequence src[i] (device lists; dst distinct, empty
  * slots that are in no src): full pages are shared, a last page that is partly

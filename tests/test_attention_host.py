@@ -156,3 +156,28 @@ def test_binding_refuses_wrong_tensors():
         tfx.Cache(torch.zeros(1, 2, 16, 2, 128), torch.zeros(1, 2, 16, 2, 128), 1, 1)
     with pytest.raises(ValueError, match="book"):
         tfx.Cache(k.view(1, 1, 4, 1, 256), k.view(1, 1, 4, 1, 256), 1, 1, book=torch.zeros(3, dtype=torch.int32))
+
+
+def test_append_with_lists_refusals(L, drv):
+    c = cache()
+    r = C.byref(c)
+    app = lambda layer=0, k=P, ldk=1024, rows=1, seqs=P, off=P, n=1: L.tfx_cache_append_listed(  # noqa: E731
+        r, layer, k, ldk, P, 1024, rows, seqs, off, n, None)
+    assert app() == tfx.ENOTRESERVED
+    assert L.tfx_cache_reserve(r, 2, 24, None) == 0
+    assert app(n=-1) == tfx.EINVAL and app(n=4) == tfx.EINVAL and app(seqs=None) == tfx.EINVAL and app(off=None) == tfx.EINVAL
+    assert app(layer=2) == tfx.EINVAL and app(rows=-1) == tfx.EINVAL and app(rows=161) == tfx.EINVAL
+    assert app(k=None) == tfx.EINVAL and app(ldk=1028) == tfx.EALIGN
+    n = tfx.launch_count()
+    assert app(rows=0) == 0 and app(n=0, seqs=None, off=None) == 0 and tfx.launch_count() == n
+    assert L.tfx_cache_release(r) == 0
+
+
+def test_a_reservation_that_cannot_clear_its_scratch_holds_nothing(L, drv):
+    drv.s.memset0 = tfx.MEMSET_FN(lambda p, n, s: -1)
+    tfx.set_driver(drv.s)
+    c = cache()
+    r = C.byref(c)
+    assert L.tfx_cache_reserve(r, 2, 24, None) == tfx.ECUDA and not drv.live
+    assert L.tfx_cache_extend(r, P, P, 1, None) == tfx.ENOTRESERVED
+    assert L.tfx_cache_release(r) == 0
