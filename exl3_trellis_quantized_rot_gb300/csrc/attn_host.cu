@@ -212,11 +212,19 @@ int prefix_splits(int batch, int heads_q, int heads_kv, int shared) {
   const int64_t fill = tfx::multiprocessors() / 2 / rest, tiles = (shared + 127) / 128;
   return (int)(fill < 1 ? 1 : fill > tiles ? tiles : fill);
 }
-int64_t prefix_rows(int batch, int heads_q, int heads_kv) {
-  return (int64_t)prefix_splits(batch, heads_q, heads_kv, INT32_MAX - 127) * batch * heads_q;
+// Rows of one K/V head from which on the shared prefix goes to the tensor cores: a
+// tile costs the same there for 1 row as for 256; from about two 16-row tiles on, the
+// warps' reading K and V again for each costs more.
+bool many_rows(int64_t batch, int64_t group) { return batch * group > 32; }
+// Partial results that the prefix's shares leave, at most: batch * heads_q times
+// the shares, which are one, or as many as give each pair of SMs an item of 256 rows.
+// It grows with both counts, as a reservation for more than is used must.
+int64_t prefix_rows(int64_t batch, int64_t heads_q, int64_t heads_kv) {
+  if (!many_rows(batch, heads_q / heads_kv)) return 0;
+  return std::max(batch * heads_q, (int64_t)tfx::multiprocessors() / 2 * 256);
 }
 
-// Decode scratch for `batch` sequences: byte offsets of its parts.
+// Decode scratch for `batch` sequences: byte offsets of its parts. No part shrinks with batch or heads.
 struct DecodeScratch {
   size_t runs, own_ml, pre_ml, own_o, pre_o, bytes;
 };
@@ -332,11 +340,7 @@ int tfx_cache_reserve(tfx_cache* c, int max_batch, int heads_q, cudaStream_t str
     return fail_with(TFX_ECUDA, "clearing %zu bytes failed", page_scratch_ints(c) * 4);
   }
   const int b = max_batch > pv->max_batch ? max_batch : pv->max_batch, hq = heads_q > pv->heads_q ? heads_q : pv->heads_q;
-  size_t part = 0;  // the most that a batch up to b takes (fewer sequences can mean more shares of the prefix)
-  for (int i = 1; i <= b; i++) {
-    const size_t bytes = decode_scratch(i, hq, c->heads_kv, c->dim, decode_warps()).bytes;
-    if (bytes > part) part = bytes;
-  }
+  const size_t part = decode_scratch(b, hq, c->heads_kv, c->dim, decode_warps()).bytes;
   if ((rc = grow(reinterpret_cast<void**>(&pv->part), &pv->part_bytes, part, stream))) return rc;
   pv->max_batch = b;
   pv->heads_q = hq;
@@ -490,9 +494,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.pages = c->pages;
   a.slots = c->slots;
   a.width = c->width;
-  // A tensor-core tile costs the same for 1 row as for 256; from about two 16-row
-  // tiles on, the warps' reading K and V again for each costs more.
-  if (batch * a.group > 32 && shared >= 256) {
+  if (many_rows(batch, a.group) && shared >= 256) {
     a.per_tile = heads_per_tile(a.group);
     a.tokens = 128 / a.per_tile;
     const int most = 2 * a.tokens, tiles = (batch + most - 1) / most;

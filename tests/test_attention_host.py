@@ -181,3 +181,20 @@ def test_a_reservation_that_cannot_clear_its_scratch_holds_nothing(L, drv):
     assert L.tfx_cache_reserve(r, 2, 24, None) == tfx.ECUDA and not drv.live
     assert L.tfx_cache_extend(r, P, P, 1, None) == tfx.ENOTRESERVED
     assert L.tfx_cache_release(r) == 0
+
+
+@pytest.mark.parametrize("hkv", [1, 4])
+def test_a_reservation_holds_for_fewer_heads_and_sequences(L, drv, hkv):
+    """What it takes does not shrink with batch or heads: a call within both finds its room."""
+    def taken(batch, group):
+        c = cache(heads_kv=hkv)
+        assert L.tfx_cache_reserve(C.byref(c), batch, group * hkv, None) == 0
+        n = sum(drv.live.values())
+        assert L.tfx_cache_release(C.byref(c)) == 0
+        return n
+
+    batches, groups = (1, 2, 5, 12, 14, 16, 21, 28, 32, 64, 200), (1, 2, 3, 4, 6, 8, 11, 16, 18, 20, 21, 24, 32, 64, 100, 128)
+    size = {(b, g): taken(b, g) for b in batches for g in groups}
+    for b in batches:
+        for g in groups:
+            assert all(size[x, y] <= size[b, g] for x in batches for y in groups if x <= b and y <= g), (b, g)

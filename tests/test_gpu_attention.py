@@ -393,3 +393,13 @@ def test_bounded_waits_of_single_warps(hq, hkv, dim, page, shared, lens):
             tfx.set_spin_limit(0)
         assert torch.equal(tfx.attn_decode(c, 0, q, seqs, shared=shared), want)
         assert tfx.attn_error() == 0
+
+
+def test_decode_with_fewer_heads_than_were_reserved():
+    """16 sequences of 16 heads take more shares of the prefix than 16 of 24."""
+    c = make_cache([5, 40] * 8, 3000, 64, 1, 128, F16)
+    tfx.cache_reserve(c, 16, 24)
+    seqs = torch.arange(16, dtype=torch.int32, device="cuda")
+    for hq, b in ((16, 16), (24, 16), (18, 14), (20, 12), (3, 16), (1, 1)):
+        q = normal((b, hq, 128), F16, hq)
+        check_decode(tfx.attn_decode(c, 0, q, seqs[:b], shared=3000), c, 0, q, seqs[:b])
