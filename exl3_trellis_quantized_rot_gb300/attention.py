@@ -83,6 +83,22 @@ def _stream(stream, device: int) -> int:
     return _raw_stream(device) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _made_on(stream, device: int, shape: tuple, dtype, clear: bool = False):
+    """A result for a call on a stream that the caller names: allocated, and cleared,
+    in that stream's order, and known to the current one, where it will be read."""
+    handle = _stream(stream, device)
+    if isinstance(stream, torch.cuda.Stream):
+        st = stream
+    elif handle == 0:  # ExternalStream takes 0 for a new stream
+        st = torch.cuda.default_stream(device)
+    else:
+        st = torch.cuda.ExternalStream(handle, device=device)
+    with torch.cuda.stream(st):
+        out = (torch.zeros if clear else torch.empty)(shape, dtype=dtype, device=f"cuda:{device}")
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def _act(dtype) -> int:
     act = _act_of.get(dtype)
     if act is None:
@@ -141,10 +157,14 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
     if last > T or last > Tk or last > Tv:
         raise ValueError(f"offsets end at {last}, past the rows of q, k or v")
     if out is None:
-        out = torch.empty((T, hq, dim), dtype=dtype, device=q.device)
+        clear = first > 0 or last < T
+        if stream is None:
+            out = torch.empty((T, hq, dim), dtype=dtype, device=q.device)
+            if clear:
+                out.zero_()
+        else:
+            out = _made_on(stream, dev, (T, hq, dim), dtype, clear)
         ldo, pout = hq * dim, out.data_ptr()
-        if first > 0 or last < T:
-            out.zero_()
     else:
         To, ldo, pout = _rows("out", out, hq, dim, dtype, dev)
         if To < last:
@@ -310,7 +330,8 @@ def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | N
     if n != b:
         raise ValueError(f"{n} sequences for {b} rows of q")
     if out is None:
-        out = torch.empty((b, hq, dim), dtype=dtype, device=q.device)
+        shape = b, hq, dim
+        out = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else _made_on(stream, dev, shape, dtype)
         ldo, po = hq * dim, out.data_ptr()
     else:
         bo, ldo, po = _rows("out", out, hq, dim, dtype, dev)

@@ -403,3 +403,31 @@ def test_decode_with_fewer_heads_than_were_reserved():
     for hq, b in ((16, 16), (24, 16), (18, 14), (20, 12), (3, 16), (1, 1)):
         q = normal((b, hq, 128), F16, hq)
         check_decode(tfx.attn_decode(c, 0, q, seqs[:b], shared=3000), c, 0, q, seqs[:b])
+
+
+@pytest.mark.parametrize("handle", [lambda st: st, lambda st: st.cuda_stream, lambda st: 0], ids=["stream", "handle", "default"])
+def test_results_made_for_another_stream(handle):
+    """The current stream is far behind: neither the zeros around late sequences nor what it
+    still does with memory that it gave back may land in the result."""
+    q, k, v = normal((300, 6, 256), F16, 1), normal((300, 1, 256), F16, 2), normal((300, 1, 256), F16, 3)
+    off = offsets_of([100, 90], 40)
+    c = make_cache([300, 2], 640, 32, 1, 256, F16)
+    tfx.cache_reserve(c, 300, 6)
+    qd, seqs = normal((300, 6, 256), F16, 4), torch.arange(300, dtype=torch.int32, device="cuda") % 2
+    want = tfx.attn_prompt(q, k, v, off), tfx.attn_decode(c, 0, qd, seqs, shared=640)
+    torch.cuda.synchronize()
+    here, st = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(here):
+        for call, w in ((lambda s: tfx.attn_prompt(q, k, v, off, stream=s), want[0]),
+                        (lambda s: tfx.attn_decode(c, 0, qd, seqs, shared=640, stream=s), want[1])):
+            given_back = torch.empty((300, 6, 256), dtype=F16, device="cuda")
+            torch.cuda._sleep(100_000_000)
+            given_back.fill_(7.0)
+            del given_back
+            out = call(handle(st))
+            st.synchronize()
+            here.synchronize()
+            torch.cuda.synchronize()
+            assert torch.equal(out, w)
+    assert not want[0][:40].any() and not want[0][230:].any()
+    check_prompt(want[0], q, k, v, off)
