@@ -60,7 +60,9 @@ def declare(L: C.CDLL) -> None:
 
 _act_of = {torch.float16: 0, torch.bfloat16: 1} if torch else {}  # TFX_F16, TFX_BF16
 _int32 = torch.int32 if torch else None
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if torch else None  # absent without CUDA
+# absent without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if torch else None
+_current_device = getattr(torch._C, "_cuda_getDevice", None) if torch else None
 
 
 def _lib():
@@ -79,7 +81,10 @@ def _check(rc: int) -> None:
 
 
 def _stream(stream, device: int) -> int:
-    """A stream's handle; by default torch's current one on the device."""
+    """A stream's handle; by default torch's current one on the device, which must be
+    the current device: that is where the library launches."""
+    if _current_device() != device:
+        raise ValueError(f"tensors on CUDA device {device}, the current one is {_current_device()}")
     return _raw_stream(device) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -171,7 +176,7 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
             raise ValueError(f"out has {To} rows, offsets end at {last}")
     rc = (_pkg._lib or _pkg.lib()).tfx_attn_prompt(
         _heads(hq, hkv, dim, _act(dtype), scale), pq, ldq, pk, ldk, pv, ldv, po, n - 1, pout, ldo,
-        _raw_stream(dev) if stream is None else _stream(stream, dev))
+        _stream(stream, dev))
     if rc:
         _check(rc)
     return out
@@ -266,7 +271,7 @@ def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=Non
         m, ldv, pv = _rows("v", v, heads, dim, dtype, dev)
         if n != m:
             raise ValueError(f"{n} rows of k, {m} of v")
-    on = _raw_stream(dev) if stream is None else _stream(stream, dev)
+    on = _stream(stream, dev)
     if seqs is None and offsets is None:
         rc = (_pkg._lib or _pkg.lib()).tfx_cache_append(c.ref, layer, pk, ldk, pv, ldv, n, on)
     elif seqs is None or offsets is None:
@@ -338,7 +343,7 @@ def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | N
         if bo != b:
             raise ValueError(f"out has {bo} rows, q {b}")
     rc = (_pkg._lib or _pkg.lib()).tfx_attn_decode(c.ref, layer, _heads(hq, c.heads_kv, dim, c.act, scale), pq, ldq, ps, b,
-                                                   shared, po, ldo, _raw_stream(dev) if stream is None else _stream(stream, dev))
+                                                   shared, po, ldo, _stream(stream, dev))
     if rc:
         _check(rc)
     return out
