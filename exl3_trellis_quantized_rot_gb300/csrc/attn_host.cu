@@ -8,6 +8,7 @@
 #include <new>
 
 #include "attn_internal.h"
+#include "per_device.h"
 
 namespace tfx {
 __device__ int g_attn_error = 0;  // device error word: a bounded wait gave up
@@ -29,12 +30,15 @@ struct CachePriv {
   int max_batch = 0, heads_q = 0;
 };
 
+// The current device's own.
 int* error_word() {
-  static int* p = []() -> int* {
+  static thread_local tfx::PerDevice<int*> words;
+  return words.of(tfx::current_device(), []() -> int* {
     void* q = nullptr;
-    return cudaGetSymbolAddress(&q, tfx::g_attn_error) == cudaSuccess ? static_cast<int*>(q) : nullptr;
-  }();
-  return p;
+    if (cudaGetSymbolAddress(&q, tfx::g_attn_error) == cudaSuccess) return static_cast<int*>(q);
+    cudaGetLastError();
+    return nullptr;
+  });
 }
 
 int check_heads(const tfx_attn_heads* h) {

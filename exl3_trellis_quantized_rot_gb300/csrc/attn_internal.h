@@ -128,6 +128,7 @@ tfx_exl3_driver driver_hooks();
 bool driver_is_runtime();
 long long spin_limit();
 int multiprocessors();
+int current_device();  // -1 where there is none
 // Whether launches may carry the programmatic dependency (tfx_exl3_set_pdl: not
 // where it is off). Every attention and cache kernel waits for the launches before
 // it (griddepcontrol.wait) ahead of its first access to memory that they may use.

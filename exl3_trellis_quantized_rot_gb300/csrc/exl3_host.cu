@@ -191,14 +191,18 @@ int validate(const tfx_exl3_weight* w) {
 }
 
 
+int current_dev() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) == cudaSuccess) return dev;
+  cudaGetLastError();
+  return -1;
+}
+
 // SMs of the current device (152 on GB300; also the answer when no device is visible).
 int sm_count() {
   static int cached[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return 152;
-  }
+  const int dev = current_dev();
+  if (dev < 0 || dev >= 64) return 152;
   if (!cached[dev]) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
@@ -1100,6 +1104,7 @@ tfx_exl3_driver driver_hooks() { return drv(); }
 bool driver_is_runtime() { return drv().alloc == rt_alloc; }
 long long spin_limit() { return g_spin.load(std::memory_order_relaxed); }
 int multiprocessors() { return sm_count(); }
+int current_device() { return current_dev(); }
 bool dependent_launches() { return g_pdl.load(std::memory_order_relaxed) != 0; }
 int launch_kernel(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t s, void* arg, bool pdl, int cluster) {
   return launch(fn, grid, block, smem, s, arg, pdl, cluster);
