@@ -16,6 +16,7 @@
 #include "attn_internal.h"
 #include "exl3_internal.h"
 #include "exl3_tc.cuh"
+#include "per_device.h"
 
 namespace tfx {
 KernelSet kernels_b1();
@@ -398,59 +399,41 @@ int tc_group(long long blocks, int rows, int C, int TK, long long S, bool spill)
   return best;
 }
 
-// Opt in to more than the default 48 KB of shared memory once per kernel and size.
+// Opt in to more than the default 48 KB of shared memory once per kernel, device and size.
 int set_smem(const void* fn, size_t smem) {
-  static thread_local const void* last_fn[16] = {};
-  static thread_local size_t last_sz[16] = {};
+  static thread_local tfx::KernelSettings<16> set;
   if (smem < 32 * 1024) return 0;
-  for (int i = 0; i < 16; i++)
-    if (last_fn[i] == fn && last_sz[i] >= smem) return 0;
+  const int dev = current_dev();
+  const long long* had = set.find(fn, dev);
+  if (had && (size_t)*had >= smem) return 0;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  static thread_local int next = 0;
-  last_fn[next] = fn;
-  last_sz[next] = smem;
-  next = (next + 1) % 16;
+  set.note(fn, dev, (long long)smem);
   return 0;
 }
 
 // Shared-memory carveout (percent of the maximum) for a kernel; the call is
-// skipped when the kernel already has that value.
+// skipped when the kernel already has that value on this device.
 int set_carveout(const void* fn, int pct) {
-  static thread_local const void* fns[32] = {};
-  static thread_local int vals[32] = {};
-  int slot = -1;
-  for (int i = 0; i < 32; i++) {
-    if (fns[i] == fn) {
-      if (vals[i] == pct) return 0;
-      slot = i;
-      break;
-    }
-    if (!fns[i] && slot < 0) slot = i;
-  }
+  static thread_local tfx::KernelSettings<32> set;
+  const int dev = current_dev();
+  const long long* had = set.find(fn, dev);
+  if (had && *had == pct) return 0;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, pct);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(carveout)");
-  if (slot >= 0) {
-    fns[slot] = fn;
-    vals[slot] = pct;
-  }
+  set.note(fn, dev, pct);
   return 0;
 }
 
-// Allow clusters above the portable 8 CTAs for a kernel, once per kernel.
+// Allow clusters above the portable 8 CTAs for a kernel, once per kernel and device.
 int allow_big_clusters(const void* fn) {
-  static thread_local const void* done[64] = {};
-  for (int i = 0; i < 64; i++) {
-    if (done[i] == fn) return 0;
-    if (!done[i]) {
-      cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(non-portable cluster size)");
-      done[i] = fn;
-      return 0;
-    }
-  }
+  static thread_local tfx::KernelSettings<64> set;
+  const int dev = current_dev();
+  if (set.find(fn, dev)) return 0;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e == cudaSuccess ? 0 : cuda_fail(e, "cudaFuncSetAttribute(non-portable cluster size)");
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(non-portable cluster size)");
+  set.note(fn, dev, 1);
+  return 0;
 }
 
 // cuTensorMapEncodeTiled from the driver the runtime loaded (no link to libcuda).

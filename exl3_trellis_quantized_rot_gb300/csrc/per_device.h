@@ -18,4 +18,29 @@ struct PerDevice {
   }
 };
 
+// The last N settings that were made for (kernel, device): an attribute set for a
+// kernel holds on the device that was current.
+template <int N>
+struct KernelSettings {
+  const void* fn[N] = {};
+  int device[N] = {};
+  long long value[N] = {};
+  int next = 0;
+  const long long* find(const void* f, int d) const {
+    for (int i = 0; i < N; i++)
+      if (fn[i] == f && device[i] == d) return &value[i];
+    return nullptr;
+  }
+  void note(const void* f, int d, long long v) {
+    int at = next;
+    if (const long long* p = find(f, d))
+      at = (int)(p - value);
+    else
+      next = (next + 1) % N;
+    fn[at] = f;
+    device[at] = d;
+    value[at] = v;
+  }
+};
+
 }  // namespace tfx

@@ -29,3 +29,19 @@ def test_each_device_has_its_own_value_and_a_failure_is_not_kept(tmp_path):
   assert(p.of(1, find(1)) == words + 1 && p.of(0, find(0)) == words && p.of(1, find(1)) == words + 1 && looked == 3);
   assert(p.of(-1, find(2)) == words + 2 && p.of(64, find(2)) == words + 2 && looked == 5);
 """)
+
+
+def test_a_kernel_setting_holds_on_its_device(tmp_path):
+    run(tmp_path, """
+  tfx::KernelSettings<3> s;
+  const char k[4] = {};
+  assert(!s.find(k, 0) && !s.find(nullptr, 0 + 1));
+  s.note(k, 0, 5);
+  assert(s.find(k, 0) && *s.find(k, 0) == 5 && !s.find(k, 1) && !s.find(k + 1, 0));
+  s.note(k, 1, 6);
+  s.note(k, 0, 7);  // a new value in the old one's place
+  s.note(k + 1, 0, 8);
+  assert(*s.find(k, 0) == 7 && *s.find(k, 1) == 6 && *s.find(k + 1, 0) == 8);
+  s.note(k + 2, 0, 9);  // no room: the oldest goes, and is set again when it is next used
+  assert(!s.find(k, 0) && *s.find(k, 1) == 6 && *s.find(k + 1, 0) == 8 && *s.find(k + 2, 0) == 9);
+""")
