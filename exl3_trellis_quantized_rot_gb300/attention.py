@@ -71,7 +71,8 @@ def _lib():
 
 @functools.lru_cache(maxsize=64)
 def _heads(hq: int, hkv: int, dim: int, act: int, scale):
-    """The C descriptor of a head layout (a model has a few); read-only once made."""
+    """The C descriptor of a head layout (a model has a few); read-only once made, so
+    scale is a float or None: a tensor would be told by its identity."""
     return C.byref(HeadsStruct(hq, hkv, dim, act, dim ** -0.5 if scale is None else scale))
 
 
@@ -155,6 +156,8 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
         T, ldq, pq = _rows("q", q, hq, dim, dtype, dev)
         Tk, ldk, pk = _rows("k", k, hkv, dim, dtype, dev)
         Tv, ldv, pv = _rows("v", v, hkv, dim, dtype, dev)
+    if scale is not None:
+        scale = float(scale)
     n, po = _ints("offsets", offsets, -1)
     if n < 1:
         raise ValueError("offsets holds at least one value")
@@ -331,6 +334,8 @@ def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | N
         pq = q.data_ptr()
     else:
         b, ldq, pq = _rows("q", q, hq, dim, dtype, dev)
+    if scale is not None:
+        scale = float(scale)
     n, ps = _ints("seqs", seqs, dev)
     if n != b:
         raise ValueError(f"{n} sequences for {b} rows of q")

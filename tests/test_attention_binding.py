@@ -101,3 +101,18 @@ def test_tensors_of_a_device_that_is_not_the_current_one(calls, name):
     with pytest.raises(ValueError, match="current"):
         entries(device=1)[name]()
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("name", ["attn_prompt", "attn_decode"])
+def test_a_scale_is_taken_by_its_value(calls, name):
+    """A tensor that holds the scale may hold another one at the next call."""
+    call, scale = entries()[name], torch.tensor(0.25)
+    taken = []
+    for value in (0.25, 0.5, 0.5):
+        scale.fill_(value)
+        call(scale=scale)
+        taken.append(next(a for a in calls[-1] if isinstance(a, tuple) and len(a) == 5)[4])
+    call(scale=2)
+    call()
+    taken += [next(a for a in c if isinstance(a, tuple) and len(a) == 5)[4] for c in calls[-2:]]
+    assert taken == [0.25, 0.5, 0.5, 2.0, 0.0625]
