@@ -21,6 +21,7 @@ _pkg = sys.modules[__package__]  # being imported when this runs: its functions 
 
 CACHE_FULL, CACHE_BAD, CACHE_TABLE_FULL = 1, 2, 4
 MAX_BATCH = 4096
+_TOP = 1 << 31
 
 ABI_SYMBOLS = ("tfx_attn_prompt", "tfx_attn_decode", "tfx_attn_debug_error", "tfx_cache_book_ints", "tfx_cache_reserve",
                "tfx_cache_release", "tfx_cache_extend", "tfx_cache_append", "tfx_cache_append_listed", "tfx_cache_fork",
@@ -87,6 +88,13 @@ def _stream(stream, device: int) -> int:
     if _current_device() != device:
         raise ValueError(f"tensors on CUDA device {device}, the current one is {_current_device()}")
     return _raw_stream(device) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _int32s(**numbers) -> None:
+    """Refuses numbers that a C int would take modulo 2^32."""
+    for name, n in numbers.items():
+        if not -_TOP <= n < _TOP:
+            raise ValueError(f"{name}={n} does not fit 32 bits")
 
 
 def _made_on(stream, device: int, shape: tuple, dtype, clear: bool = False):
@@ -238,6 +246,7 @@ class Cache:
 
 def cache_reserve(c: Cache, max_batch: int, heads: int, stream=None) -> None:
     """Scratch for attn_decode over up to max_batch sequences of `heads` query heads, and for the page calls."""
+    _int32s(max_batch=max_batch, heads=heads)
     _check(_lib().tfx_cache_reserve(c.ref, max_batch, heads, _stream(stream, c.device)))
 
 
@@ -258,6 +267,8 @@ def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=Non
     """K and V (rows, kv_heads, dim) of one layer's new tokens, into the room that
     cache_extend made. seqs and offsets (int32 vectors on the cache's device) are that
     call's, or some entries of it; left out, the last cache_extend's."""
+    if not -_TOP <= layer < _TOP:
+        _int32s(layer=layer)
     heads, dim, dtype, dev = c.heads_kv, c.dim, c.dtype, c.device
     try:
         (n, hk, dk), (m, hv, dv), (ldk, sk, ek), (ldv, sv, ev) = k.shape, v.shape, k.stride(), v.stride()
@@ -326,6 +337,8 @@ def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | N
         (b, hq, dq), (ldq, sq, eq) = q.shape, q.stride()
     except ValueError:
         raise ValueError("q is (batch, heads, dim)") from None
+    if not (-_TOP <= layer < _TOP and -_TOP <= shared < _TOP):
+        _int32s(layer=layer, shared=shared)
     dim, dtype, dev = c.dim, c.dtype, c.device
     # as in attn_prompt: _rows' conditions all at once
     if dim == dq == sq and eq == 1 and q.dtype is dtype and q.get_device() == dev and dev >= 0:

@@ -116,3 +116,16 @@ def test_a_scale_is_taken_by_its_value(calls, name):
     call()
     taken += [next(a for a in c if isinstance(a, tuple) and len(a) == 5)[4] for c in calls[-2:]]
     assert taken == [0.25, 0.5, 0.5, 2.0, 0.0625]
+
+
+@pytest.mark.parametrize("by", [2 ** 32, -2 ** 32, 2 ** 31])
+@pytest.mark.parametrize("name,what", [("attn_decode", dict(shared=5)), ("attn_decode", dict(layer=1)), ("cache_append", dict(layer=1)),
+                                       ("cache_append_listed", dict(layer=1)), ("cache_reserve", dict(b=5)),
+                                       ("cache_reserve", dict(h=24))])
+def test_numbers_past_32_bits_are_refused(calls, name, what, by):
+    """The C side would take what is left of them in 32 bits."""
+    call = entries()[name]
+    call(**what)
+    with pytest.raises(ValueError, match="32 bits"):
+        call(**{k: v + by for k, v in what.items()})
+    assert len(calls) == 1
