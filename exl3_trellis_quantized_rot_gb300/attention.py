@@ -12,11 +12,6 @@ import ctypes as C
 import functools
 import sys
 
-try:
-    import torch
-except ImportError:  # the package itself imports without it; the calls below take its tensors
-    torch = None
-
 _pkg = sys.modules[__package__]  # being imported when this runs: its functions are looked up at each call
 
 CACHE_FULL, CACHE_BAD, CACHE_TABLE_FULL = 1, 2, 4
@@ -59,11 +54,20 @@ def declare(L: C.CDLL) -> None:
     L.tfx_cache_book_ints.restype = l64
 
 
-_act_of = {torch.float16: 0, torch.bfloat16: 1} if torch else {}  # TFX_F16, TFX_BF16
-_int32 = torch.int32 if torch else None
-# absent without CUDA
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if torch else None
-_current_device = getattr(torch._C, "_cuda_getDevice", None) if torch else None
+# Set by _load: the package imports without torch; what takes its tensors brings it in.
+torch = _int32 = _raw_stream = _current_device = None
+_act_of: dict = {}
+
+
+def _load() -> None:
+    """Called where the first tensors arrive: by attn_prompt and by Cache, which every other call takes."""
+    global torch, _int32, _raw_stream, _current_device
+    import torch
+    _act_of.update({torch.float16: 0, torch.bfloat16: 1})  # TFX_F16, TFX_BF16
+    _int32 = torch.int32
+    # absent without CUDA
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _lib():
@@ -148,6 +152,8 @@ def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=N
     int32 tensor on the CPU, sequence i is rows offsets[i]:offsets[i+1].
     scale: 1/sqrt(dim) by default. Returns out (rows outside the sequences of
     an out that is made here are zero)."""
+    if torch is None:
+        _load()
     try:
         (T, hq, dim), (Tk, hkv, dk), (Tv, hv, dv) = q.shape, k.shape, v.shape
         (ldq, sq, eq), (ldk, sk, ek), (ldv, sv, ev) = q.stride(), k.stride(), v.stride()
@@ -202,6 +208,8 @@ class Cache:
     """
 
     def __init__(self, k, v, slots: int, width: int, book=None):
+        if torch is None:
+            _load()
         if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v are (layers, pages, page_size, kv_heads, dim), of one shape, type and device")
         if not k.is_contiguous() or not v.is_contiguous():

@@ -63,7 +63,9 @@ class Library:
 def calls(monkeypatch):
     L = Library()
     monkeypatch.setattr(tfx, "_lib", L)
-    monkeypatch.setattr(at, "_current_device", lambda: 0, raising=False)
+    if at.torch is None:
+        at._load()
+    monkeypatch.setattr(at, "_current_device", lambda: 0)
     return L.calls
 
 

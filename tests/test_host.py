@@ -335,3 +335,12 @@ def test_switches_are_safe_across_threads(L):
     assert set(seen) <= {0, 1, 2, 3}
     assert tfx.set_variant(9) in (0, 1, 2, 3)  # out of range: unchanged
     tfx.set_variant(old)
+
+
+def test_import_does_not_bring_in_torch():
+    """A program that passes raw pointers pays for the library alone."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = "import sys, exl3_trellis_quantized_rot_gb300 as t; t.lib(); assert t.attn_prompt; assert 'torch' not in sys.modules"
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
