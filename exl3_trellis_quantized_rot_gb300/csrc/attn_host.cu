@@ -19,6 +19,9 @@ namespace {
 using tfx::fail_with;
 
 constexpr int kRowTile = 16;  // rows of a warp
+// Tokens of one sequence: kernels round positions up to whole tiles and look up pages
+// of up to 1,008 tokens past the last, in 32 bits.
+constexpr int64_t kMostTokens = INT32_MAX - 2047;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -111,8 +114,10 @@ int check_cache(const tfx_cache* c) {
   if (c->dim != 128 && c->dim != 256) return fail_with(TFX_EUNSUPPORTED, "dim=%d (128 or 256)", c->dim);
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return fail_with(TFX_EUNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", c->page_size);
-  if ((int64_t)c->pages * c->page_size > INT32_MAX || (int64_t)c->width * c->page_size > INT32_MAX)
-    return fail_with(TFX_EUNSUPPORTED, "more than 2^31 tokens in the pool or a table");
+  if ((int64_t)c->pages * c->page_size > INT32_MAX || (int64_t)c->width * c->page_size > kMostTokens)
+    return fail_with(TFX_EUNSUPPORTED, "2^31 tokens or more in the pool, or above %lld in a table", (long long)kMostTokens);
+  // an extend adds up what a list of at most `slots` entries asks for
+  if ((int64_t)c->slots * c->width > INT32_MAX) return fail_with(TFX_EUNSUPPORTED, "2^31 table entries or more");
   if (!aligned16(c->k) || !aligned16(c->v)) return fail_with(TFX_EALIGN, "k or v is not 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(c->book) & 3u) return fail_with(TFX_EALIGN, "book is not 4-byte aligned");
   return 0;

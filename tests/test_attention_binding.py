@@ -131,3 +131,11 @@ def test_numbers_past_32_bits_are_refused(calls, name, what, by):
     with pytest.raises(ValueError, match="32 bits"):
         call(**{k: v + by for k, v in what.items()})
     assert len(calls) == 1
+
+
+def test_a_cache_in_host_memory_is_refused(calls):
+    """Its lists would be host tensors too, and the kernels would be given their addresses."""
+    k = torch.zeros(1, 2, 16, 1, 128, dtype=F16)
+    with pytest.raises(ValueError, match="CUDA"):
+        c = tfx.Cache(k, k.clone(), 1, 2)
+        tfx.cache_extend(c, torch.zeros(1, dtype=I32), torch.zeros(2, dtype=I32), stream=7)

@@ -198,3 +198,17 @@ def test_a_reservation_holds_for_fewer_heads_and_sequences(L, drv, hkv):
     for b in batches:
         for g in groups:
             assert all(size[x, y] <= size[b, g] for x in batches for y in groups if x <= b and y <= g), (b, g)
+
+
+@pytest.mark.parametrize("kw", [dict(width=(1 << 27) - 1), dict(width=(1 << 24) - 1, page_size=128), dict(width=(1 << 27) - 127),
+                                dict(slots=1 << 16, width=1 << 16), dict(slots=1 << 20, width=(1 << 11) + 1)])
+def test_sizes_whose_positions_or_entries_pass_32_bits(L, drv, kw):
+    """Kernels count tokens a sequence (and look a thousand ahead) and table entries in 32 bits."""
+    assert L.tfx_cache_reserve(C.byref(cache(**kw)), 1, 24, None) == tfx.EUNSUPPORTED and not drv.live
+
+
+@pytest.mark.parametrize("kw", [dict(width=(1 << 27) - 128), dict(slots=1 << 16, width=(1 << 15) - 1)])
+def test_the_largest_sizes(L, drv, kw):
+    c = cache(**kw)
+    assert L.tfx_cache_reserve(C.byref(c), 1, 24, None) == 0
+    assert L.tfx_cache_release(C.byref(c)) == 0
