@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kBookThreads) fork_book_kernel(const __grid_co
 }
 
 // Pages to the front: the moves, the counts, and where each page is afterwards.
+// A count below zero is a caller's mistake and a free page: there are as many holes as movers.
 __global__ void __launch_bounds__(kBookThreads) compact_book_kernel(const __grid_constant__ BookArgs a) {
   griddep_wait();
   int live = 0;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kBookThreads) compact_book_kernel(const __grid
     for (int j = 0; j < kPerThread; j++) {
       const int p = mine + j;
       r[j] = p < a.pages ? a.refs[p] : -1;
-      h += r[j] == 0 && p < used;
+      h += r[j] <= 0 && p < used;
       m += r[j] > 0 && p >= used;
     }
     int hall, mall;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kBookThreads) compact_book_kernel(const __grid
       const int p = mine + j;
       if (p >= a.pages) break;
       a.map[p] = p;
-      if (r[j] == 0 && p < used) a.move_dst[hat++] = p;
+      if (r[j] <= 0 && p < used) a.move_dst[hat++] = p;
       if (r[j] > 0 && p >= used) a.move_src[mat++] = p;
     }
     holes += hall;

@@ -165,3 +165,16 @@ def test_rows_that_an_extend_refused():
     tfx.cache_append(c, 0, k, v)
     m.put(0, k.cpu()[150:], v.cpu()[150:], [1], [0, 17])
     m.agrees(c)
+
+
+def test_compact_of_a_book_with_a_count_below_zero():
+    """A caller's broken count: the page is free, and one that is moved there brings its own."""
+    c, m = filled()
+    tfx.cache_free(c, dev([0, 1]))
+    m.free([0, 1])
+    assert m.refs[:10] == [0] * 8 + [1, 1]
+    c.refs[0] = -3
+    tfx.cache_compact(c)
+    m.compact()
+    assert m.head[1] == 2
+    m.agrees(c)
