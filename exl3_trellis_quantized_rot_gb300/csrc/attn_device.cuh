@@ -101,7 +101,8 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
 // made a warp wait about 1,100 cycles for everything it had stored (measured): what
 // they hand over is in tensor memory, or is read by the asynchronous proxy after
 // a proxy fence. Nothing orders such an arrival before the pair's closing
-// barrier, so none may be left that nobody waits for.
+// barrier, so none may be left that nobody waits for: the commits' arrivals (commit2)
+// too, which warp 11 sees out.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }

@@ -575,11 +575,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   } else if (warp >= kEdgeWarp) {
     // ---- V tiles with keys that some row must not see
     Turn<ST> t;
-    int edges = 0;
+    Turn<SB> pt;
+    int edges = 0, r = 0;
     bool ok = true;
-    for (int r = 0, x; (x = nth(a, r)) >= 0; r++) {
+    for (int x; (x = nth(a, r)) >= 0; r++) {
       const Item it = r ? item_of(a, x) : it0;
-      for (int j = 0; j < it.tiles; j++, t.next()) {
+      for (int j = 0; j < it.tiles; j++, t.next(), pt.next()) {
         const int key0 = (it.first + j) * kTileKeys;
         if (key0 + kTileKeys <= it.hidden) continue;
         const int st = t.i;
@@ -627,6 +628,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.v_full[st]), 0));
       }
     }
+    // The MMAs' last commits arrive in both CTAs, and nothing else waits for some of
+    // them (no copy is left; the softmax wants the last product's alone): none may still
+    // be on its way when a CTA leaves.
+    for (int i = 0; ok && i < ST; i++, t.next())
+      ok = wait_warp<100>(c, &bars.k_empty[t.i], t.parity ^ 1) && wait_warp<100>(c, &bars.v_empty[t.i], t.parity ^ 1);
+    for (int i = 0; ok && i < SB; i++, pt.next()) ok = wait_warp<100>(c, &bars.pv_done[pt.i], pt.parity ^ 1);
+    if (ok) wait_warp<100>(c, &bars.q_empty, (r & 1) ^ 1);
   } else {
     // ---- softmax: warps w and w + 4 share 32 rows (thread = row), and halve their
     // columns. A wait that gave up changes only what is handed on: the two warps
