@@ -431,3 +431,19 @@ def test_results_made_for_another_stream(handle):
             assert torch.equal(out, w)
     assert not want[0][:40].any() and not want[0][230:].any()
     check_prompt(want[0], q, k, v, off)
+
+
+@pytest.mark.parametrize("batch,shared,hq,hkv", [(129, 0, 2, 1), (300, 40, 2, 2), (300, 300, 6, 1), (4096, 0, 1, 1), (4096, 270, 2, 1)])
+def test_decode_of_large_batches(batch, shared, hq, hkv):
+    """More sequences than one round of the scan over them takes, up to the most that a call takes."""
+    lens = [(i * 37) % 61 + (i % 5 > 0) for i in range(batch)]
+    c = make_cache(lens, shared, 16, hkv, 128, F16, poison=float("nan"))
+    tfx.cache_reserve(c, batch, hq)
+    q = normal((batch, hq, 128), F16, 9, 1.5)
+    g = torch.Generator()
+    g.manual_seed(3)
+    seqs = torch.randperm(batch, generator=g).int().cuda()
+    out = tfx.attn_decode(c, 0, q, seqs, shared=shared)
+    some = list(range(0, batch, max(1, batch // 150))) + [127, 128, batch - 1]
+    check_decode(out[some], c, 0, q[some], seqs[some])
+    assert torch.isfinite(out).all()

@@ -1,4 +1,6 @@
 """Appends that do not directly follow their extend, against a model that keeps (slot, position) of every row."""
+import random
+
 import pytest
 import torch
 
@@ -29,7 +31,7 @@ class Rows(Model):
 def make(layers=2, pages=40, page=16, heads=2, dim=128, slots=12, width=9):
     k = torch.randn(layers, pages, page, heads, dim, device="cuda").half()
     c = tfx.Cache(k, torch.randn_like(k), slots, width)
-    tfx.cache_reserve(c, slots, heads)
+    tfx.cache_reserve(c, min(slots, 4096), heads)
     return c, Rows(c)
 
 
@@ -178,3 +180,49 @@ def test_compact_of_a_book_with_a_count_below_zero():
     m.compact()
     assert m.head[1] == 2
     m.agrees(c)
+
+
+def test_lists_of_more_than_one_round():
+    """Books are worked out 1024 entries at a time: growth, appends, forks and pages that run out in a later round."""
+    n = 2500
+    c, m = make(layers=1, pages=4200, page=16, heads=1, slots=2 * n, width=4)
+    seqs = list(range(n))
+    random.Random(1).shuffle(seqs)
+    off = [0]
+    for i in range(n):
+        off.append(off[-1] + (i * 7) % 20)
+    extend(c, m, seqs, off)
+    assert c.status() == 0
+    append(c, m, seqs, off, True, (0,))
+    append(c, m, seqs, off, False, (0,))
+    tfx.cache_fork(c, dev(seqs), dev([s + n for s in seqs]))
+    m.fork(seqs, [s + n for s in seqs])
+    m.agrees(c)
+    assert c.status() == tfx.CACHE_FULL and any(m.lens[n:]) and not all(m.lens[n:])
+    c.book[0] = m.head[0] = 0
+    gone = [s for s in range(2 * n) if s % 3]
+    tfx.cache_free(c, dev(gone))
+    m.free(gone)
+    tfx.cache_compact(c)
+    m.compact()
+    m.agrees(c)
+    step = list(range(0, 2 * n, 2))
+    extend(c, m, step, list(range(n + 1)))
+    m.agrees(c)
+    append(c, m, step, list(range(n + 1)), True, (0,))
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 700, 1024, 1025])
+def test_rows_find_their_entry(n):
+    """Lists with empty entries at their ends and in between."""
+    adds = [(0, 0, 3, 1, 0, 17)[(i * i) % 6] if n > 1 else 40 for i in range(n)]
+    off = [0]
+    for x in adds:
+        off.append(off[-1] + x)
+    c, m = make(layers=1, pages=2 * n + 3, heads=1, slots=n, width=3)
+    seqs = list(range(n))[::-1]
+    extend(c, m, seqs, off)
+    append(c, m, seqs, off, False, (0,))
+    append(c, m, seqs, off, True, (0,))
+    assert c.status() == 0
