@@ -4,7 +4,9 @@ and the steps in which each of them gets its next token.
 
     python examples/serve_attention.py
 
-Weights and activations are synthetic. ``Layer`` is the layer, ``serve`` the
+Weights and activations are synthetic, and q and k go to attention as the group gives
+them: a model that normalises or rotates them does so in between, before ``cache_append``.
+``Layer`` is the layer, ``serve`` the
 life of a small batch; it returns what each step computed.
 """
 from __future__ import annotations

@@ -263,7 +263,9 @@ def cache_release(c: Cache) -> None:
 
 
 def cache_extend(c: Cache, seqs, offsets, stream=None) -> None:
-    """Room for offsets[i+1] - offsets[i] new tokens of sequence seqs[i] (int32 vectors on the cache's device)."""
+    """Room for offsets[i+1] - offsets[i] new tokens of sequence seqs[i] (int32 vectors
+    on the cache's device). Behind one that finds too few pages, all that need any are
+    refused: put first what must not be."""
     n, ps = _ints("seqs", seqs, c.device)
     m, po = _ints("offsets", offsets, c.device)
     if m != n + 1:
@@ -340,7 +342,7 @@ def cache_copy(c: Cache, src, dst, stream=None) -> None:
 def attn_decode(c: Cache, layer: int, q, seqs, shared: int = 0, scale: float | None = None, out=None, stream=None):
     """Attention of one new token of each sequence seqs[i] over the cache's tokens
     (tfx_attn_decode). q: (batch, heads, dim); the first `shared` tokens, the same
-    in all of them, are read once. Returns out."""
+    in all of them, are read once where the batch has many rows. Returns out."""
     try:
         (b, hq, dq), (ldq, sq, eq) = q.shape, q.stride()
     except ValueError:

@@ -221,9 +221,15 @@ int prefix_splits(int batch, int heads_q, int heads_kv, int shared) {
   const int64_t fill = tfx::multiprocessors() / 2 / rest, tiles = (shared + 127) / 128;
   return (int)(fill < 1 ? 1 : fill > tiles ? tiles : fill);
 }
-// Rows of one K/V head from which on the shared prefix goes to the tensor cores: a
-// tile costs the same there for 1 row as for 256; from about two 16-row tiles on, the
-// warps' reading K and V again for each costs more.
+// Rows of one K/V head from which on the shared prefix goes to the tensor cores, where
+// it has 256 tokens or more: a tile costs the same there for 1 row as for 256, while the
+// warps read K and V again for every 16. Measured, a step on the tensor cores / by warps
+// (us; 24/4 heads of 256, 6 rows a sequence, 100 own tokens, pages of 64): prefix of
+// 65,536 and 2 sequences 55 / 63, 4: 56 / 99, 6: 57 / 89, 16: 59 / 232; of 8,192 and
+// 4: 20.5 / 20.3, 6: 21.0 / 21.5, 16: 21.9 / 29.3; of 1,024 and 6: 12.5 / 12.7, 16: 17.4 /
+// 12.7, 64: 23.5 / 23.5; of 256 and 64: 21.4 / 17.4. So the rule is right for many rows
+// or long prefixes, gives away 40 us with 17 to 32 rows of a very long one, and 5 us with
+// 96 rows of a short one.
 bool many_rows(int64_t batch, int64_t group) { return batch * group > 32; }
 // Partial results that the prefix's shares leave, at most: batch * heads_q times
 // the shares, which are one, or as many as give each pair of SMs an item of 256 rows.

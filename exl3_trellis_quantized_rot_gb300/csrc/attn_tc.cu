@@ -22,8 +22,8 @@
 // probabilities P(j) V(j) has read before it.
 //
 // What bounds it (GB300): at dim 256 the tensor pipe, 2,063 cycles a tile of 256
-// rows x 128 keys against the MMAs' 2,048 (16,384 tokens of 24/4 heads: 1.8 ms,
-// 1,840 TFLOP/s). At dim 128 two chains of nearly one length: the softmax, about 1,425
+// rows x 128 keys against the MMAs' 2,048 (16,384 tokens of 24/4 heads: 1.82 ms on the
+// GPU, 1.88 as a call among others, 1,810 and 1,755 TFLOP/s). At dim 128 two chains of nearly one length: the softmax, about 1,425
 // cycles a tile (its exponentials take 800, where the unit's rate allows 512; the rest is
 // the way from scores to maximum and back, which two warps of a scheduler walk together),
 // and the MMAs, about 1,300 where their rate allows 1,024. With either one's work halved

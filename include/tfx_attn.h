@@ -87,7 +87,10 @@ int tfx_cache_release(tfx_cache* c);
 /* Room for new tokens: sequence seqs[i] (device, distinct slots) grows by
  * offsets[i+1] - offsets[i] tokens (device, n+1 values from 0 up). New pages
  * are the free ones of lowest number, in the order of the list. A sequence
- * that finds too few, or whose table is full, keeps its length. */
+ * that finds too few, or whose table is full, keeps its length. Pages are counted
+ * down the list as they are asked for: behind a sequence that finds too few, every
+ * one that needs a page finds none either (TFX_CACHE_FULL), however few it needs. A
+ * caller puts what must not be refused first. */
 int tfx_cache_extend(tfx_cache* c, const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream);
 
 /* The new tokens' K and V of one layer, after the extend that made room for
@@ -130,11 +133,12 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * `layer`: for sequence s = seqs[i] (device), row i of q (heads_q*dim values,
  * ldq elements apart) attends to all tokens s holds, its newest included.
  * shared: the first `shared` tokens are the same in every sequence of the
- * batch (they come from one fork): they are read once, through the table of the
- * first sequence that holds them all, for the whole batch; 0 where nothing is
- * shared. A sequence shorter than that attends to as many of them as its length
- * says (what it does not hold of them must then be finite). A sequence that
- * holds no token, or a slot out of range, gives zeros. h->heads_kv, dim and act
+ * batch (they come from one fork): they are read through the table of the
+ * first sequence that holds them all, once for every 256 rows of a K/V head (batch *
+ * heads_q/heads_kv) where it has more than 32 and there are 256 such tokens or more,
+ * else once for every 16 rows; 0 where nothing is shared. A sequence shorter than
+ * that attends to as many of them as its length says (what it does not hold of
+ * them must then be finite). A sequence that holds no token, or a slot out of range, gives zeros. h->heads_kv, dim and act
  * are the cache's. Same arithmetic as tfx_attn_prompt, with partial results of
  * FP32 joined in a fixed order. */
 int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void* q, int64_t ldq, const int32_t* seqs,
