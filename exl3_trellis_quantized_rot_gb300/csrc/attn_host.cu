@@ -478,6 +478,10 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
     return fail_with(TFX_EINVAL, "shared=%d outside 0..%d", shared, c->width * c->page_size);
   if ((rc = check_reserved(c))) return rc;
   const CachePriv* pv = static_cast<const CachePriv*>(c->priv);
+  // the kernel numbers the slices of the batch's own tokens, 4,096 / dim each, in 32 bits
+  const int64_t slices = ((int64_t)c->width * c->page_size) / (4096 / c->dim) + 1;
+  if (batch * slices > INT32_MAX)
+    return fail_with(TFX_EUNSUPPORTED, "batch=%d sequences of up to %lld tokens", batch, (long long)c->width * c->page_size);
   if (batch > pv->max_batch || h->heads_q > pv->heads_q)
     return fail_with(TFX_ENOTRESERVED, "reserved for %d sequences of %d heads, called with %d of %d", pv->max_batch,
                      pv->heads_q, batch, h->heads_q);

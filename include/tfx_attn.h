@@ -49,7 +49,8 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
  * k, v  : [layers][pages][page_size][heads_kv][dim] in act, 16-byte aligned;
  *         page_size 16, 32, 64 or 128; dim 128 or 256.
  *         pages * page_size and slots * width below 2^31, width * page_size at
- *         most 2^31 - 2048 (TFX_EUNSUPPORTED otherwise).
+ *         most 2^31 - 2048, and that times the batch of a decode call below
+ *         2^31 * 4096 / dim (TFX_EUNSUPPORTED otherwise).
  * book  : int32[tfx_cache_book_ints()], device:
  *           [0] status bits, kept until the caller clears them (TFX_CACHE_*);
  *           [1] pages moved by the last compact; [2], [3] unused;

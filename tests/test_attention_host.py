@@ -212,3 +212,14 @@ def test_the_largest_sizes(L, drv, kw):
     c = cache(**kw)
     assert L.tfx_cache_reserve(C.byref(c), 1, 24, None) == 0
     assert L.tfx_cache_release(C.byref(c)) == 0
+
+
+def test_decode_of_more_slices_than_are_counted_in_32_bits(L, drv):
+    """A step's own tokens are numbered through in slices of 16 (dim 256) or 32 keys."""
+    c = cache(width=1 << 22, page_size=128, slots=128)  # 2^29 tokens a sequence
+    r = C.byref(c)
+    assert L.tfx_cache_reserve(r, 128, 24, None) == 0
+    dec = lambda batch, hh: L.tfx_attn_decode(r, 0, C.byref(hh), P, 6144, P, batch, 0, P, 6144, None)  # noqa: E731
+    assert dec(64, heads()) == tfx.EUNSUPPORTED and dec(128, heads()) == tfx.EUNSUPPORTED
+    assert dec(63, heads()) != tfx.EUNSUPPORTED
+    assert L.tfx_cache_release(r) == 0
