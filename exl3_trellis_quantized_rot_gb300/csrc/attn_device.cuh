@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t a, uint32_t rank) {
 // they hand over is in tensor memory, or is read by the asynchronous proxy after
 // a proxy fence. Nothing orders such an arrival before the pair's closing
 // barrier, so none may be left that nobody waits for: the commits' arrivals (commit2)
-// too, which warp 11 sees out.
+// too, which warp 11 sees out at the end.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }

@@ -418,6 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   __shared__ Barriers bars;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ int walked[2];    // tiles and items of this pair
   __shared__ int fix[kFixes];  // round + 1 of the item whose V had values that were not finite taken out
   __shared__ float shared_max[2][2][128], shared_sum[2][128];
   __shared__ uint4 stage[8][128];
@@ -572,15 +573,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         }
       }
     }
-  } else if (warp >= kEdgeWarp) {
+  } else if (warp == kEdgeWarp) {
     // ---- V tiles with keys that some row must not see
     Turn<ST> t;
-    Turn<SB> pt;
-    int edges = 0, r = 0;
+    int edges = 0, tiles = 0, r = 0;
     bool ok = true;
     for (int x; (x = nth(a, r)) >= 0; r++) {
       const Item it = r ? item_of(a, x) : it0;
-      for (int j = 0; j < it.tiles; j++, t.next(), pt.next()) {
+      tiles += it.tiles;
+      for (int j = 0; j < it.tiles; j++, t.next()) {
         const int key0 = (it.first + j) * kTileKeys;
         if (key0 + kTileKeys <= it.hidden) continue;
         const int st = t.i;
@@ -628,13 +629,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
         if (lane == 0 && ok) arrive_at(peer_addr(s_addr(&bars.v_full[st]), 0));
       }
     }
-    // The MMAs' last commits arrive in both CTAs, and nothing else waits for some of
-    // them (no copy is left; the softmax wants the last product's alone): none may still
-    // be on its way when a CTA leaves.
-    for (int i = 0; ok && i < ST; i++, t.next())
-      ok = wait_warp<100>(c, &bars.k_empty[t.i], t.parity ^ 1) && wait_warp<100>(c, &bars.v_empty[t.i], t.parity ^ 1);
-    for (int i = 0; ok && i < SB; i++, pt.next()) ok = wait_warp<100>(c, &bars.pv_done[pt.i], pt.parity ^ 1);
-    if (ok) wait_warp<100>(c, &bars.q_empty, (r & 1) ^ 1);
+    if (lane == 0) {
+      walked[0] = tiles;
+      walked[1] = r;
+    }
   } else {
     // ---- softmax: warps w and w + 4 share 32 rows (thread = row), and halve their
     // columns. A wait that gave up changes only what is handed on: the two warps
@@ -772,6 +770,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   }
   fence_before_sync();
   __syncthreads();
+  // The MMAs' last commits arrive in both CTAs, and nothing has waited for some of them
+  // (no copy is left that would; the softmax wants the last product's alone): none may
+  // still be on its way when a CTA leaves. All MMAs are done here, so each barrier is in its
+  // last phase or past it, and a parity tells which. A lane each.
+  if (warp == kEdgeWarp && !*c.abort_flag) {
+    const int i = lane & 3, tiles = walked[0];
+    uint64_t* bar = &bars.q_empty;
+    int use = walked[1] - 1;  // the barrier's last, from 0; -1 where it has none: such a wait returns at once
+    if (lane < 8 && i < ST) {
+      bar = lane < 4 ? &bars.k_empty[i] : &bars.v_empty[i];
+      use = tiles > i ? (tiles - 1 - i) / ST : -1;
+    } else if (lane >= 8 && lane < 12 && i < SB) {
+      bar = &bars.pv_done[i];
+      use = tiles > i ? (tiles - 1 - i) / SB : -1;
+    }
+    wait_warp<0>(c, bar, (uint32_t)use & 1);
+  }
+  __syncwarp();
   pair_sync();
   if (warp == kMmaWarp) {
     fence_after_sync();
