@@ -268,6 +268,41 @@ DecodeScratch decode_scratch(int batch, int heads_q, int heads_kv, int dim, int 
 }
 int decode_warps() { return tfx::multiprocessors() * 4; }
 
+// Rows of the given lists (null: the last extend's).
+int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
+                const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  if (layer < 0 || layer >= c->layers) return fail_with(TFX_EINVAL, "layer %d of %d", layer, c->layers);
+  if (rows < 0 || rows > c->pages * c->page_size)
+    return fail_with(TFX_EINVAL, "rows=%d outside 0..%d", rows, c->pages * c->page_size);
+  if ((rc = check_reserved(c))) return rc;
+  if (!rows) return 0;
+  if ((rc = check_rows("k", k, ldk, (int64_t)c->heads_kv * c->dim))) return rc;
+  if ((rc = check_rows("v", v, ldv, (int64_t)c->heads_kv * c->dim))) return rc;
+  const tfx::BookArgs b = book_args(c, nullptr, nullptr, 0);
+  tfx::AppendArgs a = {};
+  const int64_t layer_values = (int64_t)c->pages * page_values(c);
+  a.k_new = k;
+  a.v_new = v;
+  a.k = static_cast<uint16_t*>(c->k) + layer * layer_values;
+  a.v = static_cast<uint16_t*>(c->v) + layer * layer_values;
+  a.ldk = ldk / 8;
+  a.ldv = ldv / 8;
+  a.row = c->heads_kv * c->dim / 8;
+  a.seqs = seqs;
+  a.offsets = offsets;
+  a.n = n;
+  a.book = c->book;
+  a.table = b.tables;
+  a.slots = c->slots;
+  a.width = c->width;
+  a.pages = c->pages;
+  a.page_size = c->page_size;
+  a.grown = b.grown;
+  return tfx::launch_append(a, rows, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -381,40 +416,6 @@ int tfx_cache_extend(tfx_cache* c, const int32_t* seqs, const int32_t* offsets, 
   if (rc) return rc;
   if (n > c->slots) return fail_with(TFX_EINVAL, "%d sequences, %d slots", n, c->slots);
   return tfx::launch_extend(book_args(c, seqs, offsets, n), stream);
-}
-
-static int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
-                       const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream) {
-  int rc = check_cache(c);
-  if (rc) return rc;
-  if (layer < 0 || layer >= c->layers) return fail_with(TFX_EINVAL, "layer %d of %d", layer, c->layers);
-  if (rows < 0 || rows > c->pages * c->page_size)
-    return fail_with(TFX_EINVAL, "rows=%d outside 0..%d", rows, c->pages * c->page_size);
-  if ((rc = check_reserved(c))) return rc;
-  if (!rows) return 0;
-  if ((rc = check_rows("k", k, ldk, (int64_t)c->heads_kv * c->dim))) return rc;
-  if ((rc = check_rows("v", v, ldv, (int64_t)c->heads_kv * c->dim))) return rc;
-  const tfx::BookArgs b = book_args(c, nullptr, nullptr, 0);
-  tfx::AppendArgs a = {};
-  const int64_t layer_values = (int64_t)c->pages * page_values(c);
-  a.k_new = k;
-  a.v_new = v;
-  a.k = static_cast<uint16_t*>(c->k) + layer * layer_values;
-  a.v = static_cast<uint16_t*>(c->v) + layer * layer_values;
-  a.ldk = ldk / 8;
-  a.ldv = ldv / 8;
-  a.row = c->heads_kv * c->dim / 8;
-  a.seqs = seqs;
-  a.offsets = offsets;
-  a.n = n;
-  a.book = c->book;
-  a.table = b.tables;
-  a.slots = c->slots;
-  a.width = c->width;
-  a.pages = c->pages;
-  a.page_size = c->page_size;
-  a.grown = b.grown;
-  return tfx::launch_append(a, rows, stream);
 }
 
 int tfx_cache_append(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,

@@ -107,8 +107,8 @@ int tfx_cache_append(tfx_cache* c, int layer, const void* k, int64_t ldk, const 
 
 /* The same with lists of its own (device; n as in tfx_cache_extend): where
  * several extends have made room, the lists of the one that these rows are for, or
- * some of its entries. Row t of sequence seqs[i] is one of the tokens that the last
- * extend of that sequence made room for, which must be offsets[i+1] - offsets[i]. */
+ * some of its entries. Rows offsets[i] .. offsets[i+1]-1 are the tokens that the last
+ * extend of sequence seqs[i] made room for: as many, or none is stored. */
 int tfx_cache_append_listed(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
                             const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream);
 
@@ -139,9 +139,9 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * heads_q/heads_kv) where it has more than 32 and there are 256 such tokens or more,
  * else once for every 16 rows; 0 where nothing is shared. A sequence shorter than
  * that attends to as many of them as its length says (what it does not hold of
- * them must then be finite). A sequence that holds no token, or a slot out of range, gives zeros. h->heads_kv, dim and act
- * are the cache's. Same arithmetic as tfx_attn_prompt, with partial results of
- * FP32 joined in a fixed order. */
+ * them must then be finite). A sequence that holds no token, or a slot out of
+ * range, gives zeros. h->heads_kv, dim and act are the cache's. Same arithmetic as
+ * tfx_attn_prompt, with partial results of FP32 joined in a fixed order. */
 int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void* q, int64_t ldq, const int32_t* seqs,
                     int batch, int shared, void* out, int64_t ldo, cudaStream_t stream);
 
