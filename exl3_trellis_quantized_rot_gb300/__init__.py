@@ -15,9 +15,10 @@ import ctypes as C
 import os
 
 from .attention import (CACHE_BAD, CACHE_FULL, CACHE_TABLE_FULL, Cache, attn_decode, attn_error, attn_prompt,  # noqa: F401
-                        cache_append, cache_compact, cache_copy, cache_extend, cache_fork, cache_free, cache_release,
-                        cache_reserve)
+                        cache_append, cache_compact, cache_copy, cache_extend, cache_fork, cache_free, cache_read,
+                        cache_release, cache_reserve)
 from .attention import declare as _declare_attention
+from .rotary import Rope, declare as _declare_rope, rope, rope_frequencies  # noqa: F401
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtfx_exl3.so")
@@ -104,6 +105,7 @@ def lib() -> C.CDLL:
         L.tfx_exl3_debug_launch_count.argtypes = []
         L.tfx_exl3_debug_launch_count.restype = C.c_int64
         _declare_attention(L)
+        _declare_rope(L)
         _lib = L
     return _lib
 

@@ -3,7 +3,7 @@
 Argument marshalling and shape checks only, as in the package's linear layer:
 every step runs in the kernels of ``libtfx_exl3.so``. Names follow the C ABI:
 ``attn_prompt``, ``attn_decode``, ``cache_reserve``, ``cache_release``,
-``cache_extend``, ``cache_append``, ``cache_fork``, ``cache_free``,
+``cache_extend``, ``cache_append``, ``cache_read``, ``cache_fork``, ``cache_free``,
 ``cache_compact``, ``cache_copy``.
 """
 from __future__ import annotations
@@ -15,12 +15,14 @@ import sys
 _pkg = sys.modules[__package__]  # being imported when this runs: its functions are looked up at each call
 
 CACHE_FULL, CACHE_BAD, CACHE_TABLE_FULL = 1, 2, 4
+STORE_ACT, STORE_I8, STORE_E4M3 = 0, 1, 2
+CACHE_BLOCK = 16  # tokens of a head that share a scale in an 8-bit cache
 MAX_BATCH = 4096
 _TOP = 1 << 31
 
 ABI_SYMBOLS = ("tfx_attn_prompt", "tfx_attn_decode", "tfx_attn_debug_error", "tfx_cache_book_ints", "tfx_cache_reserve",
-               "tfx_cache_release", "tfx_cache_extend", "tfx_cache_append", "tfx_cache_append_listed", "tfx_cache_fork",
-               "tfx_cache_free", "tfx_cache_compact", "tfx_cache_copy")
+               "tfx_cache_release", "tfx_cache_extend", "tfx_cache_append", "tfx_cache_append_listed", "tfx_cache_read",
+               "tfx_cache_fork", "tfx_cache_free", "tfx_cache_compact", "tfx_cache_copy")
 
 
 class HeadsStruct(C.Structure):
@@ -30,7 +32,7 @@ class HeadsStruct(C.Structure):
 class CacheStruct(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("book", C.c_void_p), ("layers", C.c_int), ("pages", C.c_int),
                 ("page_size", C.c_int), ("heads_kv", C.c_int), ("dim", C.c_int), ("act", C.c_int), ("slots", C.c_int),
-                ("width", C.c_int), ("priv", C.c_void_p)]
+                ("width", C.c_int), ("priv", C.c_void_p), ("store", C.c_int), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
 
 
 def declare(L: C.CDLL) -> None:
@@ -45,6 +47,7 @@ def declare(L: C.CDLL) -> None:
     L.tfx_cache_extend.argtypes = [K, vp, vp, i, vp]
     L.tfx_cache_append.argtypes = [K, i, vp, l64, vp, l64, i, vp]
     L.tfx_cache_append_listed.argtypes = [K, i, vp, l64, vp, l64, i, vp, vp, i, vp]
+    L.tfx_cache_read.argtypes = [K, i, vp, vp, vp, i, i, vp, l64, vp, l64, vp]
     L.tfx_cache_fork.argtypes = [K, vp, vp, i, vp]
     L.tfx_cache_free.argtypes = [K, vp, i, vp]
     L.tfx_cache_compact.argtypes = [K, vp]
@@ -57,6 +60,7 @@ def declare(L: C.CDLL) -> None:
 # Set by _load: the package imports without torch; what takes its tensors brings it in.
 torch = _int32 = _raw_stream = _current_device = None
 _act_of: dict = {}
+_store_of: dict = {}
 
 
 def _load() -> None:
@@ -64,6 +68,7 @@ def _load() -> None:
     global torch, _int32, _raw_stream, _current_device
     import torch
     _act_of.update({torch.float16: 0, torch.bfloat16: 1})  # TFX_F16, TFX_BF16
+    _store_of.update({torch.int8: STORE_I8, torch.float8_e4m3fn: STORE_E4M3})
     _int32 = torch.int32
     # absent without CUDA
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -205,9 +210,14 @@ class Cache:
     k, v: (layers, pages, page_size, kv_heads, dim), contiguous; slots: sequences
     it can hold; width: pages that one sequence can have; book: int32 vector
     (made empty here by default), see ``lens``, ``refs`` and ``tables``.
+
+    k and v of int8 or float8_e4m3fn are a cache of 8-bit codes: act is the type of
+    the rows that calls take and give (float16 or bfloat16), k_scale and v_scale are
+    float32 (layers, pages, page_size / 16, kv_heads), contiguous (made here by
+    default): a power of two for each 16 tokens of a head.
     """
 
-    def __init__(self, k, v, slots: int, width: int, book=None):
+    def __init__(self, k, v, slots: int, width: int, book=None, k_scale=None, v_scale=None, act=None):
         if torch is None:
             _load()
         if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
@@ -215,18 +225,33 @@ class Cache:
         if not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("k and v must be contiguous")
         layers, pages, page_size, heads, dim = k.shape
-        self.s = CacheStruct(k.data_ptr(), v.data_ptr(), None, layers, pages, page_size, heads, dim, _act(k.dtype), slots,
-                             width, None)
+        store = _store_of.get(k.dtype, STORE_ACT)
+        if store == STORE_ACT:
+            if act not in (None, k.dtype) or k_scale is not None or v_scale is not None:
+                raise ValueError(f"act and scales go with k and v of int8 or float8_e4m3fn, not {k.dtype}")
+            act = k.dtype
+        elif act is None:
+            raise ValueError(f"k and v of {k.dtype}: act says the type of the rows")
+        self.s = CacheStruct(k.data_ptr(), v.data_ptr(), None, layers, pages, page_size, heads, dim, _act(act), slots,
+                             width, None, store, None, None)
         ints = 4 + slots + pages + slots * width
         if book is None:
             book = torch.zeros(ints, dtype=torch.int32, device=k.device)
             book[4 + slots + pages:] = -1
         elif book.numel() != ints:
             raise ValueError(f"book of {book.numel()} values, {ints} are wanted")
-        self.device, self.dtype, self.heads_kv, self.dim, self.act = k.get_device(), k.dtype, heads, dim, self.s.act
+        self.device, self.dtype, self.heads_kv, self.dim, self.act = k.get_device(), act, heads, dim, self.s.act
         self.ref = C.byref(self.s)
         self.s.book = _ints("book", book, self.device)[1]
-        self.k, self.v, self.book = k, v, book
+        if store != STORE_ACT:
+            shape = (layers, pages, page_size // CACHE_BLOCK, heads)
+            k_scale, v_scale = (torch.zeros(shape, dtype=torch.float32, device=k.device) if t is None else t
+                                for t in (k_scale, v_scale))
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if tuple(t.shape) != shape or t.dtype != torch.float32 or t.get_device() != self.device or not t.is_contiguous():
+                    raise ValueError(f"{name}: a contiguous float32 tensor of shape {shape} on the cache's device is wanted")
+            self.s.k_scale, self.s.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        self.k, self.v, self.book, self.k_scale, self.v_scale = k, v, book, k_scale, v_scale
 
     @property
     def lens(self):
@@ -275,8 +300,9 @@ def cache_extend(c: Cache, seqs, offsets, stream=None) -> None:
 
 def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=None) -> None:
     """K and V (rows, kv_heads, dim) of one layer's new tokens, into the room that
-    cache_extend made. seqs and offsets (int32 vectors on the cache's device) are that
-    call's, or some entries of it; left out, the last cache_extend's."""
+    cache_extend made, quantised on the way into a cache of 8-bit codes. seqs and offsets
+    (int32 vectors on the cache's device) are that call's, or some entries of it; left out,
+    the last cache_extend's."""
     if not -_TOP <= layer < _TOP:
         _int32s(layer=layer)
     heads, dim, dtype, dev = c.heads_kv, c.dim, c.dtype, c.device
@@ -308,6 +334,38 @@ def cache_append(c: Cache, layer: int, k, v, seqs=None, offsets=None, stream=Non
         rc = (_pkg._lib or _pkg.lib()).tfx_cache_append_listed(c.ref, layer, pk, ldk, pv, ldv, n, ps, po, ns, on)
     if rc:
         _check(rc)
+
+
+def cache_read(c: Cache, layer: int, seqs, starts, offsets, rows: int, out=None, stream=None):
+    """K and V (rows, kv_heads, dim) of one layer out of the cache, in its act type: rows
+    offsets[i]:offsets[i+1] are tokens starts[i], starts[i] + 1, ... of sequence seqs[i]
+    (int32 vectors on the cache's device). out: a pair to write to; rows outside the lists
+    stay as they are there, and are zero where it is made here. Returns (k, v)."""
+    _int32s(layer=layer, rows=rows)
+    dev = c.device
+    n, ps = _ints("seqs", seqs, dev)
+    m, pb = _ints("starts", starts, dev)
+    no, po = _ints("offsets", offsets, dev)
+    if m != n or no != n + 1:
+        raise ValueError(f"{m} starts and {no} offsets for {n} sequences")
+    if rows < 0:
+        raise ValueError(f"rows={rows}")
+    on = _stream(stream, dev)
+    if out is None:
+        shape = rows, c.heads_kv, c.dim
+        if stream is None:
+            out = tuple(torch.zeros(shape, dtype=c.dtype, device=c.k.device) for _ in range(2))
+        else:
+            out = tuple(_made_on(stream, dev, shape, c.dtype, True) for _ in range(2))
+    k, v = out
+    nk, ldk, pk = _rows("k", k, c.heads_kv, c.dim, c.dtype, dev)
+    nv, ldv, pv = _rows("v", v, c.heads_kv, c.dim, c.dtype, dev)
+    if nk < rows or nv < rows:
+        raise ValueError(f"out has {nk} and {nv} rows, {rows} are wanted")
+    rc = (_pkg._lib or _pkg.lib()).tfx_cache_read(c.ref, layer, ps, pb, po, n, rows, pk, ldk, pv, ldv, on)
+    if rc:
+        _check(rc)
+    return k, v
 
 
 def _pair(c: Cache, src, dst) -> tuple:

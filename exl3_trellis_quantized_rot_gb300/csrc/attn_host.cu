@@ -119,6 +119,12 @@ int check_cache(const tfx_cache* c) {
   // an extend adds up what a list of at most `slots` entries asks for
   if ((int64_t)c->slots * c->width > INT32_MAX) return fail_with(TFX_EUNSUPPORTED, "2^31 table entries or more");
   if (!aligned16(c->k) || !aligned16(c->v)) return fail_with(TFX_EALIGN, "k or v is not 16-byte aligned");
+  if (c->store != TFX_STORE_ACT) {
+    if (c->store != TFX_STORE_I8 && c->store != TFX_STORE_E4M3) return fail_with(TFX_EINVAL, "store=%d", c->store);
+    if (!c->k_scale || !c->v_scale) return fail_with(TFX_EINVAL, "null k_scale or v_scale");
+    if ((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale)) & 3u)
+      return fail_with(TFX_EALIGN, "k_scale or v_scale is not 4-byte aligned");
+  }
   if (reinterpret_cast<uintptr_t>(c->book) & 3u) return fail_with(TFX_EALIGN, "book is not 4-byte aligned");
   return 0;
 }
@@ -151,6 +157,16 @@ int* lens_of(const tfx_cache* c) { return c->book + 4; }
 int* refs_of(const tfx_cache* c) { return lens_of(c) + c->slots; }
 int* tables_of(const tfx_cache* c) { return refs_of(c) + c->pages; }
 int64_t page_values(const tfx_cache* c) { return (int64_t)c->page_size * c->heads_kv * c->dim; }
+int value_bytes(const tfx_cache* c) { return c->store == TFX_STORE_ACT ? 2 : 1; }
+int64_t page_scales(const tfx_cache* c) { return (int64_t)(c->page_size / TFX_CACHE_BLOCK) * c->heads_kv; }
+// A layer's pages and scales.
+template <typename P>
+P* layer_of(const tfx_cache* c, void* pool, int layer) {
+  return reinterpret_cast<P*>(static_cast<char*>(pool) + (int64_t)layer * c->pages * page_values(c) * value_bytes(c));
+}
+float* scales_of(const tfx_cache* c, float* scales, int layer) {
+  return c->store == TFX_STORE_ACT ? nullptr : scales + (int64_t)layer * c->pages * page_scales(c);
+}
 
 // Page-call scratch: a counter and the list length that an append uses, what
 // extends leave for the appends (a mark and a list entry of each slot), and five
@@ -208,7 +224,12 @@ tfx::MoveArgs move_args(const tfx_cache* c, const tfx::BookArgs& b, tfx::Tables 
   m.slots = c->slots;
   m.width = c->width;
   m.page_size = c->page_size;
-  m.page_words = page_values(c) / 8;
+  m.page_words = page_values(c) * value_bytes(c) / 16;
+  if (c->store != TFX_STORE_ACT) {
+    m.k_scale = c->k_scale;
+    m.v_scale = c->v_scale;
+    m.page_scales = (int)page_scales(c);
+  }
   m.tables = tables;
   return m;
 }
@@ -282,11 +303,10 @@ int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void*
   if ((rc = check_rows("v", v, ldv, (int64_t)c->heads_kv * c->dim))) return rc;
   const tfx::BookArgs b = book_args(c, nullptr, nullptr, 0);
   tfx::AppendArgs a = {};
-  const int64_t layer_values = (int64_t)c->pages * page_values(c);
   a.k_new = k;
   a.v_new = v;
-  a.k = static_cast<uint16_t*>(c->k) + layer * layer_values;
-  a.v = static_cast<uint16_t*>(c->v) + layer * layer_values;
+  a.k = layer_of<void>(c, c->k, layer);
+  a.v = layer_of<void>(c, c->v, layer);
   a.ldk = ldk / 8;
   a.ldv = ldv / 8;
   a.row = c->heads_kv * c->dim / 8;
@@ -300,7 +320,12 @@ int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void*
   a.pages = c->pages;
   a.page_size = c->page_size;
   a.grown = b.grown;
-  return tfx::launch_append(a, rows, stream);
+  if (c->store == TFX_STORE_ACT) return tfx::launch_append(a, rows, stream);
+  a.k_scale = scales_of(c, c->k_scale, layer);
+  a.v_scale = scales_of(c, c->v_scale, layer);
+  a.heads = c->heads_kv;
+  a.rows = rows;
+  return tfx::launch_append_q8(a, c->act, c->store, c->dim, rows, stream);
 }
 
 }  // namespace
@@ -431,6 +456,42 @@ int tfx_cache_append_listed(tfx_cache* c, int layer, const void* k, int64_t ldk,
   return append_rows(c, layer, k, ldk, v, ldv, n ? rows : 0, seqs, offsets, n, stream);
 }
 
+int tfx_cache_read(tfx_cache* c, int layer, const int32_t* seqs, const int32_t* starts, const int32_t* offsets, int n,
+                   int rows, void* k, int64_t ldk, void* v, int64_t ldv, cudaStream_t stream) {
+  int rc = check_list(c, n, seqs, offsets);
+  if (rc) return rc;
+  if (n && !starts) return fail_with(TFX_EINVAL, "null starts");
+  if (layer < 0 || layer >= c->layers) return fail_with(TFX_EINVAL, "layer %d of %d", layer, c->layers);
+  if (rows < 0) return fail_with(TFX_EINVAL, "rows=%d", rows);
+  if (!n || !rows) return 0;
+  if ((rc = check_rows("k", k, ldk, (int64_t)c->heads_kv * c->dim))) return rc;
+  if ((rc = check_rows("v", v, ldv, (int64_t)c->heads_kv * c->dim))) return rc;
+  tfx::ReadArgs a = {};
+  a.k = layer_of<const void>(c, c->k, layer);
+  a.v = layer_of<const void>(c, c->v, layer);
+  a.k_scale = scales_of(c, c->k_scale, layer);
+  a.v_scale = scales_of(c, c->v_scale, layer);
+  a.k_out = k;
+  a.v_out = v;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.seqs = seqs;
+  a.starts = starts;
+  a.offsets = offsets;
+  a.n = n;
+  a.rows = rows;
+  a.book = c->book;
+  a.lens = lens_of(c);
+  a.table = tables_of(c);
+  a.slots = c->slots;
+  a.width = c->width;
+  a.pages = c->pages;
+  a.page_size = c->page_size;
+  a.heads = c->heads_kv;
+  a.dim = c->dim;
+  return tfx::launch_read(a, c->act, c->store, stream);
+}
+
 int tfx_cache_fork(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {
   const int rc = check_list(c, n, src, dst);
   if (rc) return rc;
@@ -491,11 +552,13 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   if ((rc = check_rows("q", q, ldq, (int64_t)h->heads_q * h->dim))) return rc;
   if ((rc = check_rows("out", out, ldo, (int64_t)h->heads_q * h->dim))) return rc;
   tfx::DecodeAttnArgs a = {};
-  const int64_t layer_values = (int64_t)c->pages * page_values(c), ld = (int64_t)c->heads_kv * c->dim;
-  const uint16_t* kl = static_cast<const uint16_t*>(c->k) + layer * layer_values;
-  const uint16_t* vl = static_cast<const uint16_t*>(c->v) + layer * layer_values;
-  if ((rc = make_map(&a.k, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
-  if ((rc = make_map(&a.v, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
+  const bool coded = c->store != TFX_STORE_ACT;
+  const int64_t ld = (int64_t)c->heads_kv * c->dim;
+  const void *kl = layer_of<const void>(c, c->k, layer), *vl = layer_of<const void>(c, c->v, layer);
+  if (!coded) {
+    if ((rc = make_map(&a.k, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
+    if ((rc = make_map(&a.v, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
+  }
   a.q = q;
   a.out = out;
   a.ldq = ldq;
@@ -508,12 +571,19 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.heads_kv = h->heads_kv;
   a.group = h->heads_q / h->heads_kv;
   a.batch = batch;
-  a.shared = shared;
+  a.shared = coded ? shared / TFX_CACHE_BLOCK * TFX_CACHE_BLOCK : shared;
   a.page_size = c->page_size;
   a.page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
   a.pages = c->pages;
   a.slots = c->slots;
   a.width = c->width;
+  if (coded) {
+    a.codes_k = static_cast<const uint8_t*>(kl);
+    a.codes_v = static_cast<const uint8_t*>(vl);
+    a.k_scale = scales_of(c, c->k_scale, layer);
+    a.v_scale = scales_of(c, c->v_scale, layer);
+    return tfx::launch_decode_q8(a, c->act, c->store, c->dim, stream);
+  }
   if (many_rows(batch, a.group) && shared >= 256) {
     a.per_tile = heads_per_tile(a.group);
     a.tokens = 128 / a.per_tile;

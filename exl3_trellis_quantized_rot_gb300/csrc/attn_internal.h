@@ -68,6 +68,9 @@ struct DecodeAttnArgs {
   float2* pre_ml;
   int* err;
   long long spin;
+  // 8-bit stores: the layer's codes and scales
+  const uint8_t *codes_k, *codes_v;
+  const float *k_scale, *v_scale;
 };
 
 // What appends need to know of the extends before them. Only an extend writes it,
@@ -101,6 +104,20 @@ struct AppendArgs {
   const int* table;
   int slots, width, pages, page_size;
   Grown grown;
+  float *k_scale, *v_scale;  // 8-bit stores: the layer's
+  int heads, rows;
+};
+
+struct ReadArgs {
+  const void *k, *v;  // the layer's pages
+  const float *k_scale, *v_scale;
+  void *k_out, *v_out;
+  long long ldk, ldv;  // elements
+  const int *seqs, *starts, *offsets;
+  int n, rows;
+  int* book;
+  const int *lens, *table;
+  int slots, width, pages, page_size, heads, dim;
 };
 
 enum Tables { kTablesNone = 0, kTablesFork = 1, kTablesCompact = 2 };
@@ -112,16 +129,21 @@ struct MoveArgs {
   int n, layers, pages, slots, width, page_size;
   long long page_words;  // 16-byte words of one page of one layer
   Tables tables;
+  float *k_scale, *v_scale;
+  int page_scales;  // scales of one page of one layer; 0: the pages hold act
 };
 
 int launch_extend(const BookArgs& a, cudaStream_t s);
 int launch_append(const AppendArgs& a, int rows, cudaStream_t s);
+int launch_append_q8(const AppendArgs& a, int act, int store, int dim, int rows, cudaStream_t s);
+int launch_read(const ReadArgs& a, int act, int store, cudaStream_t s);
 int launch_free(const BookArgs& a, cudaStream_t s);
 int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStream_t s);
 
 int launch_prompt(const PromptArgs& a, int act, int dim, cudaStream_t s);
 int launch_prefix(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
+int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
 
 // exl3_host.cu
 tfx_exl3_driver driver_hooks();

@@ -12,6 +12,7 @@
 #include <climits>
 
 #include "attn_internal.h"
+#include "cache_device.cuh"
 #include "exl3_kernels.cuh"
 
 namespace tfx {
@@ -148,20 +149,6 @@ __global__ void __launch_bounds__(kBookThreads) extend_kernel(const __grid_const
   griddep_launch();
 }
 
-// The entry of a list of n > 0 (offsets not decreasing) that row t is of, by a warp:
-// 32 entries a step. Whether the row is in it at all is the caller's to look at.
-__device__ __forceinline__ int entry_of(const int* offsets, int n, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, len = n;
-  while (len > 1) {
-    const int step = (len + 31) / 32, x = lane * step;
-    const int k = max(__popc(__ballot_sync(~0u, x < len && offsets[lo + x] <= t)) - 1, 0);
-    lo += k * step;
-    len = min(step, len - k * step);
-  }
-  return lo;
-}
-
 // One CTA per token: its K row and its V row. Where they go follows from the lists,
 // the marks that extends left and the tables as they are now, so that other calls may come
 // between an extend and its appends.
@@ -169,23 +156,8 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
   griddep_wait();
   griddep_launch();
   const int t = blockIdx.x;
-  const int n = a.seqs ? a.n : *a.grown.n;
-  const int* offsets = a.seqs ? a.offsets : a.grown.offsets;
-  if (n < 1) return;
-  const int i = entry_of(offsets, n, t);
-  const int begin = offsets[i], end = offsets[i + 1], s = (a.seqs ? a.seqs : a.grown.seqs)[i];
-  if (t < begin || t >= end) return;
-  const int2 mark = (unsigned)s < (unsigned)a.slots ? a.grown.mark[s] : make_int2(0, 0);
-  if (mark.y < 0) return;  // refused by its extend, which said so
-  int page = -1;
-  const int pos = mark.x + (t - begin);
-  if (mark.y == end - begin && pos / a.page_size < a.width)
-    page = a.table[(long long)s * a.width + pos / a.page_size];
-  if (page < 0 || page >= a.pages) {
-    if (threadIdx.x == 0) atomicOr(&a.book[0], TFX_CACHE_BAD);
-    return;
-  }
-  const int to = page * a.page_size + pos % a.page_size;
+  const int to = place_of(a, t).to;
+  if (to < 0) return;
   const uint4* ks = reinterpret_cast<const uint4*>(a.k_new) + (long long)t * a.ldk;
   const uint4* vs = reinterpret_cast<const uint4*>(a.v_new) + (long long)t * a.ldv;
   uint4* kd = reinterpret_cast<uint4*>(a.k) + (long long)to * a.row;
@@ -384,6 +356,11 @@ __global__ void __launch_bounds__(kCopyThreads) move_kernel(const __grid_constan
 #pragma unroll
     for (int j = 0; j < kCopyVec; j++)
       if (c0 + j * kCopyThreads < a.page_words) __stcs(dst + c0 + j * kCopyThreads, x[j]);
+    if (part == 0) {
+      float* scales = lk & 1 ? a.v_scale : a.k_scale;
+      for (int c = threadIdx.x; c < a.page_scales; c += kCopyThreads)
+        scales[(layer + d) * a.page_scales + c] = scales[(layer + s) * a.page_scales + c];
+    }
   }
 }
 

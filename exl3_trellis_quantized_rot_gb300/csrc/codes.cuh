@@ -1,0 +1,92 @@
+// Codes of 8 bits with a power of two as their scale: what a value becomes, and back.
+//
+// The scale of some values with largest magnitude m is 2^e, e >= -126 the smallest
+// with m <= top * 2^e. Multiplying by 2^e or 2^-e is exact (but for results that are
+// subnormal in FP32), so a code is x rounded once, to the nearest, ties to even,
+// and a larger scale for codes is the same step again. A magnitude's float bits carry both
+// parts of the choice: the exponent, and whether the fraction is above top's own.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_internal.h"
+
+namespace tfx {
+
+constexpr uint32_t kInfBits = 0x7f800000u;  // from here on: infinities and NaN
+constexpr float kLeastScale = 1.1754943508222875e-38f;  // 2^-126
+
+// top = (1 + kFraction / 2^23) * 2^kPlace
+template <int Store>
+struct Code;
+template <>
+struct Code<TFX_STORE_I8> {
+  static constexpr int kPlace = 6;
+  static constexpr uint32_t kFraction = 0x7e0000u;  // 127 = 1.984375 * 2^6
+};
+template <>
+struct Code<TFX_STORE_E4M3> {
+  static constexpr int kPlace = 8;
+  static constexpr uint32_t kFraction = 0x600000u;  // 448 = 1.75 * 2^8
+};
+
+// The scale that magnitudes of up to the float with these bits need; NaN where it is not finite.
+template <int Store>
+__device__ __forceinline__ float scale_for(uint32_t bits) {
+  if (bits >= kInfBits) return __uint_as_float(0x7fc00000u);
+  const int e = (int)(bits >> 23) - Code<Store>::kPlace + ((bits & 0x7fffffu) > Code<Store>::kFraction);
+  return __uint_as_float((uint32_t)max(e, 1) << 23);  // at least 2^-126
+}
+// 1 / scale, for powers of two of at least 2^-126 and at most 2^126; NaN of a NaN.
+__device__ __forceinline__ float inverse_of(float scale) {
+  return __uint_as_float(scale == scale ? 0x7f000000u - __float_as_uint(scale) : 0x7fc00000u);
+}
+// A NaN stays.
+__device__ __forceinline__ float larger_scale(float a, float b) { return a != a || a > b ? a : b; }
+
+// Two values in the codes' range; NaN becomes any code.
+template <int Store>
+__device__ __forceinline__ uint32_t code2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t code2<TFX_STORE_I8>(float lo, float hi) {
+  return ((uint32_t)__float2int_rn(lo) & 0xffu) | ((uint32_t)__float2int_rn(hi) & 0xffu) << 8;
+}
+template <>
+__device__ __forceinline__ uint32_t code2<TFX_STORE_E4M3>(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int Store>
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
+  return code2<Store>(a, b) | code2<Store>(c, d) << 16;
+}
+
+// Values of the four codes in a word.
+template <int Store>
+__device__ __forceinline__ void values4(uint32_t w, float (&x)[4]);
+template <>
+__device__ __forceinline__ void values4<TFX_STORE_I8>(uint32_t w, float (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) x[i] = (float)(int8_t)(w >> (8 * i));
+}
+template <>
+__device__ __forceinline__ void values4<TFX_STORE_E4M3>(uint32_t w, float (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ float2 pair_to_float(uint32_t w, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ float2 pair_to_float(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+}  // namespace tfx

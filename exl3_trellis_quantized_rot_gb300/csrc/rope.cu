@@ -1,0 +1,172 @@
+// Rotary positions of packed rows.
+//
+//   (a, b) -> g (a cos w - b sin w, b cos w + a sin w),  w = n f_i.
+// An angle is held as a fraction of a turn in 64 bits: f_i / 2 pi as F_i / 2^64, so
+// n F_i mod 2^64 is the angle without its whole turns, exactly but for F_i's own rounding.
+// Its top 32 bits, as a signed number of half turns, go to sincospi.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "../../include/tfx_rope.h"
+#include "attn_device.cuh"
+#include "codes.cuh"
+
+namespace tfx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMostRotary = 2048;
+
+struct RopeArgs {
+  const uint64_t* table;
+  const void* in[2];  // q, k
+  void* out[2];
+  long long ld_in[2], ld_out[2];
+  const int* positions;
+  int heads[2];
+  int dim, rotary, rows;
+  float gain, sine;  // factors of cosine and sine
+  int copy;          // whether the values behind the rotated ones are written
+};
+
+// One CTA per row. Items of a head: rotary/16 pairs of 16-byte words (half) or rotary/8
+// words (interleaved), then the words that are only copied.
+template <typename T, bool Interleaved>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float cosine[kMostRotary / 2], sine[kMostRotary / 2];
+  griddep_wait();
+  griddep_launch();
+  const int t = blockIdx.x, half = a.rotary / 2;
+  const long long n = a.positions[t];
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const uint64_t turn = (uint64_t)n * a.table[i];
+    float s, c;
+    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+    cosine[i] = c * a.gain;
+    sine[i] = s * a.sine;
+  }
+  __syncthreads();
+  const int turned = Interleaved ? a.rotary / 8 : a.rotary / 16;
+  const int per = turned + (a.copy ? (a.dim - a.rotary) / 8 : 0);
+  const int all = (a.heads[0] + a.heads[1]) * per;
+  for (int it = threadIdx.x; it < all; it += kThreads) {
+    const int h = it / per, j = it - h * per, side = h >= a.heads[0];
+    const int head = side ? h - a.heads[0] : h;
+    const T* in = reinterpret_cast<const T*>(a.in[side]) + t * a.ld_in[side] + (long long)head * a.dim;
+    T* out = reinterpret_cast<T*>(a.out[side]) + t * a.ld_out[side] + (long long)head * a.dim;
+    if (j >= turned) {
+      const int c = a.rotary + (j - turned) * 8;
+      *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(in + c);
+    } else if (Interleaved) {
+      uint32_t x[4];
+      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(in + j * 8);
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float2 f = pair_to_float(x[k], T());
+        const float c = cosine[j * 4 + k], s = sine[j * 4 + k];
+        x[k] = pack2<T>(f.x * c - f.y * s, f.y * c + f.x * s);
+      }
+      *reinterpret_cast<uint4*>(out + j * 8) = *reinterpret_cast<const uint4*>(x);
+    } else {
+      uint32_t x[4], y[4];
+      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(in + j * 8);
+      *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(in + half + j * 8);
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float2 f = pair_to_float(x[k], T()), g = pair_to_float(y[k], T());
+        const int i = j * 8 + 2 * k;
+        const float c0 = cosine[i], s0 = sine[i], c1 = cosine[i + 1], s1 = sine[i + 1];
+        x[k] = pack2<T>(f.x * c0 - g.x * s0, f.y * c1 - g.y * s1);
+        y[k] = pack2<T>(g.x * c0 + f.x * s0, g.y * c1 + f.y * s1);
+      }
+      *reinterpret_cast<uint4*>(out + j * 8) = *reinterpret_cast<const uint4*>(x);
+      *reinterpret_cast<uint4*>(out + half + j * 8) = *reinterpret_cast<const uint4*>(y);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace tfx
+
+namespace {
+
+using tfx::fail_with;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_side(const char* what, const void* p, int64_t ld, const void* out, int64_t ldo, int64_t width) {
+  if (!p || !out) return fail_with(TFX_EINVAL, "null %s or its output", what);
+  if (ld < width || ldo < width)
+    return fail_with(TFX_EINVAL, "pitches %lld and %lld of %s below its %lld values", (long long)ld, (long long)ldo, what,
+                     (long long)width);
+  if (ld > (1LL << 36) || ldo > (1LL << 36)) return fail_with(TFX_EINVAL, "pitch %lld or %lld of %s", (long long)ld, (long long)ldo, what);
+  if (ld % 8 || ldo % 8 || !aligned16(p) || !aligned16(out))
+    return fail_with(TFX_EALIGN, "%s and its output: 16-byte aligned pointers and pitches of whole 8 values", what);
+  if (p == out && ld != ldo) return fail_with(TFX_EINVAL, "%s in place with two pitches", what);
+  return 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tfx_rope_table(const double* freqs, int n, uint64_t* table) {
+  if (n < 0 || (n && (!freqs || !table))) return fail_with(TFX_EINVAL, "n=%d, or a null list", n);
+  for (int i = 0; i < n; i++)
+    if (!std::isfinite(freqs[i])) return fail_with(TFX_EINVAL, "freqs[%d] is not finite", i);
+  for (int i = 0; i < n; i++) {
+    const double turns = freqs[i] / 6.283185307179586;
+    const double part = turns - std::floor(turns);  // [0, 1], 1 where a tiny negative one is rounded up
+    table[i] = part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;
+  }
+  return 0;
+}
+
+int tfx_rope_apply(const tfx_rope* r, int act, int dim, const void* q, int64_t ldq, int heads_q, void* q_out, int64_t ldqo,
+                   const void* k, int64_t ldk, int heads_k, void* k_out, int64_t ldko, const int32_t* positions, int rows,
+                   int inverse, cudaStream_t stream) {
+  if (!r || !r->table) return fail_with(TFX_EINVAL, "null rope or table");
+  if (act != TFX_F16 && act != TFX_BF16) return fail_with(TFX_EINVAL, "act=%d", act);
+  if (dim < 16 || dim > 65536) return fail_with(TFX_EINVAL, "dim=%d outside 16..65536", dim);
+  if (dim % 8) return fail_with(TFX_EALIGN, "dim=%d is not a multiple of 8", dim);
+  if (r->rotary < 16 || r->rotary % 16 || r->rotary > dim || r->rotary > tfx::kMostRotary)
+    return fail_with(TFX_EUNSUPPORTED, "rotary=%d of dim=%d: a multiple of 16, at most %d", r->rotary, dim, tfx::kMostRotary);
+  if (!std::isfinite(r->gain)) return fail_with(TFX_EINVAL, "gain=%g", (double)r->gain);
+  if (heads_q < 1 || heads_k < 0 || heads_q > 65535 || heads_k > 65535 || ((int64_t)heads_q + heads_k) * dim > INT32_MAX)
+    return fail_with(TFX_EINVAL, "heads_q=%d, heads_k=%d of %d values", heads_q, heads_k, dim);
+  if (rows < 0) return fail_with(TFX_EINVAL, "rows=%d", rows);
+  if (!rows) return 0;
+  int rc = check_side("q", q, ldq, q_out, ldqo, (int64_t)heads_q * dim);
+  if (rc) return rc;
+  if (heads_k && (rc = check_side("k", k, ldk, k_out, ldko, (int64_t)heads_k * dim))) return rc;
+  if (!positions) return fail_with(TFX_EINVAL, "null positions");
+  if (reinterpret_cast<uintptr_t>(positions) & 3u || reinterpret_cast<uintptr_t>(r->table) & 7u)
+    return fail_with(TFX_EALIGN, "positions or table is not aligned");
+  tfx::RopeArgs a = {};
+  a.table = r->table;
+  a.in[0] = q;
+  a.in[1] = k;
+  a.out[0] = q_out;
+  a.out[1] = k_out;
+  a.ld_in[0] = ldq;
+  a.ld_in[1] = ldk;
+  a.ld_out[0] = ldqo;
+  a.ld_out[1] = ldko;
+  a.positions = positions;
+  a.heads[0] = heads_q;
+  a.heads[1] = heads_k;
+  a.dim = dim;
+  a.rotary = r->rotary;
+  a.rows = rows;
+  a.gain = r->gain;
+  a.sine = inverse ? -r->gain : r->gain;
+  a.copy = q != q_out || (heads_k && k != k_out);
+  const void* fn = r->interleaved ? act == TFX_F16 ? (const void*)tfx::rope_kernel<__half, true>
+                                                   : (const void*)tfx::rope_kernel<__nv_bfloat16, true>
+                   : act == TFX_F16 ? (const void*)tfx::rope_kernel<__half, false>
+                                    : (const void*)tfx::rope_kernel<__nv_bfloat16, false>;
+  return tfx::launch_kernel(fn, dim3((unsigned)rows), dim3(tfx::kThreads), 0, stream, &a, tfx::dependent_launches(), 1);
+}
+
+}  // extern "C"

@@ -1,7 +1,7 @@
 /*
  * tfx_attn — causal attention over packed prompts, attention of single tokens
- * over a paged K/V cache whose sequences share a prefix, and that cache's page
- * operations, for GB300 (sm_103a). Between the q/k/v group and o_proj of
+ * over a paged K/V cache whose sequences share a prefix (in the activations' type
+ * or in 8 bits), and that cache's page operations, for GB300 (sm_103a). Between the q/k/v group and o_proj of
  * tfx_exl3.h these take the place of the stand-ins: rows of q, k and v are the
  * group's outputs as they are, rows of the attention output are o_proj's input.
  *
@@ -62,7 +62,23 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
  * priv  : library state, NULL until tfx_cache_reserve().
  * Calls on one cache are ordered on one stream. Slot and page numbers come
  * from device memory and are checked there: one that is out of range, or a
- * sequence that finds no room, is left as it was and leaves a status bit. */
+ * sequence that finds no room, is left as it was and leaves a status bit.
+ *
+ * store : TFX_STORE_ACT (0): k and v hold act, and the scales are not looked at.
+ *         TFX_STORE_I8, TFX_STORE_E4M3: they hold codes of 8 bits, act is the type of
+ *         the rows that calls take and give, and a code stands for
+ *             code * scale,  scale = 2^e of its block,
+ *         a block being TFX_CACHE_BLOCK tokens of one head, K and V apart.
+ * k_scale, v_scale : float[layers][pages][page_size / TFX_CACHE_BLOCK][heads_kv],
+ *         4-byte aligned, for the 8-bit stores. Appends write them; what they hold
+ *         for blocks without a token does not matter.
+ * An append takes for a block the smallest e >= -126 under which the magnitudes of
+ * its new values are at most 127 (I8) or 448 (E4M3), or the block's own e where that
+ * is larger; x becomes x / scale rounded to the nearest code, ties to even. Where a
+ * block that holds tokens gets a larger e, its codes are rounded again in the same
+ * way (for I8 that can add half a step of the new scale; for E4M3 it is exact down to
+ * its subnormals). A value that is not finite makes the block's scale NaN until its
+ * page is used anew: the block reads as NaN, as do rows that attend to it. */
 typedef struct {
   void* k;
   void* v;
@@ -70,7 +86,15 @@ typedef struct {
   int layers, pages, page_size, heads_kv, dim, act;
   int slots, width;
   void* priv;
+  int store;
+  float* k_scale;
+  float* v_scale;
 } tfx_cache;
+
+#define TFX_STORE_ACT 0
+#define TFX_STORE_I8 1
+#define TFX_STORE_E4M3 2
+#define TFX_CACHE_BLOCK 16
 
 #define TFX_CACHE_FULL 1       /* no free page was left for a sequence */
 #define TFX_CACHE_BAD 2        /* a slot, page or offset out of range, or a fork onto a slot in use */
@@ -112,6 +136,16 @@ int tfx_cache_append(tfx_cache* c, int layer, const void* k, int64_t ldk, const 
 int tfx_cache_append_listed(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
                             const int32_t* seqs, const int32_t* offsets, int n, cudaStream_t stream);
 
+/* Rows of a layer's K and V out of the cache, in act: row t of k and v, offsets[i] <=
+ * t < offsets[i+1], is token starts[i] + t - offsets[i] of sequence seqs[i] (device
+ * lists; n sequences, any of them several times; n+1 offsets, not decreasing). Values
+ * of the 8-bit stores are rounded to act once (I8: exact but for FP16's range).
+ * Rows outside the lists, and rows of the list past `rows`, are not touched; a row
+ * whose sequence does not hold its token gets zeros and leaves TFX_CACHE_BAD.
+ * ldk, ldv as in tfx_cache_append. k and v must not overlap the cache. */
+int tfx_cache_read(tfx_cache* c, int layer, const int32_t* seqs, const int32_t* starts, const int32_t* offsets, int n,
+                   int rows, void* k, int64_t ldk, void* v, int64_t ldv, cudaStream_t stream);
+
 /* dst[i] becomes a copy of sequence src[i] (device lists; dst distinct, empty
  * slots that are in no src): full pages are shared, a last page that is partly
  * filled is copied to the free page of lowest number, in the order of the list. */
@@ -141,7 +175,11 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * that attends to as many of them as its length says (what it does not hold of
  * them must then be finite). A sequence that holds no token, or a slot out of
  * range, gives zeros. h->heads_kv, dim and act are the cache's. Same arithmetic as
- * tfx_attn_prompt, with partial results of FP32 joined in a fixed order. */
+ * tfx_attn_prompt, with partial results of FP32 joined in a fixed order.
+ * Over an 8-bit store, whole blocks of the first `shared` tokens are read through the
+ * one table, the tokens behind the last whole block through each sequence's own; q
+ * and the probabilities (times a block's scale) are matrix operands of FP16, q of
+ * BF16 after a power of two that brings the row's largest magnitude below 2^15. */
 int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void* q, int64_t ldq, const int32_t* seqs,
                     int batch, int shared, void* out, int64_t ldo, cudaStream_t stream);
 
