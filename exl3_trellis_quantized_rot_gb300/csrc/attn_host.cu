@@ -64,16 +64,19 @@ int check_rows(const char* what, const void* p, int64_t ld, int64_t width) {
   return 0;
 }
 
-int encode_map(CUtensorMap* tm, const void* base, int act, const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4],
+int encode_map(CUtensorMap* tm, const void* base, CUtensorMapDataType type, const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4],
                const cuuint32_t (&box)[5]) {
   const tfx::EncodeTiled enc = tfx::tensor_map_encoder();
   if (!enc) return fail_with(TFX_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  const CUresult r = enc(tm, act == TFX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
-                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUresult r = enc(tm, type, 5, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail_with(TFX_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return 0;
+}
+
+CUtensorMapDataType type_of(int act) {
+  return act == TFX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
 // K or V as (64 values, tokens, dim/64 column blocks, heads, pages), in boxes of
@@ -83,7 +86,17 @@ int make_map(CUtensorMap* tm, const void* base, int act, int dim, int heads, int
   const cuuint64_t dims[5] = {64, (cuuint64_t)tokens, (cuuint64_t)dim / 64, (cuuint64_t)heads, (cuuint64_t)pages};
   const cuuint64_t strides[4] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)dim * 2, (cuuint64_t)page_pitch * 2};
   const cuuint32_t box[5] = {64, (cuuint32_t)box_tokens, (cuuint32_t)box_blocks, 1, 1};
-  return encode_map(tm, base, act, dims, strides, box);
+  return encode_map(tm, base, type_of(act), dims, strides, box);
+}
+
+// Pages of 8-bit codes as (128 codes, tokens, dim/128 column blocks, heads, pages), in boxes
+// of 16 tokens of one head.
+int make_code_map(CUtensorMap* tm, const void* base, const tfx_cache* c) {
+  const cuuint64_t row = (cuuint64_t)c->heads_kv * c->dim;
+  const cuuint64_t dims[5] = {128, (cuuint64_t)c->page_size, (cuuint64_t)c->dim / 128, (cuuint64_t)c->heads_kv, (cuuint64_t)c->pages};
+  const cuuint64_t strides[4] = {row, 128, (cuuint64_t)c->dim, row * c->page_size};
+  const cuuint32_t box[5] = {128, TFX_CACHE_BLOCK, (cuuint32_t)c->dim / 128, 1, 1};
+  return encode_map(tm, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box);
 }
 
 // Q as (64 values, heads, tokens, dim/64 column blocks), in boxes of one column
@@ -93,7 +106,7 @@ int make_q_map(CUtensorMap* tm, const void* base, int act, int dim, int heads, i
   const cuuint64_t dims[5] = {64, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)dim / 64, 1};
   const cuuint64_t strides[4] = {(cuuint64_t)dim * 2, (cuuint64_t)ld * 2, 128, 16};
   const cuuint32_t box[5] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1, 1};
-  return encode_map(tm, base, act, dims, strides, box);
+  return encode_map(tm, base, type_of(act), dims, strides, box);
 }
 
 // Query heads of one K/V head that share a 128-row tile: the most that divide
@@ -287,7 +300,7 @@ DecodeScratch decode_scratch(int batch, int heads_q, int heads_kv, int dim, int 
   d.bytes = (size_t)at;
   return d;
 }
-int decode_warps() { return tfx::multiprocessors() * 4; }
+int decode_warps(const tfx_cache* c) { return tfx::multiprocessors() * (c->store == TFX_STORE_ACT ? 4 : tfx::kCodedWarps); }
 
 // Rows of the given lists (null: the last extend's).
 int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
@@ -415,7 +428,7 @@ int tfx_cache_reserve(tfx_cache* c, int max_batch, int heads_q, cudaStream_t str
     return fail_with(TFX_ECUDA, "clearing %zu bytes failed", page_scratch_ints(c) * 4);
   }
   const int b = max_batch > pv->max_batch ? max_batch : pv->max_batch, hq = heads_q > pv->heads_q ? heads_q : pv->heads_q;
-  const size_t part = decode_scratch(b, hq, c->heads_kv, c->dim, decode_warps()).bytes;
+  const size_t part = decode_scratch(b, hq, c->heads_kv, c->dim, decode_warps(c)).bytes;
   if ((rc = grow(reinterpret_cast<void**>(&pv->part), &pv->part_bytes, part, stream))) return rc;
   pv->max_batch = b;
   pv->heads_q = hq;
@@ -555,7 +568,11 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   const bool coded = c->store != TFX_STORE_ACT;
   const int64_t ld = (int64_t)c->heads_kv * c->dim;
   const void *kl = layer_of<const void>(c, c->k, layer), *vl = layer_of<const void>(c, c->v, layer);
-  if (!coded) {
+  if (coded) {
+    if ((rc = make_code_map(&a.k, kl, c)) || (rc = make_code_map(&a.v, vl, c))) return rc;
+    a.k_scale = scales_of(c, c->k_scale, layer);
+    a.v_scale = scales_of(c, c->v_scale, layer);
+  } else {
     if ((rc = make_map(&a.k, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
     if ((rc = make_map(&a.v, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), 16, c->dim / 64))) return rc;
   }
@@ -577,14 +594,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.pages = c->pages;
   a.slots = c->slots;
   a.width = c->width;
-  if (coded) {
-    a.codes_k = static_cast<const uint8_t*>(kl);
-    a.codes_v = static_cast<const uint8_t*>(vl);
-    a.k_scale = scales_of(c, c->k_scale, layer);
-    a.v_scale = scales_of(c, c->v_scale, layer);
-    return tfx::launch_decode_q8(a, c->act, c->store, c->dim, stream);
-  }
-  if (many_rows(batch, a.group) && shared >= 256) {
+  if (!coded && many_rows(batch, a.group) && shared >= 256) {
     a.per_tile = heads_per_tile(a.group);
     a.tokens = 128 / a.per_tile;
     const int most = 2 * a.tokens, tiles = (batch + most - 1) / most;
@@ -599,7 +609,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
     if ((rc = make_map(&a.kt, kl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), box, 1))) return rc;
     if ((rc = make_map(&a.vt, vl, c->act, c->dim, c->heads_kv, c->page_size, ld, c->pages, page_values(c), box, 1))) return rc;
   }
-  a.warps = decode_warps();
+  a.warps = decode_warps(c);
   a.own_rows = a.group < kRowTile ? a.group : kRowTile;
   const DecodeScratch d = decode_scratch(batch, h->heads_q, c->heads_kv, c->dim, a.warps);
   if (d.bytes > pv->part_bytes)
@@ -613,7 +623,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.spin = tfx::spin_limit();
   if (!a.err) return fail_with(TFX_ECUDA, "no device error word");
   if (a.pre_splits && (rc = tfx::launch_prefix(a, c->act, c->dim, stream))) return rc;
-  return tfx::launch_decode(a, c->act, c->dim, stream);
+  return coded ? tfx::launch_decode_q8(a, c->act, c->store, c->dim, stream) : tfx::launch_decode(a, c->act, c->dim, stream);
 }
 
 int tfx_attn_debug_error(int* device_error) {

@@ -10,6 +10,7 @@
 
 namespace tfx {
 
+constexpr int kCodedWarps = 8;     // of a CTA of the decode kernel over 8-bit codes
 constexpr int kAttnMaxSeqs = 512;  // sequences of one prompt launch (longer lists take several launches)
 
 // Work of one prompt launch, in the kernel's parameters: nothing is copied to
@@ -68,9 +69,7 @@ struct DecodeAttnArgs {
   float2* pre_ml;
   int* err;
   long long spin;
-  // 8-bit stores: the layer's codes and scales
-  const uint8_t *codes_k, *codes_v;
-  const float *k_scale, *v_scale;
+  const float *k_scale, *v_scale;  // 8-bit stores: the layer's
 };
 
 // What appends need to know of the extends before them. Only an extend writes it,
@@ -143,6 +142,7 @@ int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStrea
 int launch_prompt(const PromptArgs& a, int act, int dim, cudaStream_t s);
 int launch_prefix(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
+int launch_join(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
 
 // exl3_host.cu

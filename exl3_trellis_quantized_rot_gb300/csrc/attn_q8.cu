@@ -1,99 +1,475 @@
 // Attention of single tokens over a cache of 8-bit codes.
 //
-//   s_j = scale q . c_j ks(j),  p = softmax(s),  o = sum_j p_j vs(j) d_j,
-// c_j, d_j the codes of K and V, ks and vs the scales of their blocks of 16 tokens.
-#include <cuda_runtime.h>
+//   s_j = scale log2(e) q . c_j ks(j),  p_j = 2^(s_j - m),  l = sum_j p_j,
+//   o = sum_j p_j vs(j) d_j / l,
+// c_j, d_j the codes of K and V, ks and vs the scales of their blocks of 16 tokens, one
+// pass over the keys. Codes become FP16 exactly, and FP16 MMAs take them: the scale of K is a
+// factor of a block's scores, that of V goes into the other operand,
+//   w_j = p_j vs(j) = 2^(s_j + log2 vs(j) - M),
+// with a running reference M of its own (the largest s_j + log2 vs(j)), so that blocks of any
+// size of V, zeros too, leave w in FP16's range; o is brought to m where a partial result is
+// stored. l sums the p_j in FP32.
+//
+// The keys are the MMAs' 16 rows and the query rows their 8 columns, S^T = K Q^T and
+// O^T = V^T W^T: the 6 rows of a K/V head of a 24/4 layout cost half of what 16 rows by 8
+// keys would, in MMAs and in registers of O. A contraction may take its index in any order, so
+// a lane's four consecutive bytes of K stand for k = 2t, 2t+1, 2t+8, 2t+9 of the fragment, and
+// q is loaded to match; transposed 16-bit matrix loads of V give a lane two dims of two keys,
+// which the conversion to FP16 takes apart: even dims are rows 0-7 of V^T, odd ones 8-15.
+//
+// A warp owns its rows, its slices (8 KB of K and V of one K/V head: 16 keys of 256, 32 of
+// 128) and a ring of three of them, which it fills itself, a slice as soon as one is done.
+// Every warp gets the same number of slices, as in attn_warp.cu; decode_join_kernel joins.
+#include <cuda_fp16.h>
 
-#include "attn_device.cuh"
+#include "attn_split.cuh"
 #include "codes.cuh"
 
 namespace tfx {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kCodedWarps;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr int kFewest = 2;     // slices a warp takes at least
+constexpr float kShift = 7.f;  // the largest weight is 2^kShift: 11 bits down to 2^-21 of it
 
-// One CTA per (sequence, query head): a warp every fourth token, a lane D/32 values.
-template <typename T, int Store, int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_q8_kernel(const __grid_constant__ DecodeAttnArgs a) {
-  constexpr int V = D / 32;
-  __shared__ float so[kWarps][D];
-  __shared__ float2 sml[kWarps];
-  griddep_wait();
-  griddep_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = blockIdx.x / a.heads_q, head = blockIdx.x - i * a.heads_q, kvh = head / a.group;
-  const int len = seq_len(a, i);
-  const int* shared_table = prefix_table(a);
-  const int* table = len ? a.tables + (long long)a.seqs[i] * a.width : shared_table;
-  const T* qr = reinterpret_cast<const T*>(a.q) + (long long)i * a.ldq + (long long)head * D + lane * V;
-  float q[V], o[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int c = 0; c < V; c++) {
-    q[c] = (float)qr[c] * a.scale_log2;
-    o[c] = 0.f;
-  }
-  for (int j = warp; j < len; j += kWarps) {
-    const int page = (j < a.shared ? shared_table : table)[j >> a.page_shift];
-    if ((unsigned)page >= (unsigned)a.pages) continue;
-    const long long tok = ((long long)page << a.page_shift) + (j & (a.page_size - 1));
-    const long long at = (tok * a.heads_kv + kvh) * D + lane * V;
-    const float ks = a.k_scale[tok / 16 * a.heads_kv + kvh], vs = a.v_scale[tok / 16 * a.heads_kv + kvh];
-    float dot = 0.f;
-#pragma unroll
-    for (int w = 0; w < V / 4; w++) {
-      float f[4];
-      values4<Store>(*reinterpret_cast<const uint32_t*>(a.codes_k + at + 4 * w), f);
-#pragma unroll
-      for (int c = 0; c < 4; c++) dot += q[4 * w + c] * f[c];
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
-    const float s = dot * ks, mn = fmaxf(m, s), keep = exp2_fast(m - mn), p = exp2_fast(s - mn);
-    m = mn;
-    l = l * keep + p;
-#pragma unroll
-    for (int w = 0; w < V / 4; w++) {
-      float f[4];
-      values4<Store>(*reinterpret_cast<const uint32_t*>(a.codes_v + at + 4 * w), f);
-#pragma unroll
-      for (int c = 0; c < 4; c++) o[4 * w + c] = o[4 * w + c] * keep + p * vs * f[c];
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < V; c++) so[warp][lane * V + c] = o[c];
-  if (lane == 0) sml[warp] = make_float2(m, l);
-  __syncthreads();
-  float mn = -INFINITY, sum = 0.f;
-  for (int k = 0; k < kWarps; k++) mn = fmaxf(mn, sml[k].x);
-  const float ref = mn == -INFINITY ? 0.f : mn;
-  for (int k = 0; k < kWarps; k++) sum += sml[k].y * exp2_fast(sml[k].x - ref);
-  T* out = reinterpret_cast<T*>(a.out) + (long long)i * a.ldo + (long long)head * D;
-  for (int c = threadIdx.x * 2; c < D; c += kWarps * 64) {
-    float x = 0.f, y = 0.f;
-    for (int k = 0; k < kWarps; k++) {
-      const float f = exp2_fast(sml[k].x - ref);
-      x += so[k][c] * f;
-      y += so[k][c + 1] * f;
-    }
-    // a sequence without tokens: zeros
-    *reinterpret_cast<uint32_t*>(out + c) = len == 0 ? 0u : pack2<T>(x / sum, y / sum);
+template <int D>
+struct Slice {
+  static constexpr int kKeys = 4096 / D;  // 16 (D = 256) or 32 (D = 128)
+  static constexpr int kBlocks = kKeys / 16;
+  static constexpr int kHalf = 4096;      // bytes of K (or V)
+  static constexpr int kBlock = 16 * D;   // bytes of one copy of 16 tokens
+  static constexpr int kStage = 2 * kHalf;
+};
+constexpr size_t kSmem = (size_t)kWarps * kStages * 8192 + 1024;
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 matrix of 16-bit values over the warp, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// The four codes of a word as FP16: bytes (0, 1) and (2, 3), or (0, 2) and (1, 3).
+template <int Store, bool Split>
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& a, uint32_t& b) {
+  if constexpr (Store == TFX_STORE_I8) {
+    // 0x64xx is 1024 + xx
+    w ^= 0x80808080u;
+    const uint32_t x = __byte_perm(w, 0x64646464u, Split ? 0x4240 : 0x4140);
+    const uint32_t y = __byte_perm(w, 0x64646464u, Split ? 0x4341 : 0x4342);
+    const __half2 by = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), by);
+    const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), by);
+    a = *reinterpret_cast<const uint32_t*>(&p);
+    b = *reinterpret_cast<const uint32_t*>(&q);
+  } else {
+    if (Split) w = __byte_perm(w, 0, 0x3120);
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi; }"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
   }
 }
 
+// log2 of a scale, NaN of a NaN.
+__device__ __forceinline__ float log2_scale(float s) {
+  return s == s ? (float)((int)(__float_as_uint(s) >> 23) - 127) : s;
+}
+
+// 8 * NT rows of a warp; a lane has columns 2t and 2t + 1 of each 8.
+template <int NT, int D>
+struct Rows {
+  uint32_t q[NT][D / 16][2];  // m16n8k16 B fragments
+  float o[NT][D / 16][4];     // O^T: dims 16 i + 2 g (elements 0, 1) and + 1 (2, 3)
+  float m[NT][2], M[NT][2], l[NT][2];
+  float by[NT][2];  // factor of the scores
+  int hi[NT][2];    // keys the row sees end here
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+      for (int i = 0; i < D / 16; i++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) o[n][i][c] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        m[n][c] = M[n][c] = -INFINITY;
+        l[n][c] = 0.f;
+      }
+    }
+  }
+  // Row g of 8 rows; null: zeros. BF16 rows become FP16 under a power of two that brings their
+  // largest magnitude to [2^14, 2^15).
+  template <typename T>
+  __device__ __forceinline__ void load(int n, const T* row, float scale, int lane) {
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) {
+      const uint2 x = row ? *reinterpret_cast<const uint2*>(row + 16 * i + 4 * (lane & 3)) : make_uint2(0, 0);
+      q[n][i][0] = x.x;
+      q[n][i][1] = x.y;
+    }
+    by[n][0] = by[n][1] = scale;
+    if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < D / 16; i++)
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+          top = max(top, max(q[n][i][c] & 0x7fffu, q[n][i][c] >> 16 & 0x7fffu));
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
+      const uint32_t e = max(top >> 7, 15u);  // of the largest magnitude; at least 2^-112
+      const float up = __uint_as_float((268u - e) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 16; i++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          const float2 f = pair_to_float(q[n][i][c], T());
+          q[n][i][c] = pack2<__half>(f.x * up, f.y * up);
+        }
+      const float back = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+      for (int c = 0; c < 2; c++) by[n][c] *= __shfl_sync(~0u, back, 4 * (2 * (lane & 3) + c));
+    }
+  }
+};
+
+// A warp's ring, and what of its slices is asked for.
+template <int D, int Rows>
+struct Ring {
+  static constexpr int NB = Slice<D>::kBlocks;
+  uint8_t* buf;
+  uint64_t* full;
+  float* scales;    // [kStages][K, V][NB]
+  int got = 0;      // slices taken so far: stage got % kStages, phase got / kStages
+  int asked = 0;    // slices asked for
+  long long x, end;
+  int s, s1, head;  // the next one to ask for
+  const int* table;
+  int page[NB];     // its pages
+
+  __device__ __forceinline__ void look(const DecodeAttnArgs& a) {
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      const int p = (s * Slice<D>::kKeys + 16 * b) >> a.page_shift;
+      page[b] = p < a.width ? __ldg(table + p) : -1;
+    }
+  }
+  __device__ __forceinline__ void begin(const DecodeAttnArgs& a, const Walk& w, const int* starts) {
+    if (x >= end) return;
+    const Segment g = segment_at<Slice<D>::kKeys, Rows>(a, w, starts, x, end);
+    s = g.s0;
+    s1 = g.s1;
+    head = g.head;
+    table = g.table;
+    look(a);
+  }
+  // The next slice into its stage, whose last reads are behind the warp.
+  __device__ __forceinline__ void ask(const DecodeAttnArgs& a, const Walk& w, const int* starts, int lane) {
+    if (x >= end) return;
+    const int st = asked % kStages;
+    if (lane == 0) {
+      uint8_t* dst = buf + st * Slice<D>::kStage;
+      uint64_t* bar = full + st;
+      float* sc = scales + st * 2 * NB;
+#pragma unroll
+      for (int b = 0; b < NB; b++)
+        if ((unsigned)page[b] >= (unsigned)a.pages) sc[b] = sc[NB + b] = 1.f;
+      mbar_expect_tx(bar, Slice<D>::kStage);
+#pragma unroll
+      for (int b = 0; b < NB; b++) {
+        const int at = (s * Slice<D>::kKeys + 16 * b) & (a.page_size - 1);
+        const bool in = (unsigned)page[b] < (unsigned)a.pages;
+        const int p = in ? page[b] : -1;  // -1 is out of the map's range: zeros
+        tma_load_5d(dst + b * Slice<D>::kBlock, &a.k, 0, at, 0, head, p, bar);
+        tma_load_5d(dst + Slice<D>::kHalf + b * Slice<D>::kBlock, &a.v, 0, at, 0, head, p, bar);
+        if (in) {
+          const long long i = ((long long)p * (a.page_size / 16) + at / 16) * a.heads_kv + head;
+          copy4(sc + b, a.k_scale + i);
+          copy4(sc + NB + b, a.v_scale + i);
+        }
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s_addr(bar)) : "memory");
+    }
+    asked++;
+    x++;
+    if (++s < s1)
+      look(a);
+    else
+      begin(a, w, starts);
+  }
+  static __device__ __forceinline__ void copy4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_addr(dst)), "l"(src) : "memory");
+  }
+};
+
+// The rows against slices [s0, s1) of the keys lo <= key < hi. False: a wait gave up.
+template <int Store, int NT, int D>
+__device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, 8 * NT>& rg, const DecodeAttnArgs& a, const Walk& w,
+                                       const int* starts, int s0, int s1, int lo, int lane) {
+  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks;
+  const int g = lane >> 2, mi = lane >> 3, mr = lane & 7;
+  int hmin = INT_MAX, hmax = 0;
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+      hmin = min(hmin, R.hi[n][c]);
+      hmax = max(hmax, R.hi[n][c]);
+    }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    hmin = min(hmin, __shfl_xor_sync(~0u, hmin, d));
+    hmax = max(hmax, __shfl_xor_sync(~0u, hmax, d));
+  }
+  // 16-byte column c of a key's 8: where the copies' 128-byte swizzle put it
+  const int key = (mi & 1) * 8 + mr;
+  auto at = [&](int block, int c) {
+    return block * Slice<D>::kBlock + (c >> 3) * 2048 + key * 128 + (((c & 7) ^ (key & 7)) << 4);
+  };
+  for (int s = s0; s < s1; s++) {
+    const int st = rg.got % kStages;
+    // the warp gives up together: what follows wants all its lanes
+    if (!__all_sync(~0u, mbar_wait_bounded(rg.full + st, (rg.got / kStages) & 1, a.spin))) return false;
+    uint8_t* kb = rg.buf + st * Slice<D>::kStage;
+    uint8_t* vb = kb + Slice<D>::kHalf;
+    const float* sc = rg.scales + st * 2 * NB;
+    const int k0 = s * KS;
+    const bool edge = k0 < lo || k0 + KS > hmin;
+    // what no row may see: 0 * NaN would be NaN in the product, so V's codes there become zeros
+    if (k0 < lo || k0 + KS > hmax) {
+      for (int r = 0; r < KS; r++)
+        if (k0 + r < lo || k0 + r >= hmax)
+          for (int c = lane; c < D / 16; c += 32)
+            *reinterpret_cast<uint4*>(vb + (r >> 4) * Slice<D>::kBlock + (c >> 3) * 2048 + (r & 15) * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+      fence_async_smem();  // ordinary stores to memory that a later copy writes
+      __syncwarp();
+    }
+    float sx[NB][NT][4];
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      float s2[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) sx[b][n][c] = s2[n][c] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; i++) {
+        uint32_t r[4], x[4][2];
+        ldsm4(r, s_addr(kb) + at(b, 2 * i + (mi >> 1)));
+#pragma unroll
+        for (int j = 0; j < 4; j++) halves<Store, false>(r[j], x[j][0], x[j][1]);
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          mma(sx[b][n], x[0][0], x[1][0], x[0][1], x[1][1], R.q[n][2 * i][0], R.q[n][2 * i][1]);
+          mma(s2[n], x[2][0], x[3][0], x[2][1], x[3][1], R.q[n][2 * i + 1][0], R.q[n][2 * i + 1][1]);
+        }
+      }
+      const float ks = sc[b];
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 4; c++) sx[b][n][c] = (sx[b][n][c] + s2[n][c]) * (R.by[n][c & 1] * ks);
+      if (edge) {
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            const int k = k0 + b * 16 + g + (c >> 1) * 8;
+            if (k < lo || k >= R.hi[n][c & 1]) sx[b][n][c] = -INFINITY;
+          }
+      }
+    }
+    uint32_t p[NB][NT][2];  // W^T: m16n8k16 B fragments
+    float keep[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      float ref[2], off[NB][2];
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        float mn = R.m[n][c], Mn = R.M[n][c];
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+          float mx = fmaxf(sx[b][n][c], sx[b][n][c + 2]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+          mn = fmaxf(mn, mx);
+          // a block of which the row sees nothing may have any scale
+          off[b][c] = mx == -INFINITY ? 0.f : log2_scale(sc[NB + b]);
+          Mn = fmaxf(Mn, mx + off[b][c]);
+        }
+        ref[c] = mn == -INFINITY ? 0.f : mn;
+        const float Ref = Mn == -INFINITY ? 0.f : Mn;
+        keep[n][c] = exp2_fast(R.M[n][c] - Ref);
+        R.l[n][c] *= exp2_fast(R.m[n][c] - ref[c]);
+        R.m[n][c] = mn;
+        R.M[n][c] = Mn;
+#pragma unroll
+        for (int b = 0; b < NB; b++) off[b][c] += kShift - Ref;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; b++) {
+        float e[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          R.l[n][c & 1] += exp2_fast(sx[b][n][c] - ref[c & 1]);
+          e[c] = exp2_fast(sx[b][n][c] + off[b][c & 1]);
+        }
+        // the weights become matrix operands of FP16
+        p[b][n][0] = transposed(pack2<__half>(e[0], e[1]));
+        p[b][n][1] = transposed(pack2<__half>(e[2], e[3]));
+      }
+    }
+    bool move = false;
+#pragma unroll
+    for (int n = 0; n < NT; n++) move = move || keep[n][0] != 1.f || keep[n][1] != 1.f;
+    if (__any_sync(~0u, move)) {
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+#pragma unroll
+          for (int c = 0; c < 4; c++) R.o[n][i][c] *= keep[n][c & 1];
+    }
+#pragma unroll
+    for (int b = 0; b < NB; b++)
+#pragma unroll
+      for (int i = 0; i < D / 32; i++) {
+        uint32_t r[4], x[4][2];
+        ldsm4t(r, s_addr(vb) + at(b, 2 * i + (mi >> 1)));
+#pragma unroll
+        for (int j = 0; j < 4; j++) halves<Store, true>(r[j], x[j][0], x[j][1]);
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          mma(R.o[n][2 * i], x[0][0], x[0][1], x[1][0], x[1][1], p[b][n][0], p[b][n][1]);
+          mma(R.o[n][2 * i + 1], x[2][0], x[2][1], x[3][0], x[3][1], p[b][n][0], p[b][n][1]);
+        }
+      }
+    __syncwarp();
+    rg.got++;
+    rg.ask(a, w, starts, lane);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int c = 0; c < 2; c++)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) R.l[n][c] += __shfl_xor_sync(~0u, R.l[n][c], d);
+  return true;
+}
+
+template <typename T, int Store, int NT, int D>
+__global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const __grid_constant__ DecodeAttnArgs a) {
+  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks;
+  extern __shared__ uint8_t dyn[];
+  __shared__ uint64_t full[kWarps][kStages];
+  __shared__ float scales[kWarps][kStages * 2 * NB];
+  __shared__ int starts[TFX_ATTN_MAX_BATCH + 1];
+  __shared__ int wsum[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    // a slice's bytes, and its scales
+    for (int i = 0; i < kWarps * kStages; i++) mbar_init(&full[0][0] + i, 2);
+    fence_mbar_init();
+  }
+  griddep_wait();
+  const Walk w = walk_of<KS, 8 * NT>(a, sequence_starts<KS, kWarps>(a, starts, wsum));
+  const long long per = max((w.total + a.warps - 1) / a.warps, (long long)kFewest);
+  // neighbouring runs go to neighbouring CTAs: few runs still use every SM
+  const int me = warp * gridDim.x + blockIdx.x;
+  Ring<D, 8 * NT> rg;
+  rg.buf = dyn + ((1024u - (s_addr(dyn) & 1023u)) & 1023u) + warp * kStages * Slice<D>::kStage;
+  rg.full = full[warp];
+  rg.scales = scales[warp];
+  rg.x = me * per;
+  rg.end = min(rg.x + per, w.total);
+  long long x = rg.x;
+  const long long end = rg.end;
+  rg.begin(a, w, starts);
+  for (int i = 0; i < kStages; i++) rg.ask(a, w, starts, lane);
+  note_runs(a, w, starts, per);
+  griddep_launch();
+  const T* q = reinterpret_cast<const T*>(a.q);
+  Rows<NT, D> R;
+  bool ok = true;
+  while (ok && x < end) {
+    const Segment g = segment_at<KS, 8 * NT>(a, w, starts, x, end);
+    auto source = [&](int r, int* seq) {  // row r of the tile: its row of q, its sequence
+      const int row = g.row0 + (r < g.rows ? r : 0);
+      *seq = g.prefix ? row / a.group : g.seq;
+      const int head = g.head * a.group + (g.prefix ? row % a.group : row);
+      return r < g.rows ? q + (long long)*seq * a.ldq + (long long)head * D : nullptr;
+    };
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      int seq;
+      R.load(n, source(8 * n + (lane >> 2), &seq), a.scale_log2, lane);
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        const bool in = source(8 * n + 2 * (lane & 3) + c, &seq) != nullptr;
+        const int len = seq_len(a, seq);
+        R.hi[n][c] = !g.prefix ? len : in ? min(a.shared, len) : 0;
+      }
+    }
+    R.reset();
+    ok = attend<Store>(R, rg, a, w, starts, g.s0, g.s1, g.prefix ? 0 : a.shared, lane);
+    if (!ok) break;
+    const long long slot = me + g.group;
+    float* po = g.prefix ? a.pre_o + slot * 16 * D : a.own_o + slot * a.own_rows * D;
+    float2* pml = g.prefix ? a.pre_ml + slot * 16 : a.own_ml + slot * a.own_rows;
+    x += g.s1 - g.s0;
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        const int r = 8 * n + 2 * (lane & 3) + c;
+        if (r >= g.rows) continue;
+        if (lane < 4) pml[r] = make_float2(R.m[n][c], R.l[n][c]);
+        // o relative to m, in two steps that stay in FP32's range
+        const float by = R.m[n][c] == -INFINITY ? 0.f : exp2_fast(R.M[n][c] - R.m[n][c]);
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+          *reinterpret_cast<float2*>(po + (long long)r * D + i * 16 + 2 * (lane >> 2)) =
+              make_float2(R.o[n][i][c] * 0.0078125f * by, R.o[n][i][c + 2] * 0.0078125f * by);  // 2^-kShift
+      }
+  }
+  if (!ok) gave_up(a.err);
+}
+
+template <typename T, int Store, int NT, int D>
+int run_of(const DecodeAttnArgs& a, cudaStream_t s) {
+  const void* fn = (const void*)decode_q8_kernel<T, Store, NT, D>;
+  const int rc = opt_in_smem(fn, kSmem);
+  if (rc) return rc;
+  return launch_kernel(fn, dim3((unsigned)(a.warps / kWarps)), dim3(kThreads), kSmem, s, const_cast<DecodeAttnArgs*>(&a),
+                       dependent_launches(), 1);
+}
 template <typename T, int Store>
-const void* kernel_of(int dim) {
-  return dim == 128 ? (const void*)decode_q8_kernel<T, Store, 128> : (const void*)decode_q8_kernel<T, Store, 256>;
+int run_of(const DecodeAttnArgs& a, int dim, cudaStream_t s) {
+  // a prefix's rows fill 16 columns; a group of up to 8 rows does not
+  const bool few = a.group <= 8 && a.shared == 0;
+  if (dim == 128) return few ? run_of<T, Store, 1, 128>(a, s) : run_of<T, Store, 2, 128>(a, s);
+  return few ? run_of<T, Store, 1, 256>(a, s) : run_of<T, Store, 2, 256>(a, s);
 }
 
 }  // namespace
 
 int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s) {
-  const void* fn = store == TFX_STORE_I8
-                       ? act == TFX_F16 ? kernel_of<__half, TFX_STORE_I8>(dim) : kernel_of<__nv_bfloat16, TFX_STORE_I8>(dim)
-                   : act == TFX_F16 ? kernel_of<__half, TFX_STORE_E4M3>(dim)
-                                    : kernel_of<__nv_bfloat16, TFX_STORE_E4M3>(dim);
-  return launch_kernel(fn, dim3((unsigned)(a.batch * a.heads_q)), dim3(kWarps * 32), 0, s, const_cast<DecodeAttnArgs*>(&a),
-                       dependent_launches(), 1);
+  int rc;
+  if (store == TFX_STORE_I8)
+    rc = act == TFX_F16 ? run_of<__half, TFX_STORE_I8>(a, dim, s) : run_of<__nv_bfloat16, TFX_STORE_I8>(a, dim, s);
+  else
+    rc = act == TFX_F16 ? run_of<__half, TFX_STORE_E4M3>(a, dim, s) : run_of<__nv_bfloat16, TFX_STORE_E4M3>(a, dim, s);
+  return rc ? rc : launch_join(a, act, dim, s);
 }
 
 }  // namespace tfx

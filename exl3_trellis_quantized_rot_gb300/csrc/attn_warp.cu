@@ -24,6 +24,7 @@
 
 #include "attn_device.cuh"
 #include "attn_internal.h"
+#include "attn_split.cuh"
 
 namespace tfx {
 namespace {
@@ -45,18 +46,6 @@ constexpr size_t warp_smem() {
   return (size_t)kWarps * kStages * Slice<D>::kStage + 1024;
 }
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -108,72 +97,6 @@ struct Ring {
   int it = 0;  // slices so far: stage it % kStages, phase it / kStages
 };
 
-// A run of slices of one group: 16 rows of one K/V head against keys of one sequence.
-struct Segment {
-  bool prefix;
-  int s0, s1;    // slices, from the sequence's first token
-  int head;      // K/V head
-  int seq;       // of the batch; -1: the shared prefix
-  int row0;      // first row of the tile: of the batch's rows (prefix) or of the group's heads
-  int rows;
-  long long group;  // number of the group in its list
-  const int* table;
-};
-
-struct Walk {
-  long long pre_total, total;
-  int own, sp, tiles, ptiles;
-};
-template <int D>
-__device__ __forceinline__ Walk walk_of(const DecodeAttnArgs& a, int own) {
-  constexpr int KS = Slice<D>::kKeys;
-  Walk w;
-  w.own = own;
-  w.sp = a.pre_splits ? 0 : (a.shared + KS - 1) / KS;
-  w.tiles = (a.group + 15) / 16;
-  w.ptiles = (a.batch * a.group + 15) / 16;
-  w.pre_total = (long long)a.heads_kv * w.ptiles * w.sp;
-  w.total = w.pre_total + (long long)a.heads_kv * w.tiles * own;
-  return w;
-}
-
-// The segment that begins with slice x of those before `end`.
-template <int D>
-__device__ __forceinline__ Segment segment_at(const DecodeAttnArgs& a, const Walk& w, const int* starts, long long x,
-                                              long long end) {
-  Segment g;
-  g.prefix = x < w.pre_total;
-  if (g.prefix) {
-    const int grp = (int)(x / w.sp);
-    g.group = grp;
-    g.s0 = (int)(x % w.sp);
-    g.s1 = (int)min((long long)w.sp, g.s0 + (end - x));
-    g.head = grp / w.ptiles;
-    g.seq = -1;
-    g.row0 = grp % w.ptiles * 16;
-    g.rows = min(16, a.batch * a.group - g.row0);
-    g.table = prefix_table(a);
-  } else {
-    const long long y = x - w.pre_total;
-    const int hr = (int)(y / w.own), z = (int)(y % w.own);
-    int lo = 0, hi = a.batch - 1;  // the sequence that slice z belongs to
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (starts[mid + 1] > z) hi = mid; else lo = mid + 1;
-    }
-    const int off = a.shared / Slice<D>::kKeys;
-    g.seq = lo;
-    g.group = (long long)hr * a.batch + lo;
-    g.s0 = z - starts[lo] + off;
-    g.s1 = (int)min((long long)(starts[lo + 1] - starts[lo] + off), g.s0 + (end - x));
-    g.head = hr / w.tiles;
-    g.row0 = hr % w.tiles * 16;
-    g.rows = min(16, a.group - g.row0);
-    g.table = a.tables + (long long)a.seqs[lo] * a.width;  // it has slices, so its slot is in range
-  }
-  return g;
-}
-
 // One lane: the slices [x, end) into a ring, in order.
 template <int D>
 __device__ __forceinline__ bool feed(const DecodeAttnArgs& a, const Walk& w, const int* starts, Ring& rg, long long x,
@@ -184,7 +107,7 @@ __device__ __forceinline__ bool feed(const DecodeAttnArgs& a, const Walk& w, con
     return p < a.width ? __ldg(table + p) : -1;
   };
   while (x < end) {
-    const Segment g = segment_at<D>(a, w, starts, x, end);
+    const Segment g = segment_at<Slice<D>::kKeys, 16>(a, w, starts, x, end);
     int next = page_at(g.table, g.s0 * KS);
     for (int s = g.s0; s < g.s1; s++) {
       const int page0 = next, st = rg.it % kStages;
@@ -352,14 +275,6 @@ __device__ __forceinline__ bool attend(Rows<T, D>& R, Ring& rg, int s0, int s1, 
   return true;
 }
 
-// After a wait that gave up: the error word, and time for the copies in flight to land.
-__device__ __forceinline__ void gave_up(int* err) {
-  atomicExch(err, 1);
-  const long long t0 = clock64();
-  while (clock64() - t0 < 2000000) {
-  }
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_constant__ DecodeAttnArgs a) {
   constexpr int KS = Slice<D>::kKeys;
@@ -374,47 +289,14 @@ __global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_cons
       mbar_init(&empty[0][0] + i, 1);
     }
     fence_mbar_init();
-    starts[0] = 0;
   }
   // after the tensor-core kernel, this one starts where that leaves room: they
   // share no memory that is written, and that one lets this one start only when
   // all that came before has ended
   if (!a.pre_splits) griddep_wait();
-  // own slices before each sequence
-  int carry = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWarps * 32) {
-    const int i = b0 + threadIdx.x;
-    const int len = warp < kWarps && i < a.batch ? seq_len(a, i) : 0;
-    int x = len > a.shared ? (len + KS - 1) / KS - a.shared / KS : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(~0u, x, d);
-      if (lane >= d) x += y;
-    }
-    if (lane == 31 && warp < kWarps) wsum[warp] = x;
-    __syncthreads();
-    int before = carry, all = carry;
-    for (int w = 0; w < kWarps; w++) {
-      if (w < warp) before += wsum[w];
-      all += wsum[w];
-    }
-    if (warp < kWarps && i < a.batch) starts[i + 1] = before + x;
-    carry = all;
-    __syncthreads();
-  }
-  const Walk w = walk_of<D>(a, carry);
+  const Walk w = walk_of<KS, 16>(a, sequence_starts<KS, kWarps>(a, starts, wsum));
   const long long per = max((w.total + a.warps - 1) / a.warps, (long long)kFewest);
-  // for the join: the runs that hold a part of each group
-  {
-    const int pre = a.heads_kv * w.ptiles * (w.sp > 0), own = a.heads_kv * w.tiles * a.batch;
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < pre + own; i += gridDim.x * kThreads) {
-      const int y = i - pre, hr = y / a.batch, seq = y - hr * a.batch;
-      const long long x0 = i < pre ? (long long)i * w.sp : w.pre_total + (long long)hr * w.own + starts[seq];
-      const int n = i < pre ? w.sp : starts[seq + 1] - starts[seq];
-      const int first = (int)(x0 / per);
-      a.runs[i] = make_int2(first, n ? (int)((x0 + n - 1) / per) - first + 1 : 0);
-    }
-  }
+  note_runs(a, w, starts, per);
   griddep_launch();
   uint8_t* base = dyn + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
   auto ring_of = [&](int r) {
@@ -441,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_cons
     Rows<T, D> R;
     Segment g;
     auto begin = [&]() {  // the segment at x: its rows of q are asked for
-      g = segment_at<D>(a, w, starts, x, end);
+      g = segment_at<Slice<D>::kKeys, 16>(a, w, starts, x, end);
       const T* rp[2];
 #pragma unroll
       for (int h = 0; h < 2; h++) {
@@ -574,18 +456,27 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
 }
 
 template <typename T, int D>
+int join_of(const DecodeAttnArgs& a, cudaStream_t s) {
+  return launch_kernel((const void*)decode_join_kernel<T, D>, dim3((unsigned)(a.batch * a.heads_q)), dim3(kWarps * 32), 0,
+                       s, const_cast<DecodeAttnArgs*>(&a), dependent_launches(), 1);
+}
+
+template <typename T, int D>
 int decode_of(const DecodeAttnArgs& a, cudaStream_t s) {
   const void* fn = (const void*)decode_warp_kernel<T, D>;
   int rc = opt_in_smem(fn, warp_smem<D>());
   if (rc) return rc;
   rc = launch_kernel(fn, dim3((unsigned)(a.warps / kWarps)), dim3(kThreads), warp_smem<D>(), s,
                      const_cast<DecodeAttnArgs*>(&a), dependent_launches(), 1);
-  if (rc) return rc;
-  return launch_kernel((const void*)decode_join_kernel<T, D>, dim3((unsigned)(a.batch * a.heads_q)), dim3(kWarps * 32), 0,
-                       s, const_cast<DecodeAttnArgs*>(&a), dependent_launches(), 1);
+  return rc ? rc : join_of<T, D>(a, s);
 }
 
 }  // namespace
+
+int launch_join(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s) {
+  if (act == TFX_F16) return dim == 128 ? join_of<__half, 128>(a, s) : join_of<__half, 256>(a, s);
+  return dim == 128 ? join_of<__nv_bfloat16, 128>(a, s) : join_of<__nv_bfloat16, 256>(a, s);
+}
 
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s) {
   if (act == TFX_F16) return dim == 128 ? decode_of<__half, 128>(a, s) : decode_of<__half, 256>(a, s);
