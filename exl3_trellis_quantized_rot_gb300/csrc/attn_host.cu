@@ -64,13 +64,14 @@ int check_rows(const char* what, const void* p, int64_t ld, int64_t width) {
   return 0;
 }
 
-int encode_map(CUtensorMap* tm, const void* base, CUtensorMapDataType type, const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4],
-               const cuuint32_t (&box)[5]) {
+int encode_map(CUtensorMap* tm, const void* base, CUtensorMapDataType type, const cuuint64_t (&dims)[5],
+               const cuuint64_t (&strides)[4], const cuuint32_t (&box)[5],
+               CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   const tfx::EncodeTiled enc = tfx::tensor_map_encoder();
   if (!enc) return fail_with(TFX_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = enc(tm, type, 5, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail_with(TFX_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return 0;
 }
@@ -96,7 +97,9 @@ int make_code_map(CUtensorMap* tm, const void* base, const tfx_cache* c) {
   const cuuint64_t dims[5] = {128, (cuuint64_t)c->page_size, (cuuint64_t)c->dim / 128, (cuuint64_t)c->heads_kv, (cuuint64_t)c->pages};
   const cuuint64_t strides[4] = {row, 128, (cuuint64_t)c->dim, row * c->page_size};
   const cuuint32_t box[5] = {128, TFX_CACHE_BLOCK, (cuuint32_t)c->dim / 128, 1, 1};
-  return encode_map(tm, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box);
+  // a head's codes of a token are 128 or 256 bytes, and what lies beside them is another head's
+  return encode_map(tm, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box,
+                    c->dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // Q as (64 values, heads, tokens, dim/64 column blocks), in boxes of one column

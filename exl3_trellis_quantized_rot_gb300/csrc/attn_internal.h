@@ -142,7 +142,7 @@ int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStrea
 int launch_prompt(const PromptArgs& a, int act, int dim, cudaStream_t s);
 int launch_prefix(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
-int launch_join(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
+int launch_join(const DecodeAttnArgs& a, int act, int dim, bool wide, cudaStream_t s);
 int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
 
 // exl3_host.cu

@@ -469,7 +469,9 @@ int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaS
     rc = act == TFX_F16 ? run_of<__half, TFX_STORE_I8>(a, dim, s) : run_of<__nv_bfloat16, TFX_STORE_I8>(a, dim, s);
   else
     rc = act == TFX_F16 ? run_of<__half, TFX_STORE_E4M3>(a, dim, s) : run_of<__nv_bfloat16, TFX_STORE_E4M3>(a, dim, s);
-  return rc ? rc : launch_join(a, act, dim, s);
+  // where few rows have all the warps' partial results, a row's are joined by four times the warps
+  const bool wide = a.batch * a.heads_kv * 24LL < a.warps;
+  return rc ? rc : launch_join(a, act, dim, wide, s);
 }
 
 }  // namespace tfx

@@ -366,13 +366,13 @@ __global__ void __launch_bounds__(kThreads) decode_warp_kernel(const __grid_cons
 }
 
 // One CTA per (sequence, query head): the row's partial results, prefix first,
-// in slot order. Each warp joins every fourth one, then the four are joined.
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_constant__ DecodeAttnArgs a) {
+// in slot order. Each of W warps joins every W-th one, then theirs are joined.
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(W * 32) decode_join_kernel(const __grid_constant__ DecodeAttnArgs a) {
   constexpr int V = D / 32;  // values of a row per lane, as V/4 runs of 4
   constexpr int kBatch = 6;  // partial results in flight a warp
-  __shared__ float so[kWarps][D];
-  __shared__ float2 sml[kWarps];
+  __shared__ float so[W][D];
+  __shared__ float2 sml[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x / a.heads_q, head = blockIdx.x - i * a.heads_q;
   const int kvh = head / a.group, gh = head % a.group, r = i * a.group + gh;
@@ -390,12 +390,12 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
   const int shares = a.pre_splits, all = shares + first.y + own.y;
   const long long pre0 = (long long)(first.x + grp) * 16 + r % 16;
   const long long own0 = ((long long)own.x + (long long)hr * a.batch + i) * a.own_rows + gh % 16;
-  for (int z0 = warp; z0 < all; z0 += kWarps * kBatch) {
+  for (int z0 = warp; z0 < all; z0 += W * kBatch) {
     float2 ml[kBatch];
     float4 x[kBatch][V / 4];
 #pragma unroll
     for (int k = 0; k < kBatch; k++) {
-      const int z = min(z0 + k * kWarps, all - 1), y = z - shares;
+      const int z = min(z0 + k * W, all - 1), y = z - shares;
       const bool mine = y >= first.y;
       const long long row = y < 0    ? (long long)z * a.batch * a.heads_q + blockIdx.x
                             : mine ? own0 + (long long)(y - first.y) * a.own_rows
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
       const float* po = (mine ? a.own_o : a.pre_o) + row * D + lane * 4;
 #pragma unroll
       for (int c = 0; c < V / 4; c++) x[k][c] = *reinterpret_cast<const float4*>(po + c * 128);
-      if (z0 + k * kWarps >= all) ml[k] = make_float2(-INFINITY, 0.f);  // past the end: no weight
+      if (z0 + k * W >= all) ml[k] = make_float2(-INFINITY, 0.f);  // past the end: no weight
     }
     float mn = m;
 #pragma unroll
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
     for (int c = 0; c < V; c++) o[c] *= f;
 #pragma unroll
     for (int k = 0; k < kBatch; k++) {
-      if (z0 + k * kWarps >= all) break;
+      if (z0 + k * W >= all) break;
       const float g = exp2_fast(ml[k].x - ref);
       l += ml[k].y * g;
 #pragma unroll
@@ -433,20 +433,20 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
   for (int c = 0; c < V; c++) so[warp][(c >> 2) * 128 + lane * 4 + (c & 3)] = o[c];
   if (lane == 0) sml[warp] = make_float2(m, l);
   __syncthreads();
-  float mn = -INFINITY, sum = 0.f, f[kWarps];
-  for (int k = 0; k < kWarps; k++) mn = fmaxf(mn, sml[k].x);
+  float mn = -INFINITY, sum = 0.f, f[W];
+  for (int k = 0; k < W; k++) mn = fmaxf(mn, sml[k].x);
   const float ref = mn == -INFINITY ? 0.f : mn;
 #pragma unroll
-  for (int k = 0; k < kWarps; k++) {
+  for (int k = 0; k < W; k++) {
     f[k] = exp2_fast(sml[k].x - ref);
     sum += sml[k].y * f[k];
   }
   const float inv = 1.f / sum;
   T* out = reinterpret_cast<T*>(a.out) + (long long)i * a.ldo + (long long)head * D;
-  for (int c = threadIdx.x * 2; c < D; c += kWarps * 64) {
+  for (int c = threadIdx.x * 2; c < D; c += W * 64) {
     float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; k++) {
+    for (int k = 0; k < W; k++) {
       x += so[k][c] * f[k];
       y += so[k][c + 1] * f[k];
     }
@@ -455,10 +455,10 @@ __global__ void __launch_bounds__(kWarps * 32) decode_join_kernel(const __grid_c
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int W = kWarps>
 int join_of(const DecodeAttnArgs& a, cudaStream_t s) {
-  return launch_kernel((const void*)decode_join_kernel<T, D>, dim3((unsigned)(a.batch * a.heads_q)), dim3(kWarps * 32), 0,
-                       s, const_cast<DecodeAttnArgs*>(&a), dependent_launches(), 1);
+  return launch_kernel((const void*)decode_join_kernel<T, D, W>, dim3((unsigned)(a.batch * a.heads_q)), dim3(W * 32), 0, s,
+                       const_cast<DecodeAttnArgs*>(&a), dependent_launches(), 1);
 }
 
 template <typename T, int D>
@@ -473,7 +473,11 @@ int decode_of(const DecodeAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int launch_join(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s) {
+int launch_join(const DecodeAttnArgs& a, int act, int dim, bool wide, cudaStream_t s) {
+  if (wide) {
+    if (act == TFX_F16) return dim == 128 ? join_of<__half, 128, 16>(a, s) : join_of<__half, 256, 16>(a, s);
+    return dim == 128 ? join_of<__nv_bfloat16, 128, 16>(a, s) : join_of<__nv_bfloat16, 256, 16>(a, s);
+  }
   if (act == TFX_F16) return dim == 128 ? join_of<__half, 128>(a, s) : join_of<__half, 256>(a, s);
   return dim == 128 ? join_of<__nv_bfloat16, 128>(a, s) : join_of<__nv_bfloat16, 256>(a, s);
 }
