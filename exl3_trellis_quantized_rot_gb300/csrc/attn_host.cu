@@ -341,7 +341,7 @@ int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void*
   a.v_scale = scales_of(c, c->v_scale, layer);
   a.heads = c->heads_kv;
   a.rows = rows;
-  return tfx::launch_append_q8(a, c->act, c->store, c->dim, rows, stream);
+  return tfx::launch_append_q8(a, c->act, c->store, c->dim, stream);
 }
 
 }  // namespace

@@ -10,7 +10,7 @@
 
 namespace tfx {
 
-constexpr int kCodedWarps = 8;     // of a CTA of the decode kernel over 8-bit codes
+constexpr int kCodedWarps = 12;    // of a CTA of the decode kernel over 8-bit codes, at most
 constexpr int kAttnMaxSeqs = 512;  // sequences of one prompt launch (longer lists take several launches)
 
 // Work of one prompt launch, in the kernel's parameters: nothing is copied to
@@ -104,7 +104,7 @@ struct AppendArgs {
   int slots, width, pages, page_size;
   Grown grown;
   float *k_scale, *v_scale;  // 8-bit stores: the layer's
-  int heads, rows;
+  int heads, rows, per;  // per: rows of a CTA
 };
 
 struct ReadArgs {
@@ -116,7 +116,7 @@ struct ReadArgs {
   int n, rows;
   int* book;
   const int *lens, *table;
-  int slots, width, pages, page_size, heads, dim;
+  int slots, width, pages, page_size, heads, dim, per;  // per: rows of a CTA
 };
 
 enum Tables { kTablesNone = 0, kTablesFork = 1, kTablesCompact = 2 };
@@ -134,8 +134,8 @@ struct MoveArgs {
 
 int launch_extend(const BookArgs& a, cudaStream_t s);
 int launch_append(const AppendArgs& a, int rows, cudaStream_t s);
-int launch_append_q8(const AppendArgs& a, int act, int store, int dim, int rows, cudaStream_t s);
-int launch_read(const ReadArgs& a, int act, int store, cudaStream_t s);
+int launch_append_q8(AppendArgs& a, int act, int store, int dim, cudaStream_t s);
+int launch_read(ReadArgs& a, int act, int store, cudaStream_t s);
 int launch_free(const BookArgs& a, cudaStream_t s);
 int launch_move(const BookArgs* book, bool compact, const MoveArgs& m, cudaStream_t s);
 
@@ -143,7 +143,7 @@ int launch_prompt(const PromptArgs& a, int act, int dim, cudaStream_t s);
 int launch_prefix(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_join(const DecodeAttnArgs& a, int act, int dim, bool wide, cudaStream_t s);
-int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
+int launch_decode_q8(DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
 
 // exl3_host.cu
 tfx_exl3_driver driver_hooks();

@@ -28,9 +28,6 @@
 namespace tfx {
 namespace {
 
-constexpr int kWarps = kCodedWarps;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
 constexpr int kFewest = 2;     // slices a warp takes at least
 constexpr float kShift = 7.f;  // the largest weight is 2^kShift: 11 bits down to 2^-21 of it
 
@@ -42,11 +39,17 @@ struct Slice {
   static constexpr int kBlock = 16 * D;   // bytes of one copy of 16 tokens
   static constexpr int kStage = 2 * kHalf;
 };
-constexpr size_t kSmem = (size_t)kWarps * kStages * 8192 + 1024;
+// Warps of a CTA, and stages of each one's ring.
+template <int NT, int D>
+struct Shape {
+  static constexpr int kWarps = 8;
+  static constexpr int kStages = 3;
+};
+constexpr size_t kSmem = 24 * 8192 + 1024;
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -143,8 +146,9 @@ struct Rows {
 };
 
 // A warp's ring, and what of its slices is asked for.
-template <int D, int Rows>
+template <int D, int NT>
 struct Ring {
+  static constexpr int kStages = Shape<NT, D>::kStages, Rows = 8 * NT;
   static constexpr int NB = Slice<D>::kBlocks;
   uint8_t* buf;
   uint64_t* full;
@@ -213,9 +217,9 @@ struct Ring {
 
 // The rows against slices [s0, s1) of the keys lo <= key < hi. False: a wait gave up.
 template <int Store, int NT, int D>
-__device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, 8 * NT>& rg, const DecodeAttnArgs& a, const Walk& w,
+__device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const DecodeAttnArgs& a, const Walk& w,
                                        const int* starts, int s0, int s1, int lo, int lane) {
-  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks;
+  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks, kStages = Shape<NT, D>::kStages;
   const int g = lane >> 2, mi = lane >> 3, mr = lane & 7;
   int hmin = INT_MAX, hmax = 0;
 #pragma unroll
@@ -262,12 +266,14 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, 8 * NT>& rg, cons
       for (int n = 0; n < NT; n++)
 #pragma unroll
         for (int c = 0; c < 4; c++) sx[b][n][c] = s2[n][c] = 0.f;
+      uint32_t r[2][4];  // a step's codes are asked for a step ahead
+      ldsm4(r[0], s_addr(kb) + at(b, mi >> 1));
 #pragma unroll
       for (int i = 0; i < D / 32; i++) {
-        uint32_t r[4], x[4][2];
-        ldsm4(r, s_addr(kb) + at(b, 2 * i + (mi >> 1)));
+        uint32_t x[4][2];
+        if (i + 1 < D / 32) ldsm4(r[(i + 1) & 1], s_addr(kb) + at(b, 2 * (i + 1) + (mi >> 1)));
 #pragma unroll
-        for (int j = 0; j < 4; j++) halves<Store, false>(r[j], x[j][0], x[j][1]);
+        for (int j = 0; j < 4; j++) halves<Store, false>(r[i & 1][j], x[j][0], x[j][1]);
 #pragma unroll
         for (int n = 0; n < NT; n++) {
           mma(sx[b][n], x[0][0], x[1][0], x[0][1], x[1][1], R.q[n][2 * i][0], R.q[n][2 * i][1]);
@@ -341,19 +347,22 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, 8 * NT>& rg, cons
           for (int c = 0; c < 4; c++) R.o[n][i][c] *= keep[n][c & 1];
     }
 #pragma unroll
-    for (int b = 0; b < NB; b++)
+    for (int b = 0; b < NB; b++) {
+      uint32_t r[2][4];
+      ldsm4t(r[0], s_addr(vb) + at(b, mi >> 1));
 #pragma unroll
       for (int i = 0; i < D / 32; i++) {
-        uint32_t r[4], x[4][2];
-        ldsm4t(r, s_addr(vb) + at(b, 2 * i + (mi >> 1)));
+        uint32_t x[4][2];
+        if (i + 1 < D / 32) ldsm4t(r[(i + 1) & 1], s_addr(vb) + at(b, 2 * (i + 1) + (mi >> 1)));
 #pragma unroll
-        for (int j = 0; j < 4; j++) halves<Store, true>(r[j], x[j][0], x[j][1]);
+        for (int j = 0; j < 4; j++) halves<Store, true>(r[i & 1][j], x[j][0], x[j][1]);
 #pragma unroll
         for (int n = 0; n < NT; n++) {
           mma(R.o[n][2 * i], x[0][0], x[0][1], x[1][0], x[1][1], p[b][n][0], p[b][n][1]);
           mma(R.o[n][2 * i + 1], x[2][0], x[2][1], x[3][0], x[3][1], p[b][n][0], p[b][n][1]);
         }
       }
+    }
     __syncwarp();
     rg.got++;
     rg.ask(a, w, starts, lane);
@@ -368,8 +377,10 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, 8 * NT>& rg, cons
 }
 
 template <typename T, int Store, int NT, int D>
-__global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const __grid_constant__ DecodeAttnArgs a) {
+__global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, 1)
+    decode_q8_kernel(const __grid_constant__ DecodeAttnArgs a) {
   constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks;
+  constexpr int kWarps = Shape<NT, D>::kWarps, kStages = Shape<NT, D>::kStages;
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ float scales[kWarps][kStages * 2 * NB];
@@ -386,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const __grid_con
   const long long per = max((w.total + a.warps - 1) / a.warps, (long long)kFewest);
   // neighbouring runs go to neighbouring CTAs: few runs still use every SM
   const int me = warp * gridDim.x + blockIdx.x;
-  Ring<D, 8 * NT> rg;
+  Ring<D, NT> rg;
   rg.buf = dyn + ((1024u - (s_addr(dyn) & 1023u)) & 1023u) + warp * kStages * Slice<D>::kStage;
   rg.full = full[warp];
   rg.scales = scales[warp];
@@ -446,15 +457,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const __grid_con
 }
 
 template <typename T, int Store, int NT, int D>
-int run_of(const DecodeAttnArgs& a, cudaStream_t s) {
+int run_of(DecodeAttnArgs& a, cudaStream_t s) {
+  a.warps = multiprocessors() * Shape<NT, D>::kWarps;
   const void* fn = (const void*)decode_q8_kernel<T, Store, NT, D>;
   const int rc = opt_in_smem(fn, kSmem);
   if (rc) return rc;
-  return launch_kernel(fn, dim3((unsigned)(a.warps / kWarps)), dim3(kThreads), kSmem, s, const_cast<DecodeAttnArgs*>(&a),
+  return launch_kernel(fn, dim3((unsigned)multiprocessors()), dim3(Shape<NT, D>::kWarps * 32), kSmem, s, &a,
                        dependent_launches(), 1);
 }
 template <typename T, int Store>
-int run_of(const DecodeAttnArgs& a, int dim, cudaStream_t s) {
+int run_of(DecodeAttnArgs& a, int dim, cudaStream_t s) {
   // a prefix's rows fill 16 columns; a group of up to 8 rows does not
   const bool few = a.group <= 8 && a.shared == 0;
   if (dim == 128) return few ? run_of<T, Store, 1, 128>(a, s) : run_of<T, Store, 2, 128>(a, s);
@@ -463,7 +475,7 @@ int run_of(const DecodeAttnArgs& a, int dim, cudaStream_t s) {
 
 }  // namespace
 
-int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s) {
+int launch_decode_q8(DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s) {
   int rc;
   if (store == TFX_STORE_I8)
     rc = act == TFX_F16 ? run_of<__half, TFX_STORE_I8>(a, dim, s) : run_of<__nv_bfloat16, TFX_STORE_I8>(a, dim, s);

@@ -41,7 +41,7 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int t) {
   if (mark.y == x.end - x.begin && x.pos / a.page_size < a.width)
     page = a.table[(long long)s * a.width + x.pos / a.page_size];
   if (page < 0 || page >= a.pages) {
-    if (threadIdx.x == 0) atomicOr(&a.book[0], TFX_CACHE_BAD);
+    if ((threadIdx.x & 31) == 0) atomicOr(&a.book[0], TFX_CACHE_BAD);
     return x;
   }
   x.to = page * a.page_size + x.pos % a.page_size;

@@ -31,57 +31,76 @@ struct RopeArgs {
 };
 
 // One CTA per row. Items of a head: rotary/16 pairs of 16-byte words (half) or rotary/8
-// words (interleaved), then the words that are only copied.
+// words (interleaved), then the words that are only copied. A thread asks for its first items
+// before it works out the row's sines.
 template <typename T, bool Interleaved>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float cosine[kMostRotary / 2], sine[kMostRotary / 2];
+  constexpr int kAhead = Interleaved ? 4 : 2;
+  __shared__ __align__(16) float cosine[kMostRotary / 2], sine[kMostRotary / 2];
   griddep_wait();
   griddep_launch();
   const int t = blockIdx.x, half = a.rotary / 2;
-  const long long n = a.positions[t];
+  const int turned = Interleaved ? a.rotary / 8 : a.rotary / 16;
+  const int per = turned + (a.copy ? (a.dim - a.rotary) / 8 : 0);
+  const int all = (a.heads[0] + a.heads[1]) * per;
+  uint4 x[kAhead], y[Interleaved ? 1 : kAhead];
+  T* out[kAhead];
+  int word[kAhead];  // a copied one's: -1
+  auto ask = [&](int it0) {
+#pragma unroll
+    for (int n = 0; n < kAhead; n++) {
+      const int it = it0 + n * kThreads;
+      out[n] = nullptr;
+      if (it >= all) continue;
+      const int h = it / per, j = it - h * per, side = h >= a.heads[0];
+      const int at = (side ? h - a.heads[0] : h) * a.dim + (j < turned ? j * 8 : a.rotary + (j - turned) * 8);
+      const T* in = reinterpret_cast<const T*>(a.in[side]) + t * a.ld_in[side] + at;
+      out[n] = reinterpret_cast<T*>(a.out[side]) + t * a.ld_out[side] + at;
+      word[n] = j < turned ? j : -1;
+      x[n] = *reinterpret_cast<const uint4*>(in);
+      if (!Interleaved && j < turned) y[Interleaved ? 0 : n] = *reinterpret_cast<const uint4*>(in + half);
+    }
+  };
+  ask(threadIdx.x);
+  const long long position = a.positions[t];
   for (int i = threadIdx.x; i < half; i += kThreads) {
-    const uint64_t turn = (uint64_t)n * a.table[i];
+    const uint64_t turn = (uint64_t)position * a.table[i];
     float s, c;
     sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
     cosine[i] = c * a.gain;
     sine[i] = s * a.sine;
   }
   __syncthreads();
-  const int turned = Interleaved ? a.rotary / 8 : a.rotary / 16;
-  const int per = turned + (a.copy ? (a.dim - a.rotary) / 8 : 0);
-  const int all = (a.heads[0] + a.heads[1]) * per;
-  for (int it = threadIdx.x; it < all; it += kThreads) {
-    const int h = it / per, j = it - h * per, side = h >= a.heads[0];
-    const int head = side ? h - a.heads[0] : h;
-    const T* in = reinterpret_cast<const T*>(a.in[side]) + t * a.ld_in[side] + (long long)head * a.dim;
-    T* out = reinterpret_cast<T*>(a.out[side]) + t * a.ld_out[side] + (long long)head * a.dim;
-    if (j >= turned) {
-      const int c = a.rotary + (j - turned) * 8;
-      *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(in + c);
-    } else if (Interleaved) {
-      uint32_t x[4];
-      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(in + j * 8);
+  for (int it0 = threadIdx.x; it0 < all; it0 += kThreads * kAhead) {
+    if (it0 != threadIdx.x) ask(it0);
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const float2 f = pair_to_float(x[k], T());
-        const float c = cosine[j * 4 + k], s = sine[j * 4 + k];
-        x[k] = pack2<T>(f.x * c - f.y * s, f.y * c + f.x * s);
-      }
-      *reinterpret_cast<uint4*>(out + j * 8) = *reinterpret_cast<const uint4*>(x);
-    } else {
-      uint32_t x[4], y[4];
-      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(in + j * 8);
-      *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(in + half + j * 8);
+    for (int n = 0; n < kAhead; n++) {
+      if (!out[n]) continue;
+      uint32_t v[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      if (word[n] >= 0) {
+        if constexpr (Interleaved) {
+          const float4 c = *reinterpret_cast<const float4*>(cosine + word[n] * 4);
+          const float4 s = *reinterpret_cast<const float4*>(sine + word[n] * 4);
+          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const float2 f = pair_to_float(x[k], T()), g = pair_to_float(y[k], T());
-        const int i = j * 8 + 2 * k;
-        const float c0 = cosine[i], s0 = sine[i], c1 = cosine[i + 1], s1 = sine[i + 1];
-        x[k] = pack2<T>(f.x * c0 - g.x * s0, f.y * c1 - g.y * s1);
-        y[k] = pack2<T>(g.x * c0 + f.x * s0, g.y * c1 + f.y * s1);
+          for (int k = 0; k < 4; k++) {
+            const float2 f = pair_to_float(v[k], T());
+            v[k] = pack2<T>(f.x * cs[k] - f.y * sn[k], f.y * cs[k] + f.x * sn[k]);
+          }
+        } else {
+          uint32_t u[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const float2 f = pair_to_float(v[k], T()), g = pair_to_float(u[k], T());
+            const float2 c = *reinterpret_cast<const float2*>(cosine + word[n] * 8 + 2 * k);
+            const float2 s = *reinterpret_cast<const float2*>(sine + word[n] * 8 + 2 * k);
+            v[k] = pack2<T>(f.x * c.x - g.x * s.x, f.y * c.y - g.y * s.y);
+            u[k] = pack2<T>(g.x * c.x + f.x * s.x, g.y * c.y + f.y * s.y);
+          }
+          *reinterpret_cast<uint4*>(out[n] + half) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
       }
-      *reinterpret_cast<uint4*>(out + j * 8) = *reinterpret_cast<const uint4*>(x);
-      *reinterpret_cast<uint4*>(out + half + j * 8) = *reinterpret_cast<const uint4*>(y);
+      *reinterpret_cast<uint4*>(out[n]) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
 }
