@@ -39,7 +39,7 @@ def _sources():
     jobs.append((os.path.join(CSRC, "exl3_host.cu"), os.path.join(OUT, "exl3_host.o"), []))
     jobs.append((os.path.join(CSRC, "exl3_noalloc.cu"), os.path.join(OUT, "exl3_noalloc.o"), []))
     jobs.append((os.path.join(CSRC, "exl3_encode.cu"), os.path.join(OUT, "exl3_encode.o"), []))
-    for name in ("attn_host", "attn_tc", "attn_warp", "attn_q8", "cache_ops", "cache_q8", "rope"):
+    for name in ("attn_host", "attn_tc", "attn_warp", "attn_q8", "attn_q8_tc", "cache_ops", "cache_q8", "rope"):
         jobs.append((os.path.join(CSRC, name + ".cu"), os.path.join(OUT, name + ".o"), []))
     return deps, jobs
 

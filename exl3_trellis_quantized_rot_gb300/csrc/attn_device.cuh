@@ -181,6 +181,54 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Where a warp is in a ring of N barriers, and the parity it waits for there.
+template <int N>
+struct Turn {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// A CTA whose warps wait for one another: one that gives up takes the others along.
+struct Ctx {
+  volatile int* abort_flag;
+  int* err;
+  long long spin;
+};
+
+// The whole warp waits, its lanes together, as the warp-wide instructions that
+// follow want them: after a timeout too. Warps that have time to spare sleep NAP
+// ns between polls and leave issue slots and the shared-memory pipe to the softmax
+// warps beside them (48/8 heads of 128: 299 -> 288 us).
+template <int NAP>
+__device__ __forceinline__ bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(~0u, mbar_poll(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (true) {
+    for (int i = 0; i < 8; i++) {
+      if (NAP) __nanosleep(NAP);
+      if (__all_sync(~0u, mbar_poll(bar, parity))) return true;
+    }
+    const bool late = clock64() - t0 > c.spin;
+    if (late && (threadIdx.x & 31) == 0) {
+      *c.abort_flag = 1;
+      atomicExch(c.err, 1);
+    }
+    if (__any_sync(~0u, late || *c.abort_flag)) return false;
+  }
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // Tokens that sequence i of a decode batch holds; 0 for a slot out of range.
 __device__ __forceinline__ int seq_len(const DecodeAttnArgs& a, int i) {
   const int s = a.seqs[i];

@@ -597,6 +597,16 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.pages = c->pages;
   a.slots = c->slots;
   a.width = c->width;
+  if (coded && many_rows(batch, a.group) && a.shared >= 256) {
+    const int64_t rows = (int64_t)batch * a.group, per = tfx::prefix_q8_rows();
+    a.mt = (int)((rows + per - 1) / per);
+    const int64_t rest = (int64_t)c->heads_kv * a.mt, fill = tfx::multiprocessors() / rest, tiles = tfx::prefix_q8_tiles(a.shared);
+    a.pre_splits = (int)(fill < 1 ? 1 : fill > tiles ? tiles : fill);
+    if (rest * a.pre_splits > INT32_MAX) return fail_with(TFX_EUNSUPPORTED, "%lld tiles of rows", (long long)rest);
+    a.items = (int)(rest * a.pre_splits);
+    a.codes_k = static_cast<const uint8_t*>(kl);
+    a.codes_v = static_cast<const uint8_t*>(vl);
+  }
   if (!coded && many_rows(batch, a.group) && shared >= 256) {
     a.per_tile = heads_per_tile(a.group);
     a.tokens = 128 / a.per_tile;
@@ -625,7 +635,9 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.err = error_word();
   a.spin = tfx::spin_limit();
   if (!a.err) return fail_with(TFX_ECUDA, "no device error word");
-  if (a.pre_splits && (rc = tfx::launch_prefix(a, c->act, c->dim, stream))) return rc;
+  if (a.pre_splits && (rc = coded ? tfx::launch_prefix_q8(a, c->act, c->store, c->dim, stream)
+                                  : tfx::launch_prefix(a, c->act, c->dim, stream)))
+    return rc;
   return coded ? tfx::launch_decode_q8(a, c->act, c->store, c->dim, stream) : tfx::launch_decode(a, c->act, c->dim, stream);
 }
 

@@ -69,7 +69,8 @@ struct DecodeAttnArgs {
   float2* pre_ml;
   int* err;
   long long spin;
-  const float *k_scale, *v_scale;  // 8-bit stores: the layer's
+  const uint8_t *codes_k, *codes_v;  // 8-bit stores: the layer's pages and scales
+  const float *k_scale, *v_scale;
 };
 
 // What appends need to know of the extends before them. Only an extend writes it,
@@ -143,6 +144,9 @@ int launch_prompt(const PromptArgs& a, int act, int dim, cudaStream_t s);
 int launch_prefix(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_decode(const DecodeAttnArgs& a, int act, int dim, cudaStream_t s);
 int launch_join(const DecodeAttnArgs& a, int act, int dim, bool wide, cudaStream_t s);
+int prefix_q8_rows();            // rows of a tile of that kernel
+int prefix_q8_tiles(int shared);  // key tiles of the prefix
+int launch_prefix_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
 int launch_decode_q8(DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
 
 // exl3_host.cu

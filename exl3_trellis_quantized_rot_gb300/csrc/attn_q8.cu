@@ -60,32 +60,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return r;
 }
 
-// The four codes of a word as FP16: bytes (0, 1) and (2, 3), or (0, 2) and (1, 3).
-template <int Store, bool Split>
-__device__ __forceinline__ void halves(uint32_t w, uint32_t& a, uint32_t& b) {
-  if constexpr (Store == TFX_STORE_I8) {
-    // 0x64xx is 1024 + xx
-    w ^= 0x80808080u;
-    const uint32_t x = __byte_perm(w, 0x64646464u, Split ? 0x4240 : 0x4140);
-    const uint32_t y = __byte_perm(w, 0x64646464u, Split ? 0x4341 : 0x4342);
-    const __half2 by = __half2half2(__ushort_as_half(0x6480));  // 1152
-    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), by);
-    const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), by);
-    a = *reinterpret_cast<const uint32_t*>(&p);
-    b = *reinterpret_cast<const uint32_t*>(&q);
-  } else {
-    if (Split) w = __byte_perm(w, 0, 0x3120);
-    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi; }"
-        : "=r"(a), "=r"(b)
-        : "r"(w));
-  }
-}
-
-// log2 of a scale, NaN of a NaN.
-__device__ __forceinline__ float log2_scale(float s) {
-  return s == s ? (float)((int)(__float_as_uint(s) >> 23) - 127) : s;
-}
-
 // 8 * NT rows of a warp; a lane has columns 2t and 2t + 1 of each 8.
 template <int NT, int D>
 struct Rows {
@@ -129,8 +103,7 @@ struct Rows {
           top = max(top, max(q[n][i][c] & 0x7fffu, q[n][i][c] >> 16 & 0x7fffu));
       top = max(top, __shfl_xor_sync(~0u, top, 1));
       top = max(top, __shfl_xor_sync(~0u, top, 2));
-      const uint32_t e = max(top >> 7, 15u);  // of the largest magnitude; at least 2^-112
-      const float up = __uint_as_float((268u - e) << 23);
+      const float up = brings_up(top);
 #pragma unroll
       for (int i = 0; i < D / 16; i++)
 #pragma unroll
@@ -138,7 +111,7 @@ struct Rows {
           const float2 f = pair_to_float(q[n][i][c], T());
           q[n][i][c] = pack2<__half>(f.x * up, f.y * up);
         }
-      const float back = __uint_as_float((e - 14u) << 23);
+      const float back = inverse_of(up);
 #pragma unroll
       for (int c = 0; c < 2; c++) by[n][c] *= __shfl_sync(~0u, back, 4 * (2 * (lane & 3) + c));
     }
@@ -392,7 +365,8 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, 1)
     for (int i = 0; i < kWarps * kStages; i++) mbar_init(&full[0][0] + i, 2);
     fence_mbar_init();
   }
-  griddep_wait();
+  // after the tensor-core kernel, this one starts where that leaves room: see attn_warp.cu
+  if (!a.pre_splits) griddep_wait();
   const Walk w = walk_of<KS, 8 * NT>(a, sequence_starts<KS, kWarps>(a, starts, wsum));
   const long long per = max((w.total + a.warps - 1) / a.warps, (long long)kFewest);
   // neighbouring runs go to neighbouring CTAs: few runs still use every SM
@@ -454,6 +428,7 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, 1)
       }
   }
   if (!ok) gave_up(a.err);
+  if (a.pre_splits) griddep_wait();  // this grid's end says to the next that both are done
 }
 
 template <typename T, int Store, int NT, int D>
@@ -468,7 +443,7 @@ int run_of(DecodeAttnArgs& a, cudaStream_t s) {
 template <typename T, int Store>
 int run_of(DecodeAttnArgs& a, int dim, cudaStream_t s) {
   // a prefix's rows fill 16 columns; a group of up to 8 rows does not
-  const bool few = a.group <= 8 && a.shared == 0;
+  const bool few = a.group <= 8 && (a.shared == 0 || a.pre_splits);
   if (dim == 128) return few ? run_of<T, Store, 1, 128>(a, s) : run_of<T, Store, 2, 128>(a, s);
   return few ? run_of<T, Store, 1, 256>(a, s) : run_of<T, Store, 2, 256>(a, s);
 }

@@ -1,0 +1,528 @@
+// The shared prefix of a decode batch of many rows, over a cache of 8-bit codes, on the
+// tensor cores: tiles of 128 rows against 64 keys at a time, a CTA a tile and share of the keys.
+//
+// The mathematics is attn_q8.cu's: codes become FP16 operands exactly, K's scale is a factor
+// of a block's scores, V's goes into the weights, w_j = p_j vs(j), which have a reference of
+// their own. Here that one follows the running maximum only when it is passed by more than
+// 2^8 (weights reach 2^15), and a weight is p_j times one factor a block and row, except where
+// that factor would leave FP32's range: there the exponent is taken again.
+//
+// A row is a (sequence, query head) pair of one K/V head; 128 of them fill a tile however the
+// heads are grouped. Warps of a CTA: 0-3 softmax and results (a thread a row); 4-11 turn codes
+// into operands: 16 codes a lane and load, two tiles ahead in registers, as two 16-byte pieces
+// into the 128-byte swizzle; 12 issues the MMAs. Order of the MMAs: S0, S1, P0 V0, S2, P1 V1, ...
+// Tensor memory: O in columns 0..dim-1, two buffers of 64 columns for scores, whose first 32
+// take the weights.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_device.cuh"
+#include "codes.cuh"
+
+namespace tfx {
+namespace {
+
+constexpr int kSoft = 4, kConvert = 8;  // warps
+constexpr int kMmaWarp = kSoft + kConvert;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kKeys = 64, kRows = 128;
+constexpr int kBlocks = kKeys / 16;
+constexpr int kScaleTiles = 8;  // tiles whose scales are kept: stages and score buffers, and more
+constexpr float kShift = 7.f, kSlack = 8.f;
+constexpr float kMostFactor = 100.f;  // log2 of a block's factor, at most
+
+template <int D>
+struct Geom {
+  static constexpr int kStages = D == 256 ? 2 : 4;
+  static constexpr int kQ = kRows * D * 2;
+  static constexpr int kKV = kKeys * D * 2;  // bytes of K, or of V, of a stage
+  static constexpr size_t kSmem = (size_t)kQ + 2 * kStages * kKV + 1024;
+};
+
+struct Barriers {
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2];   // scores are in tensor memory
+  uint64_t p_full[2];   // weights are
+  uint64_t pv_done[2];  // P V of a tile is added
+  uint64_t scales_full[kScaleTiles];
+};
+
+// kind::f16 on FP16, FP32 accumulator, M = 128, A K-major; `mn`: B's columns are its N index.
+__host__ __device__ constexpr uint32_t idesc(int N, bool mn) {
+  return (1u << 4) | ((uint32_t)mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
+      "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
+      "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(s_addr(b)) : "memory");
+}
+__device__ __forceinline__ void store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// The CTA's rows and key tiles.
+struct Item {
+  int head, row0, rows;     // K/V head; rows of the batch's batch * group
+  int split, first, tiles;  // share of the prefix; its key tiles
+};
+__device__ __forceinline__ Item item_of(const DecodeAttnArgs& a) {
+  const int x = blockIdx.x, y = x / a.heads_kv;
+  Item it;
+  it.head = x - y * a.heads_kv;
+  it.split = y / a.mt;
+  it.row0 = (y - it.split * a.mt) * kRows;
+  it.rows = min(kRows, a.batch * a.group - it.row0);
+  // the tiles evenly: the first all % splits shares have one more
+  const int all = (a.shared + kKeys - 1) / kKeys, each = all / a.pre_splits, more = all - each * a.pre_splits;
+  it.first = each * it.split + min(more, it.split);
+  it.tiles = each + (it.split < more);
+  return it;
+}
+
+// What a converting warp has under way: the codes of two tiles, and the pages ahead.
+template <int D>
+struct Codes {
+  static constexpr int kLanes = D / 16;            // of a key
+  static constexpr int kPer = 32 / kLanes;         // keys of a load
+  static constexpr int kLoads = kKeys / (kConvert * kPer);
+  uint4 k[kLoads], v[kLoads];
+  float scale;  // lanes 0-3 of the first warp: K's blocks; 4-7: V's
+};
+struct Pages {
+  const int* table;
+  int page, next;  // of the block of 16 keys that a lane stands for: eight tiles at a time
+};
+__device__ __forceinline__ int page_of(const DecodeAttnArgs& a, const Pages& pg, int tile, int lane) {
+  const int p = (tile * kKeys + lane * 16) >> a.page_shift;
+  return p < a.width ? __ldg(pg.table + p) : -1;
+}
+
+template <int D>
+__device__ __forceinline__ void ask(const DecodeAttnArgs& a, const Item& it, Pages& pg, int j, Codes<D>& c, int warp, int lane) {
+  using G = Codes<D>;
+  if (j >= it.tiles) return;
+  if ((j & 7) == 0) {
+    pg.page = j ? pg.next : page_of(a, pg, it.first, lane);
+    pg.next = page_of(a, pg, it.first + j + 8, lane);
+  }
+  const int key0 = (it.first + j) * kKeys;
+  auto place = [&](int key, int page) {  // a key's number in the layer's pool, -1 where there is none
+    return key0 + key < a.shared && (unsigned)page < (unsigned)a.pages
+               ? ((long long)page << a.page_shift) + ((key0 + key) & (a.page_size - 1))
+               : -1ll;
+  };
+#pragma unroll
+  for (int i = 0; i < G::kLoads; i++) {
+    const int key = (i * kConvert + warp) * G::kPer + lane / G::kLanes;
+    const long long to = place(key, __shfl_sync(~0u, pg.page, (j & 7) * kBlocks + (key >> 4)));
+    const long long at = (to * a.heads_kv + it.head) * D + lane % G::kLanes * 16;
+    c.k[i] = to < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(a.codes_k + at));
+    c.v[i] = to < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(a.codes_v + at));
+  }
+  const int b = lane & (kBlocks - 1);
+  const long long to = place(16 * b, __shfl_sync(~0u, pg.page, (j & 7) * kBlocks + b));
+  if (warp == 0 && lane < 2 * kBlocks)
+    c.scale = to < 0 ? 1.f : __ldg((lane < kBlocks ? a.k_scale : a.v_scale) + to / 16 * a.heads_kv + it.head);
+}
+
+// A tile's codes as FP16 rows of keys, in column blocks of 64 values. A lane's two pieces go to
+// one column block; every other four lanes begin with the second, so that eight lanes meet
+// all banks.
+template <int Store, int D>
+__device__ __forceinline__ void convert(const uint4 (&x)[Codes<D>::kLoads], uint32_t dst, int warp, int lane) {
+  using G = Codes<D>;
+  const int l = lane % G::kLanes, swap = (l >> 2) & 1;
+#pragma unroll
+  for (int i = 0; i < G::kLoads; i++) {
+    const int key = (i * kConvert + warp) * G::kPer + lane / G::kLanes;
+    uint32_t h[8];
+    halves<Store, false>(x[i].x, h[0], h[1]);
+    halves<Store, false>(x[i].y, h[2], h[3]);
+    halves<Store, false>(x[i].z, h[4], h[5]);
+    halves<Store, false>(x[i].w, h[6], h[7]);
+    const uint32_t at = dst + (l >> 2) * (kKeys * 128) + key * 128;
+    const int p = (l & 3) * 2;
+    const uint32_t at0 = at + (((p + swap) ^ (key & 7)) << 4), at1 = at + (((p + 1 - swap) ^ (key & 7)) << 4);
+    store16(at0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+    store16(at1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+  }
+}
+
+template <typename T, int Store, int D>
+__global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_constant__ DecodeAttnArgs a) {
+  using G = Geom<D>;
+  constexpr int ST = G::kStages;
+  extern __shared__ uint8_t dyn[];
+  __shared__ Barriers bars;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float scales[kScaleTiles][2 * kBlocks];
+  __shared__ float row_by[kRows];  // factor of a row's scores
+  __shared__ uint4 stage[kSoft][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t base = s_addr(dyn) + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
+  const uint32_t sq = base, sk = base + G::kQ, sv = sk + ST * G::kKV;
+  const Ctx c = {&abort_flag, a.err, a.spin};
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < ST; i++) {
+      mbar_init(&bars.k_full[i], kConvert);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], kConvert);
+      mbar_init(&bars.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], kSoft);
+      mbar_init(&bars.pv_done[i], 1);
+    }
+    for (int i = 0; i < kScaleTiles; i++) mbar_init(&bars.scales_full[i], 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s_addr(&tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const Item it = item_of(a);
+  const int conv = warp - kSoft;
+  griddep_wait();
+  griddep_launch();  // what follows waits for this grid before it reads what it wrote
+  Codes<D> ahead[2];
+  Pages pg = {};
+  if (warp >= kSoft && warp < kMmaWarp) {
+    pg.table = prefix_table(a);
+    ask<D>(a, it, pg, 0, ahead[0], conv, lane);
+    ask<D>(a, it, pg, 1, ahead[1], conv, lane);
+  }
+  // Q: a row by D/8 lanes of a warp, two rows at a time where that is half of them
+  if (warp < kMmaWarp) {
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kSteps = (kRows / kPer + kMmaWarp - 1) / kMmaWarp;
+    const int l = lane % kLanes;
+    constexpr int kBatch = 4;
+    for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) {
+        const int r = ((i0 + k) * kMmaWarp + warp) * kPer + lane / kLanes, row = it.row0 + r;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (r < it.rows)
+          x[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + (long long)(row / a.group) * a.ldq +
+                                                 (long long)(it.head * a.group + row % a.group) * D + l * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) {
+        const int r = ((i0 + k) * kMmaWarp + warp) * kPer + lane / kLanes;
+        uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        float by = a.scale_log2;
+        if constexpr (!__is_same(T, __half)) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int n = 0; n < 4; n++) top = max(top, max(w[n] & 0x7fffu, w[n] >> 16 & 0x7fffu));
+#pragma unroll
+          for (int d = kLanes / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+          const float up = brings_up(top);
+#pragma unroll
+          for (int n = 0; n < 4; n++) {
+            const float2 f = pair_to_float(w[n], T());
+            w[n] = pack2<__half>(f.x * up, f.y * up);
+          }
+          by *= inverse_of(up);
+        }
+        if (r < kRows) {
+          store16(sq + (l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+          if (l == 0) row_by[r] = by;
+        }
+      }
+    }
+  }
+  fence_async_smem();
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tm = *(volatile uint32_t*)&tmem_slot;
+
+  if (warp == kMmaWarp) {
+    // ---- MMAs
+    constexpr uint32_t is = idesc(kKeys, false), ip = idesc(D, true);
+    constexpr uint64_t kmaj = operand_bits(16), vmaj = operand_bits(kKeys * 128);
+    const uint64_t qd = operand(sq, kmaj), kd0 = operand(sk, kmaj), vd0 = operand(sv, vmaj);
+    Turn<ST> kt, vt;
+    Turn<2> st, pt;
+    auto scores = [&]() -> bool {
+      if (!wait_warp<10>(c, &bars.k_full[kt.i], kt.parity)) return false;
+      fence_after_sync();
+      const uint64_t kd = kd0 + kt.i * (G::kKV >> 4);
+      const uint32_t d = tm + D + st.i * kKeys;
+      if (elected()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; k++)
+          mma_ss(d, qd + (((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4), kd + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4),
+                 is, k > 0);
+        commit(&bars.s_full[st.i]);
+        commit(&bars.k_empty[kt.i]);
+      }
+      __syncwarp();
+      kt.next();
+      st.next();
+      return true;
+    };
+    bool ok = true;
+    int issued = 0;
+    for (int j = 0; ok && j < it.tiles; j++) {
+      for (; ok && issued < it.tiles && issued < j + 2; issued++) ok = scores();
+      if (!ok || !(ok = wait_warp<10>(c, &bars.p_full[pt.i], pt.parity) && wait_warp<10>(c, &bars.v_full[vt.i], vt.parity))) break;
+      fence_after_sync();
+      const uint64_t vd = vd0 + vt.i * (G::kKV >> 4);
+      const uint32_t p = tm + D + pt.i * kKeys;
+      if (elected()) {
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; k++) mma_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
+        commit(&bars.v_empty[vt.i]);
+        commit(&bars.pv_done[pt.i]);
+      }
+      __syncwarp();
+      vt.next();
+      pt.next();
+    }
+    // the last commits that nothing else waits for: none may be on its way when the CTA leaves
+    for (int i = 0; i < ST && ok; i++) {
+      const int use = it.tiles > i ? (it.tiles - 1 - i) / ST : -1;
+      ok = wait_warp<0>(c, &bars.k_empty[i], (uint32_t)use & 1) && wait_warp<0>(c, &bars.v_empty[i], (uint32_t)use & 1);
+    }
+  } else if (warp >= kSoft) {
+    // ---- codes to operands
+    Turn<ST> t;
+    bool ok = true;
+    auto step = [&](int j, const Codes<D>& x) {
+      if (!(ok = wait_warp<30>(c, &bars.k_empty[t.i], t.parity ^ 1))) return;
+      convert<Store, D>(x.k, sk + t.i * G::kKV, conv, lane);
+      if (conv == 0 && lane < 2 * kBlocks) scales[j % kScaleTiles][lane] = x.scale;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars.k_full[t.i]);
+        if (conv == 0) mbar_arrive(&bars.scales_full[j % kScaleTiles]);
+      }
+      if (!(ok = wait_warp<30>(c, &bars.v_empty[t.i], t.parity ^ 1))) return;
+      convert<Store, D>(x.v, sv + t.i * G::kKV, conv, lane);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.v_full[t.i]);
+      t.next();
+    };
+    for (int j = 0; ok && j < it.tiles; j += 2) {
+      step(j, ahead[0]);
+      ask<D>(a, it, pg, j + 2, ahead[0], conv, lane);
+      if (!ok || j + 1 >= it.tiles) break;
+      step(j + 1, ahead[1]);
+      ask<D>(a, it, pg, j + 3, ahead[1], conv, lane);
+    }
+  } else {
+    // ---- softmax: a thread a row. A wait that gave up changes only what is handed on.
+    const int r = warp * 32 + lane, row = it.row0 + r;
+    const uint32_t tw = tm + ((uint32_t)warp << 21);
+    const bool live = r < it.rows;
+    const int seq = live ? row / a.group : 0, head = it.head * a.group + (live ? row % a.group : 0);
+    const int hi = live ? min(a.shared, seq_len(a, seq)) : INT_MAX;  // keys the row sees
+    const float by = row_by[r];
+    Turn<2> t, before;
+    bool ok = true;
+    float m = -INFINITY, ref = -INFINITY, l = 0.f;
+    for (int j = 0; j < it.tiles; j++, before = t, t.next()) {
+      ok = wait_warp<0>(c, &bars.scales_full[j % kScaleTiles], (j / kScaleTiles) & 1) && ok;
+      ok = wait_warp<0>(c, &bars.s_full[t.i], t.parity) && ok;
+      fence_after_sync();
+      const uint32_t buf = tw + D + t.i * kKeys;
+      float s[kKeys];
+      tmem_ld32(buf, s);
+      tmem_ld32(buf + 32, s + 32);
+      tmem_loaded();
+#pragma unroll
+      for (int b = 0; b < kBlocks; b++) {
+        const float f = by * scales[j % kScaleTiles][b];
+        const uint64_t f2 = pair_of(f, f);
+#pragma unroll
+        for (int i = 16 * b; i < 16 * b + 16; i += 2) parts_of(mul2(pair_of(s[i], s[i + 1]), f2), s[i], s[i + 1]);
+      }
+      const int left = hi - (it.first + j) * kKeys;
+      if (__any_sync(~0u, left < kKeys)) {
+        asm volatile("");  // a branch, not selects in every tile
+#pragma unroll
+        for (int i = 0; i < kKeys; i++)
+          if (i >= left) s[i] = -INFINITY;
+      }
+      float off[kBlocks], want = -INFINITY, top = m;
+#pragma unroll
+      for (int b = 0; b < kBlocks; b++) {
+        const float* x = s + 16 * b;
+        float mx = max3(max3(x[0], x[1], x[2]), x[3], x[4]), my = max3(max3(x[5], x[6], x[7]), x[8], x[9]);
+        mx = max3(max3(mx, my, x[10]), max3(x[11], x[12], x[13]), max3(x[14], x[15], x[15]));
+        // a block of which the row sees nothing may have any scale
+        off[b] = mx == -INFINITY ? 0.f : log2_scale(scales[j % kScaleTiles][kBlocks + b]);
+        want = fmaxf(want, mx + off[b]);
+        top = fmaxf(top, mx);
+      }
+      const float m0 = top == -INFINITY ? 0.f : top;
+      l *= exp2_fast(m - m0);
+      m = top;
+      want -= kShift;
+      const bool move = want > ref + kSlack;  // never for a row that sees nothing; always for its first keys
+      if (__any_sync(~0u, move)) {
+        const float f = move ? exp2_fast(ref - want) : 1.f;
+        if (move) ref = want;
+        if (j > 0) {
+          ok = wait_warp<0>(c, &bars.pv_done[before.i], before.parity) && ok;
+          fence_after_sync();
+          const uint64_t ff = pair_of(f, f);
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            tmem_ld32(tw + i, o);
+            tmem_loaded();
+            uint32_t u[32];
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float y0, y1;
+              parts_of(mul2(pair_of(o[k], o[k + 1]), ff), y0, y1);
+              u[k] = __float_as_uint(y0);
+              u[k + 1] = __float_as_uint(y1);
+            }
+            tmem_st32(tw + i, u);
+          }
+        }
+      }
+      const float ref0 = ref == -INFINITY ? 0.f : ref;
+      bool wide = false;
+#pragma unroll
+      for (int b = 0; b < kBlocks; b++) {
+        off[b] -= ref0;
+        wide = wide || off[b] + m0 > kMostFactor;
+      }
+      uint64_t sum2[2] = {0, 0};
+      uint32_t p[kKeys / 2];
+      if (__any_sync(~0u, wide)) {
+#pragma unroll
+        for (int i = 0; i < kKeys / 2; i++) {
+          const float x = s[2 * i], y = s[2 * i + 1], o = off[i / 8];
+          sum2[0] = add2(sum2[0], pair_of(exp2_fast(x - m0), exp2_fast(y - m0)));
+          p[i] = pack2<__half>(exp2_fast(x + o), exp2_fast(y + o));
+        }
+      } else {
+        const uint64_t m2 = pair_of(-m0, -m0);
+#pragma unroll
+        for (int b = 0; b < kBlocks; b++) {
+          const float f = exp2_fast(off[b] + m0);
+          const uint64_t f2 = pair_of(f, f);
+#pragma unroll
+          for (int i = 8 * b; i < 8 * b + 8; i++) {
+            float x, y;
+            parts_of(add2(pair_of(s[2 * i], s[2 * i + 1]), m2), x, y);
+            const uint64_t e = pair_of(exp2_fast(x), exp2_fast(y));
+            sum2[i & 1] = add2(sum2[i & 1], e);
+            parts_of(mul2(e, f2), x, y);
+            p[i] = pack2<__half>(x, y);  // FP16 matrix operands; the sum stays FP32
+          }
+        }
+      }
+      tmem_st32(buf, p);
+      tmem_stored();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(&bars.p_full[t.i]);
+      float y0, y1;
+      parts_of(add2(sum2[0], sum2[1]), y0, y1);
+      l += y0 + y1;
+    }
+    ok = wait_warp<0>(c, &bars.pv_done[before.i], before.parity) && ok;
+    fence_after_sync();
+    // o relative to m, in two steps that stay in FP32's range
+    const float scale = m == -INFINITY ? 0.f : exp2_fast(ref + kShift - m);
+    const long long slot = ((long long)it.split * a.batch + seq) * a.heads_q + head;
+    const bool stored = live && ok;
+    if (stored) a.pre_ml[slot] = make_float2(m, l);
+    float* po = stored ? a.pre_o + slot * D : nullptr;
+    // 16 rows at a time through shared memory, eight lanes a row's 128 bytes
+    float* to[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      to[k] = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(po), k * 4 + (lane >> 3)));
+    uint4* mine = stage[warp];
+    const int q = lane & 7;
+#pragma unroll 1
+    for (int i = 0; i < D; i += 32) {
+      float o[32];
+      tmem_ld32(tw + i, o);
+      tmem_loaded();
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        if ((lane >> 4) == h)
+#pragma unroll
+          for (int k = 0; k < 8; k++) {
+            uint32_t u[4];
+#pragma unroll
+            for (int n = 0; n < 4; n++) u[n] = __float_as_uint(o[4 * k + n] * 0.0078125f * scale);  // 2^-kShift
+            mine[(lane & 15) * 8 + (k ^ q)] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        __syncwarp();
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const int x = k * 4 + (lane >> 3);
+          w[k] = mine[x * 8 + (q ^ (x & 7))];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (to[h * 4 + k]) *reinterpret_cast<uint4*>(to[h * 4 + k] + i + q * 4) = w[k];
+      }
+    }
+  }
+  __syncwarp();
+  if (*c.abort_flag) {  // MMAs in flight land
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) {
+    }
+    __syncwarp();
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+  }
+}
+
+template <typename T, int Store, int D>
+int prefix_of(const DecodeAttnArgs& a, cudaStream_t s) {
+  const void* fn = (const void*)prefix_q8_kernel<T, Store, D>;
+  const int rc = opt_in_smem(fn, Geom<D>::kSmem);
+  if (rc) return rc;
+  return launch_kernel(fn, dim3((unsigned)a.items), dim3(kThreads), Geom<D>::kSmem, s, const_cast<DecodeAttnArgs*>(&a),
+                       dependent_launches(), 1);
+}
+template <typename T>
+int prefix_of(const DecodeAttnArgs& a, int store, int dim, cudaStream_t s) {
+  if (store == TFX_STORE_I8) return dim == 128 ? prefix_of<T, TFX_STORE_I8, 128>(a, s) : prefix_of<T, TFX_STORE_I8, 256>(a, s);
+  return dim == 128 ? prefix_of<T, TFX_STORE_E4M3, 128>(a, s) : prefix_of<T, TFX_STORE_E4M3, 256>(a, s);
+}
+
+}  // namespace
+
+int prefix_q8_rows() { return kRows; }
+int prefix_q8_tiles(int shared) { return (shared + kKeys - 1) / kKeys; }
+
+int launch_prefix_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s) {
+  return act == TFX_F16 ? prefix_of<__half>(a, store, dim, s) : prefix_of<__nv_bfloat16>(a, store, dim, s);
+}
+
+}  // namespace tfx

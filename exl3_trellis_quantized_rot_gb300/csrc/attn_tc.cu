@@ -83,55 +83,8 @@ struct Barriers {
   uint64_t o_empty;            // both CTAs have read an item's result
 };
 
-// Where a warp is in a ring of N barriers, and the parity it waits for there.
-template <int N>
-struct Turn {
-  int i = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void next() {
-    if (++i == N) {
-      i = 0;
-      parity ^= 1;
-    }
-  }
-};
-
-struct Ctx {
-  Barriers* b;
-  volatile int* abort_flag;
-  int* err;
-  long long spin;
-};
-
-// The whole warp waits, its lanes together, as the warp-wide instructions that
-// follow want them: after a timeout too. Warps that have time to spare sleep NAP
-// ns between polls and leave issue slots and the shared-memory pipe to the softmax
-// warps beside them (48/8 heads of 128: 299 -> 288 us).
-template <int NAP>
-__device__ __forceinline__ bool wait_warp(const Ctx& c, uint64_t* bar, uint32_t parity) {
-  if (__all_sync(~0u, mbar_poll(bar, parity))) return true;
-  const long long t0 = clock64();
-  while (true) {
-    for (int i = 0; i < 8; i++) {
-      if (NAP) __nanosleep(NAP);
-      if (__all_sync(~0u, mbar_poll(bar, parity))) return true;
-    }
-    const bool late = clock64() - t0 > c.spin;
-    if (late && (threadIdx.x & 31) == 0) {
-      *c.abort_flag = 1;
-      atomicExch(c.err, 1);
-    }
-    if (__any_sync(~0u, late || *c.abort_flag)) return false;
-  }
-}
-
 // The two warps that share rows meet at their named barrier.
 __device__ __forceinline__ void bar_meet(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
 
 template <typename T>
 struct Bits;
@@ -426,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attn_tc
   const uint32_t rank = cluster_rank();
   const uint32_t base = s_addr(dyn) + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
   const uint32_t sq = base, sk = base + G::kQ, sv = sk + ST * G::kKV;
-  Ctx c = {&bars, &abort_flag, a.err, a.spin};
+  Ctx c = {&abort_flag, a.err, a.spin};
 
   if (threadIdx.x == 0) {
     abort_flag = 0;

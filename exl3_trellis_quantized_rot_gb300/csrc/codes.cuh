@@ -82,6 +82,36 @@ __device__ __forceinline__ void values4<TFX_STORE_E4M3>(uint32_t w, float (&x)[4
   }
 }
 
+// The four codes of a word as FP16: bytes (0, 1) and (2, 3), or (0, 2) and (1, 3).
+template <int Store, bool Split>
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& a, uint32_t& b) {
+  if constexpr (Store == TFX_STORE_I8) {
+    // 0x64xx is 1024 + xx
+    w ^= 0x80808080u;
+    const uint32_t x = __byte_perm(w, 0x64646464u, Split ? 0x4240 : 0x4140);
+    const uint32_t y = __byte_perm(w, 0x64646464u, Split ? 0x4341 : 0x4342);
+    const __half2 by = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), by);
+    const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&y), by);
+    a = *reinterpret_cast<const uint32_t*>(&p);
+    b = *reinterpret_cast<const uint32_t*>(&q);
+  } else {
+    if (Split) w = __byte_perm(w, 0, 0x3120);
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi; }"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+  }
+}
+
+// log2 of a scale, NaN of a NaN.
+__device__ __forceinline__ float log2_scale(float s) {
+  return s == s ? (float)((int)(__float_as_uint(s) >> 23) - 127) : s;
+}
+
+// BF16 values whose largest magnitude has the bits `top`: the power of two that brings it to
+// [2^14, 2^15), where FP16 holds them exactly but for those 2^28 times smaller; at most 2^126.
+__device__ __forceinline__ float brings_up(uint32_t top) { return __uint_as_float((268u - max(top >> 7, 15u)) << 23); }
+
 __device__ __forceinline__ float2 pair_to_float(uint32_t w, __half) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }

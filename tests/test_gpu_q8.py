@@ -334,3 +334,63 @@ def test_decode_of_values_with_very_different_scales(store):
         p = torch.softmax(q[0, h:h + 1].double() @ kk.T, 1)[0]
         most = TOP[store] * float((p.view(-1, 16).amax(1).cpu() * torch.tensor(m.seqs[0][1].scales[:, 0])).max())
         assert_near(got[:, h], o, A, qk, n, 128, most)
+
+
+@pytest.mark.parametrize("store", STORES)
+@pytest.mark.parametrize("act,hq,hkv,dim,page,shared,n", [
+    (BF16, 24, 4, 256, 64, 1000, 30), (F16, 8, 1, 128, 16, 703, 17), (F16, 128, 1, 256, 32, 320, 2), (BF16, 6, 2, 128, 128, 5000, 64),
+    (F16, 16, 16, 128, 16, 300, 40), (BF16, 20, 1, 256, 16, 256, 7), (F16, 12, 2, 256, 64, 575, 70)])
+def test_decode_of_many_rows_behind_a_prefix(store, act, hq, hkv, dim, page, shared, n):
+    """Rows that fill several tiles and part of one, shares of the prefix, sequences that end inside it and one that is empty."""
+    width = shared // page + 2
+    c = make(store, act, layers=1, pages=width * 2 + n * 2 + 4, page=page, heads=hkv, dim=dim, slots=n + 4, width=width, batch=n + 3, hq=hq)
+    m = Model(c, store)
+    m.put(0, {n: shared}, 2)
+    tfx.cache_fork(c, dev(*[n] * n), dev(*range(n)))
+    for i in range(n):
+        m.seqs[i] = [Coded(store, hkv, dim) for _ in range(2)]
+        for a, b in zip(m.seqs[n], m.seqs[i]):
+            b.codes, b.scales = a.codes.copy(), a.scales.copy()
+    m.put(0, {i: 1 + i % 3 for i in range(n)}, 4, 3.0)
+    # shorter ones: the prefix's first tokens
+    for slot, held in ((n + 1, 100), (n + 2, 17)):
+        m.seqs[slot] = [Coded(store, hkv, dim) for _ in range(2)]
+        for a, b in zip(m.seqs[n], m.seqs[slot]):
+            b.codes, b.scales = a.codes[:held].copy(), a.scales[:-(-held // BLOCK)].copy()
+        c.lens[slot] = held
+        c.tables[slot] = c.tables[n]
+    order = list(range(n)) + [n + 1, n + 2, n + 3]
+    q = normal((n + 3, hq, dim), act, 7, 0.3)
+    got = tfx.attn_decode(c, 0, q, dev(*order), shared=shared)
+    assert tfx.attn_error() == 0
+    check_decode(c, m, 0, q, order, shared, got, dim ** -0.5)
+
+
+@pytest.mark.parametrize("store", STORES)
+def test_prefix_of_values_with_very_different_scales(store):
+    """As test_decode_of_values_with_very_different_scales, in the prefix of a batch; scales of 2^100 that have next to no weight."""
+    n, batch = 512, 16
+    c = make(store, BF16, layers=1, page=64, heads=1, dim=128, pages=30, width=12, slots=batch + 1, batch=batch, hq=4)
+    k, v = normal((n, 1, 128), BF16, 1), normal((n, 1, 128), BF16, 2)
+    q = normal((batch, 4, 128), BF16, 3)
+    v[:16] = 0
+    for b in range(1, n // 16):
+        v[16 * b:16 * b + 16] *= 2.0 ** ((b * 37) % 61 - 30)
+    v[160:176] *= 2.0 ** 100
+    k[160:176] = q[:, 0].float().mean(0).to(BF16) * -40
+    k[3] = 2 * q[0, 1]
+    tfx.cache_extend(c, dev(batch), dev(0, n))
+    tfx.cache_append(c, 0, k, v)
+    tfx.cache_fork(c, dev(*[batch] * batch), dev(*range(batch)))
+    pair = [Coded(store, 1, 128) for _ in range(2)]
+    for x, y in zip(pair, (k, v)):
+        x.append(y.double().cpu().numpy())
+    got = tfx.attn_decode(c, 0, q, dev(*range(batch)), shared=n, scale=1.0)
+    kk, vv = (torch.tensor(x.values()).cuda()[:, 0] for x in pair)
+    scales = torch.tensor(pair[1].scales[:, 0])
+    for i in range(batch):
+        for h in range(4):
+            o, A, qk = attend(q[i, h:h + 1], kk, vv, 1.0)
+            p = torch.softmax(q[i, h:h + 1].double() @ kk.T, 1)[0]
+            most = TOP[store] * float((p.view(-1, 16).amax(1).cpu() * scales).max())
+            assert_near(got[i:i + 1, h], o, A, qk, n, 128, most)
