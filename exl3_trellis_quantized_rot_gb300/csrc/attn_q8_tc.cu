@@ -10,7 +10,7 @@
 // A row is a (sequence, query head) pair of one K/V head; 128 of them fill a tile however the
 // heads are grouped. Warps of a CTA: 0-3 softmax and results (a thread a row); 4-11 turn codes
 // into operands: 16 codes a lane and load, two tiles ahead in registers, as two 16-byte pieces
-// into the 128-byte swizzle; 12 issues the MMAs. Order of the MMAs: S0, S1, P0 V0, S2, P1 V1, ...
+// into the 128-byte swizzle; 12 issues the MMAs; 0-11 store the result. Order of the MMAs: S0, S1, P0 V0, S2, P1 V1, ...
 // Tensor memory: O in columns 0..dim-1, two buffers of 64 columns for scores, whose first 32
 // take the weights.
 #include <cuda_bf16.h>
@@ -24,7 +24,8 @@ namespace {
 
 constexpr int kSoft = 4, kConvert = 8;  // warps
 constexpr int kMmaWarp = kSoft + kConvert;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kWarps = kMmaWarp + 4;  // whole groups of four, for the register split; the last three only load Q
+constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 64, kRows = 128;
 constexpr int kBlocks = kKeys / 16;
 constexpr int kScaleTiles = 8;  // tiles whose scales are kept: stages and score buffers, and more
@@ -45,6 +46,8 @@ struct Barriers {
   uint64_t p_full[2];   // weights are
   uint64_t pv_done[2];  // P V of a tile is added
   uint64_t scales_full[kScaleTiles];
+  uint64_t q_full;      // Q is in shared memory
+  uint64_t ends_full;   // factors of the rows' results are
 };
 
 // kind::f16 on FP16, FP32 accumulator, M = 128, A K-major; `mn`: B's columns are its N index.
@@ -167,8 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float scales[kScaleTiles][2 * kBlocks];
-  __shared__ float row_by[kRows];  // factor of a row's scores
-  __shared__ uint4 stage[kSoft][128];
+  __shared__ float row_by[kRows];   // factor of a row's scores
+  __shared__ float row_end[kRows];  // of its result
+  __shared__ uint4 stage[kMmaWarp][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t base = s_addr(dyn) + ((1024u - (s_addr(dyn) & 1023u)) & 1023u);
   const uint32_t sq = base, sk = base + G::kQ, sv = sk + ST * G::kKV;
@@ -187,6 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
       mbar_init(&bars.pv_done[i], 1);
     }
     for (int i = 0; i < kScaleTiles; i++) mbar_init(&bars.scales_full[i], 1);
+    mbar_init(&bars.q_full, kWarps - 1);
+    mbar_init(&bars.ends_full, kSoft);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -194,26 +200,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   const Item it = item_of(a);
-  const int conv = warp - kSoft;
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tm = *(volatile uint32_t*)&tmem_slot;
   griddep_wait();
   griddep_launch();  // what follows waits for this grid before it reads what it wrote
-  Codes<D> ahead[2];
-  Pages pg = {};
-  if (warp >= kSoft && warp < kMmaWarp) {
-    pg.table = prefix_table(a);
-    ask<D>(a, it, pg, 0, ahead[0], conv, lane);
-    ask<D>(a, it, pg, 1, ahead[1], conv, lane);
-  }
-  // Q: a row by D/8 lanes of a warp, two rows at a time where that is half of them
-  if (warp < kMmaWarp) {
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kSteps = (kRows / kPer + kMmaWarp - 1) / kMmaWarp;
+
+  // Q, by all warps but the MMAs': a row by D/8 lanes, two rows at a time where that is half of them
+  auto load_q = [&](int helper) {
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kHelpers = kWarps - 1, kSteps = (kRows / kPer + kHelpers - 1) / kHelpers;
     const int l = lane % kLanes;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 3;
+#pragma unroll 1
     for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
       uint4 x[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; k++) {
-        const int r = ((i0 + k) * kMmaWarp + warp) * kPer + lane / kLanes, row = it.row0 + r;
+        const int r = ((i0 + k) * kHelpers + helper) * kPer + lane / kLanes, row = it.row0 + r;
         x[k] = make_uint4(0, 0, 0, 0);
         if (r < it.rows)
           x[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + (long long)(row / a.group) * a.ldq +
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
       }
 #pragma unroll
       for (int k = 0; k < kBatch; k++) {
-        const int r = ((i0 + k) * kMmaWarp + warp) * kPer + lane / kLanes;
+        const int r = ((i0 + k) * kHelpers + helper) * kPer + lane / kLanes;
         uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
         float by = a.scale_log2;
         if constexpr (!__is_same(T, __half)) {
@@ -244,63 +248,118 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
         }
       }
     }
-  }
-  fence_async_smem();
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  const uint32_t tm = *(volatile uint32_t*)&tmem_slot;
-
-  if (warp == kMmaWarp) {
-    // ---- MMAs
-    constexpr uint32_t is = idesc(kKeys, false), ip = idesc(D, true);
-    constexpr uint64_t kmaj = operand_bits(16), vmaj = operand_bits(kKeys * 128);
-    const uint64_t qd = operand(sq, kmaj), kd0 = operand(sk, kmaj), vd0 = operand(sv, vmaj);
-    Turn<ST> kt, vt;
-    Turn<2> st, pt;
-    auto scores = [&]() -> bool {
-      if (!wait_warp<10>(c, &bars.k_full[kt.i], kt.parity)) return false;
-      fence_after_sync();
-      const uint64_t kd = kd0 + kt.i * (G::kKV >> 4);
-      const uint32_t d = tm + D + st.i * kKeys;
-      if (elected()) {
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.q_full);
+  };
+  // The result's columns, 32 at a time: every third run of them by a warp, of the 32 rows whose
+  // tensor memory it reaches. 16 rows at a time go through shared memory, eight lanes a row's 128 bytes.
+  auto store_result = [&](bool ok) {
+    const int quarter = warp & 3, r = quarter * 32 + lane, row = it.row0 + r;
+    const bool stored = ok && r < it.rows;
+    const int seq = stored ? row / a.group : 0, head = it.head * a.group + (stored ? row % a.group : 0);
+    float* po = stored ? a.pre_o + (((long long)it.split * a.batch + seq) * a.heads_q + head) * D : nullptr;
+    float* to[8];
 #pragma unroll
-        for (int k = 0; k < D / 16; k++)
-          mma_ss(d, qd + (((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4), kd + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4),
-                 is, k > 0);
-        commit(&bars.s_full[st.i]);
-        commit(&bars.k_empty[kt.i]);
-      }
-      __syncwarp();
-      kt.next();
-      st.next();
-      return true;
-    };
-    bool ok = true;
-    int issued = 0;
-    for (int j = 0; ok && j < it.tiles; j++) {
-      for (; ok && issued < it.tiles && issued < j + 2; issued++) ok = scores();
-      if (!ok || !(ok = wait_warp<10>(c, &bars.p_full[pt.i], pt.parity) && wait_warp<10>(c, &bars.v_full[vt.i], vt.parity))) break;
-      fence_after_sync();
-      const uint64_t vd = vd0 + vt.i * (G::kKV >> 4);
-      const uint32_t p = tm + D + pt.i * kKeys;
-      if (elected()) {
+    for (int k = 0; k < 8; k++)
+      to[k] = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(po), k * 4 + (lane >> 3)));
+    const float scale = row_end[r];
+    uint4* mine = stage[warp];
+    const int q = lane & 7;
+#pragma unroll 1
+    for (int i = (warp >> 2) * 32; i < D; i += 96) {
+      float o[32];
+      tmem_ld32(tm + ((uint32_t)quarter << 21) + i, o);
+      tmem_loaded();
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; k++) mma_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
-        commit(&bars.v_empty[vt.i]);
-        commit(&bars.pv_done[pt.i]);
+      for (int h = 0; h < 2; h++) {
+        if ((lane >> 4) == h)
+#pragma unroll
+          for (int k = 0; k < 8; k++) {
+            uint32_t u[4];
+#pragma unroll
+            for (int n = 0; n < 4; n++) u[n] = __float_as_uint(o[4 * k + n] * 0.0078125f * scale);  // 2^-kShift
+            mine[(lane & 15) * 8 + (k ^ q)] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        __syncwarp();
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const int x = k * 4 + (lane >> 3);
+          w[k] = mine[x * 8 + (q ^ (x & 7))];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (to[h * 4 + k]) *reinterpret_cast<uint4*>(to[h * 4 + k] + i + q * 4) = w[k];
       }
-      __syncwarp();
-      vt.next();
-      pt.next();
     }
-    // the last commits that nothing else waits for: none may be on its way when the CTA leaves
-    for (int i = 0; i < ST && ok; i++) {
-      const int use = it.tiles > i ? (it.tiles - 1 - i) / ST : -1;
-      ok = wait_warp<0>(c, &bars.k_empty[i], (uint32_t)use & 1) && wait_warp<0>(c, &bars.v_empty[i], (uint32_t)use & 1);
+  };
+
+  // registers: 512 x 128 at launch; 128 x 176 + 256 x 136 + 128 x 64 are as many from here on
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp > kMmaWarp) {
+      load_q(warp - 1);
+    } else {
+      // ---- MMAs
+      constexpr uint32_t is = idesc(kKeys, false), ip = idesc(D, true);
+      constexpr uint64_t kmaj = operand_bits(16), vmaj = operand_bits(kKeys * 128);
+      const uint64_t qd = operand(sq, kmaj), kd0 = operand(sk, kmaj), vd0 = operand(sv, vmaj);
+      Turn<ST> kt, vt;
+      Turn<2> st, pt;
+      auto scores = [&]() -> bool {
+        if (!wait_warp<10>(c, &bars.k_full[kt.i], kt.parity)) return false;
+        fence_after_sync();
+        const uint64_t kd = kd0 + kt.i * (G::kKV >> 4);
+        const uint32_t d = tm + D + st.i * kKeys;
+        if (elected()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; k++)
+            mma_ss(d, qd + (((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4), kd + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4),
+                   is, k > 0);
+          commit(&bars.s_full[st.i]);
+          commit(&bars.k_empty[kt.i]);
+        }
+        __syncwarp();
+        kt.next();
+        st.next();
+        return true;
+      };
+      bool ok = wait_warp<10>(c, &bars.q_full, 0);
+      int issued = 0;
+      for (int j = 0; ok && j < it.tiles; j++) {
+        for (; ok && issued < it.tiles && issued < j + 2; issued++) ok = scores();
+        if (!ok || !(ok = wait_warp<10>(c, &bars.p_full[pt.i], pt.parity) && wait_warp<10>(c, &bars.v_full[vt.i], vt.parity))) break;
+        fence_after_sync();
+        const uint64_t vd = vd0 + vt.i * (G::kKV >> 4);
+        const uint32_t p = tm + D + pt.i * kKeys;
+        if (elected()) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; k++) mma_ts(tm, p + k * 8, vd + ((k * 2048) >> 4), ip, j > 0 || k > 0);
+          commit(&bars.v_empty[vt.i]);
+          commit(&bars.pv_done[pt.i]);
+        }
+        __syncwarp();
+        vt.next();
+        pt.next();
+      }
+      // the last commits that nothing else waits for: none may be on its way when the CTA leaves
+      for (int i = 0; i < ST && ok; i++) {
+        const int use = it.tiles > i ? (it.tiles - 1 - i) / ST : -1;
+        ok = wait_warp<0>(c, &bars.k_empty[i], (uint32_t)use & 1) && wait_warp<0>(c, &bars.v_empty[i], (uint32_t)use & 1);
+      }
     }
   } else if (warp >= kSoft) {
     // ---- codes to operands
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    const int conv = warp - kSoft;
+    Codes<D> ahead[2];
+    Pages pg = {};
+    pg.table = prefix_table(a);
+    ask<D>(a, it, pg, 0, ahead[0], conv, lane);
+    ask<D>(a, it, pg, 1, ahead[1], conv, lane);
+    load_q(warp);
     Turn<ST> t;
     bool ok = true;
     auto step = [&](int j, const Codes<D>& x) {
@@ -327,16 +386,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
       step(j + 1, ahead[1]);
       ask<D>(a, it, pg, j + 3, ahead[1], conv, lane);
     }
+    // the last product is added, and the rows' factors are there
+    const int last = it.tiles - 1;
+    ok = ok && wait_warp<100>(c, &bars.ends_full, 0) && wait_warp<30>(c, &bars.pv_done[last & 1], (last >> 1) & 1);
+    fence_after_sync();
+    store_result(ok);
   } else {
     // ---- softmax: a thread a row. A wait that gave up changes only what is handed on.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    load_q(warp);
     const int r = warp * 32 + lane, row = it.row0 + r;
     const uint32_t tw = tm + ((uint32_t)warp << 21);
     const bool live = r < it.rows;
     const int seq = live ? row / a.group : 0, head = it.head * a.group + (live ? row % a.group : 0);
     const int hi = live ? min(a.shared, seq_len(a, seq)) : INT_MAX;  // keys the row sees
+    bool ok = wait_warp<0>(c, &bars.q_full, 0);
     const float by = row_by[r];
     Turn<2> t, before;
-    bool ok = true;
     float m = -INFINITY, ref = -INFINITY, l = 0.f;
     for (int j = 0; j < it.tiles; j++, before = t, t.next()) {
       ok = wait_warp<0>(c, &bars.scales_full[j % kScaleTiles], (j / kScaleTiles) & 1) && ok;
@@ -443,49 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
       parts_of(add2(sum2[0], sum2[1]), y0, y1);
       l += y0 + y1;
     }
+    // o relative to m, in two steps that stay in FP32's range: see store_result
+    row_end[r] = m == -INFINITY ? 0.f : exp2_fast(ref + kShift - m);
+    __syncwarp();
+    if (lane == 0 && ok) mbar_arrive(&bars.ends_full);
+    ok = wait_warp<0>(c, &bars.ends_full, 0) && ok;
     ok = wait_warp<0>(c, &bars.pv_done[before.i], before.parity) && ok;
     fence_after_sync();
-    // o relative to m, in two steps that stay in FP32's range
-    const float scale = m == -INFINITY ? 0.f : exp2_fast(ref + kShift - m);
-    const long long slot = ((long long)it.split * a.batch + seq) * a.heads_q + head;
-    const bool stored = live && ok;
-    if (stored) a.pre_ml[slot] = make_float2(m, l);
-    float* po = stored ? a.pre_o + slot * D : nullptr;
-    // 16 rows at a time through shared memory, eight lanes a row's 128 bytes
-    float* to[8];
-#pragma unroll
-    for (int k = 0; k < 8; k++)
-      to[k] = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(po), k * 4 + (lane >> 3)));
-    uint4* mine = stage[warp];
-    const int q = lane & 7;
-#pragma unroll 1
-    for (int i = 0; i < D; i += 32) {
-      float o[32];
-      tmem_ld32(tw + i, o);
-      tmem_loaded();
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        if ((lane >> 4) == h)
-#pragma unroll
-          for (int k = 0; k < 8; k++) {
-            uint32_t u[4];
-#pragma unroll
-            for (int n = 0; n < 4; n++) u[n] = __float_as_uint(o[4 * k + n] * 0.0078125f * scale);  // 2^-kShift
-            mine[(lane & 15) * 8 + (k ^ q)] = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        __syncwarp();
-        uint4 w[4];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const int x = k * 4 + (lane >> 3);
-          w[k] = mine[x * 8 + (q ^ (x & 7))];
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-          if (to[h * 4 + k]) *reinterpret_cast<uint4*>(to[h * 4 + k] + i + q * 4) = w[k];
-      }
-    }
+    if (live && ok) a.pre_ml[((long long)it.split * a.batch + seq) * a.heads_q + head] = make_float2(m, l);
+    store_result(ok);
   }
   __syncwarp();
   if (*c.abort_flag) {  // MMAs in flight land
