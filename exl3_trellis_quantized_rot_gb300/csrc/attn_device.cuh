@@ -11,13 +11,17 @@
 namespace tfx {
 
 // 5-D tensor copy: (value within a 64-value column block, token, column block, head, page).
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* tm, int c0, int c1, int c2, int c3, int c4,
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, int c3, int c4,
                                             uint64_t* b) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-      "[%7];" ::"r"(s_addr(dst)),
+      "[%7];" ::"r"(dst),
       "l"(tm), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(s_addr(b))
       : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* tm, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* b) {
+  tma_load_5d(s_addr(dst), tm, c0, c1, c2, c3, c4, b);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
