@@ -601,7 +601,9 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
     const int64_t rows = (int64_t)batch * a.group, per = tfx::prefix_q8_rows();
     a.mt = (int)((rows + per - 1) / per);
     const int64_t rest = (int64_t)c->heads_kv * a.mt, fill = tfx::multiprocessors() / rest, tiles = tfx::prefix_q8_tiles(a.shared);
-    a.pre_splits = (int)(fill < 1 ? 1 : fill > tiles ? tiles : fill);
+    // of the most tiles that a share must have then, as few shares: each leaves partial results
+    const int64_t most = fill < 1 ? tiles : (tiles + fill - 1) / fill;
+    a.pre_splits = (int)((tiles + most - 1) / most);
     if (rest * a.pre_splits > INT32_MAX) return fail_with(TFX_EUNSUPPORTED, "%lld tiles of rows", (long long)rest);
     a.items = (int)(rest * a.pre_splits);
     a.codes_k = static_cast<const uint8_t*>(kl);

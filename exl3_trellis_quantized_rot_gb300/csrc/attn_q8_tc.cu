@@ -139,16 +139,16 @@ struct Convert {
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
       const int key = key_of(i, warp, lane);
+      // the lane's first piece, and its second
       uint32_t h[8];
-      halves<Store, false>(x[i].x, h[0], h[1]);
-      halves<Store, false>(x[i].y, h[2], h[3]);
-      halves<Store, false>(x[i].z, h[4], h[5]);
-      halves<Store, false>(x[i].w, h[6], h[7]);
+      halves<Store, false>(swap ? x[i].z : x[i].x, h[0], h[1]);
+      halves<Store, false>(swap ? x[i].w : x[i].y, h[2], h[3]);
+      halves<Store, false>(swap ? x[i].x : x[i].z, h[4], h[5]);
+      halves<Store, false>(swap ? x[i].y : x[i].w, h[6], h[7]);
       const uint32_t at = dst + (l >> 2) * (kKeys * 128) + key * 128;
-      const int p = (l & 3) * 2;
-      const uint32_t at0 = at + (((p + swap) ^ (key & 7)) << 4), at1 = at + (((p + 1 - swap) ^ (key & 7)) << 4);
-      store16(at0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-      store16(at1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+      const int p = (l & 3) * 2 + swap;
+      store16(at + ((p ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
+      store16(at + ((p ^ 1 ^ (key & 7)) << 4), h[4], h[5], h[6], h[7]);
     }
   }
 };
@@ -203,44 +203,43 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
   griddep_wait();
   griddep_launch();  // what follows waits for this grid before it reads what it wrote
 
-  // Q: a row by D/8 lanes, two rows at a time where that is half of them
+  // Q: a row by D/8 lanes, two rows at a time where that is half of them. A lane works out where
+  // one of the warp's 16 rows is.
   auto load_q = [&](int helper) {
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kHelpers = kSoft, kSteps = kRows / kPer / kHelpers;
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kSteps = kRows / kPer / kSoft;
     const int l = lane % kLanes;
-    constexpr int kBatch = 8;
-#pragma unroll 1
-    for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
-      uint4 x[kBatch];
+    const int my_r = (lane & 15) / kPer * (kSoft * kPer) + helper * kPer + (lane & 15) % kPer, my_row = it.row0 + my_r;
+    const int my_seq = my_row / a.group;
+    const long long my_at = my_r < it.rows ? my_seq * a.ldq + (long long)(it.head * a.group + my_row - my_seq * a.group) * D : -1;
+    uint4 x[kSteps];
 #pragma unroll
-      for (int k = 0; k < kBatch; k++) {
-        const int r = ((i0 + k) * kHelpers + helper) * kPer + lane / kLanes, row = it.row0 + r;
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (r < it.rows)
-          x[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + (long long)(row / a.group) * a.ldq +
-                                                 (long long)(it.head * a.group + row % a.group) * D + l * 8);
-      }
+    for (int k = 0; k < kSteps; k++) {
+      const long long at = __shfl_sync(~0u, my_at, k * kPer + lane / kLanes);
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (at >= 0) x[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + at + l * 8);
+    }
 #pragma unroll
-      for (int k = 0; k < kBatch; k++) {
-        const int r = ((i0 + k) * kHelpers + helper) * kPer + lane / kLanes;
-        uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-        float by = a.scale_log2;
-        if constexpr (!__is_same(T, __half)) {
-          uint32_t top = 0;
+    for (int k = 0; k < kSteps; k++) {
+      const int r = (k * kSoft + helper) * kPer + lane / kLanes;
+      uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      float by = a.scale_log2;
+      if constexpr (!__is_same(T, __half)) {
+        uint32_t top = 0;
 #pragma unroll
-          for (int n = 0; n < 4; n++) top = max(top, max(w[n] & 0x7fffu, w[n] >> 16 & 0x7fffu));
+        for (int n = 0; n < 4; n++) top = __vmaxu2(top, w[n] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-          for (int d = kLanes / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-          const float up = brings_up(top);
+        for (int d = kLanes / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+        const float up = brings_up(top);
 #pragma unroll
-          for (int n = 0; n < 4; n++) {
-            const float2 f = pair_to_float(w[n], T());
-            w[n] = pack2<__half>(f.x * up, f.y * up);
-          }
-          by *= inverse_of(up);
+        for (int n = 0; n < 4; n++) {
+          const float2 f = pair_to_float(w[n], T());
+          w[n] = pack2<__half>(f.x * up, f.y * up);
         }
-        store16(sq + (l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-        if (l == 0) row_by[r] = by;
+        by *= inverse_of(up);
       }
+      store16(sq + (l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+      if (l == 0) row_by[r] = by;
     }
     fence_async_smem();
     __syncwarp();
