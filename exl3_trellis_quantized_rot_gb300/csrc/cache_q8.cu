@@ -6,6 +6,8 @@
 // only where the scale grows.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "attn_device.cuh"
 #include "cache_device.cuh"
 #include "codes.cuh"
@@ -15,191 +17,258 @@ namespace tfx {
 namespace {
 
 constexpr int kBlock = TFX_CACHE_BLOCK;
-constexpr int kAppendThreads = 256;
-constexpr int kAppendWarps = kAppendThreads / 32;
-constexpr int kMostRows = 16;  // rows of the list that a CTA looks at
+constexpr int kMostRows = 32;  // rows of the list that are looked at together: a lane each
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
-// A CTA looks at a.per rows of the list. A row that is the first of its block's new tokens
-// stands for the block, also where the block's tokens go on past the CTA's rows. A warp takes
-// 256 values of a block's tokens (a lane 8 of each token): one head of 256 or two of 128.
+// The next of a window's tasks, for a warp.
+__device__ __forceinline__ int take(int* taken) {
+  int it = 0;
+  if ((threadIdx.x & 31) == 0) it = atomicAdd(taken, 1);
+  return __shfl_sync(~0u, it, 0);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b);  // of magnitudes; a NaN stays
+template <>
+__device__ __forceinline__ uint32_t larger2<__half>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{ .reg .b32 x; abs.f16x2 x, %2; max.NaN.f16x2 %0, %1, x; }" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t larger2<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{ .reg .b32 x; abs.bf16x2 x, %2; max.NaN.bf16x2 %0, %1, x; }" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The blocks of a window of rows of a list: first row, first token of the pool (-1: none), and
+// rows, up to 16 of one block.
+struct Blocks {
+  int first[kMostRows], rows[kMostRows];
+  long long to[kMostRows];
+  int n, taken;
+
+  // By a warp, a lane a row: those that stand for a block.
+  __device__ __forceinline__ void list(bool stands, int row, long long token, int count) {
+    const int lane = threadIdx.x & 31;
+    const unsigned all = __ballot_sync(~0u, stands);
+    if (stands) {
+      const int i = __popc(all & ((1u << lane) - 1));
+      first[i] = row;
+      to[i] = token;
+      rows[i] = count;
+    }
+    if (lane == 0) {
+      n = __popc(all);
+      taken = 0;
+    }
+  }
+};
+
+// A task's place: a lane has 8 values of each of up to 16 tokens. D: values of a head.
+struct Task {
+  int t, n, at, in;
+  long long to, block;
+  bool value, mine;
+};
+__device__ __forceinline__ Task task_of(const Blocks& w, int it, int parts, int row) {
+  Task k;
+  const int i = it / (2 * parts), rest = it - i * 2 * parts;
+  k.value = rest >= parts;
+  k.at = (k.value ? rest - parts : rest) * 256 + (threadIdx.x & 31) * 8;
+  k.mine = k.at < row;
+  k.t = w.first[i];
+  k.n = w.rows[i];
+  k.to = w.to[i];
+  k.in = (int)(k.to & (kBlock - 1));
+  k.block = k.to / kBlock;
+  return k;
+}
+
+// Windows of a.per rows of the list. A row that is the first of its block's new tokens stands
+// for the block, also where the block's tokens go on past the window. The first warp of a CTA
+// looks up the next window's blocks while the others do this one's: the way from the lists to a
+// page is five loads that wait for one another. A task is 256 values of a block's tokens: one
+// head of 256 or two of 128.
 template <typename T, int Store, int D>
-__global__ void __launch_bounds__(kAppendThreads, 2) append_q8_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ int first[kMostRows], to[kMostRows], fresh[kMostRows], blocks;
+__global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ Blocks ring[2];
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = blockIdx.x * a.per, rows = min(a.per, a.rows - t0);
-  if (threadIdx.x == 0) blocks = 0;
-  __syncthreads();
-  for (int r = warp; r < rows; r += kAppendWarps) {
-    const Place at = place_of(a, t0 + r);
+  const int row = a.heads * D, parts = (row + 255) / 256, step = row / 8;  // step: words of 8 values
+  const int windows = (int)(((long long)a.rows + a.per - 1) / a.per);
+  auto look_up = [&](int window, Blocks& w) {
+    const int t0 = window * a.per, t = t0 + lane;
+    const Place at = places_of(a, t0, min(a.per, a.rows - t0));
     const int in = at.pos % kBlock;
-    if (lane == 0 && at.to >= 0 && (t0 + r == at.begin || in == 0)) {
-      const int i = atomicAdd(&blocks, 1);  // in any order
-      first[i] = t0 + r;
-      to[i] = at.to;
-      fresh[i] = min(min(kBlock - in, at.end - t0 - r), a.rows - t0 - r);
-    }
-  }
-  __syncthreads();
-  const int row = a.heads * D, parts = (row + 255) / 256;
-  for (int it = warp; it < blocks * 2 * parts; it += kAppendWarps) {
-    const int i = it / (2 * parts), rest = it - i * 2 * parts;
-    const bool value = rest >= parts;
-    const int at = (value ? rest - parts : rest) * 256 + lane * 8;
-    const bool mine = at < row;
-    const int t = first[i], n = fresh[i], in = to[i] % kBlock;
-    const long long block = to[i] / kBlock;
-    const long long ld = value ? a.ldv : a.ldk;  // words of 8 values
-    const uint4* src = reinterpret_cast<const uint4*>(value ? a.v_new : a.k_new) + t * ld + at / 8;
-    uint2* codes = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(value ? a.v : a.k) + block * kBlock * row + at);
-    float* scales = (value ? a.v_scale : a.k_scale) + block * a.heads + at / D;
+    w.list(at.to >= 0 && (t == at.begin || in == 0), t, at.to, min(min(kBlock - in, at.end - t), a.rows - t));
+  };
+  auto run = [&](const Task& k, auto whole) {  // whole: 16 new tokens
+    constexpr bool kWhole = decltype(whole)::value;
+    const long long ld = k.value ? a.ldv : a.ldk;  // words of 8 values
+    const uint4* src = reinterpret_cast<const uint4*>(k.value ? a.v_new : a.k_new) + k.t * ld + k.at / 8;
+    uint2* codes = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(k.value ? a.v : a.k) + k.block * kBlock * row + k.at);
+    float* scales = (k.value ? a.v_scale : a.k_scale) + k.block * a.heads + k.at / D;
     uint4 x[kBlock];
 #pragma unroll
-    for (int j = 0; j < kBlock; j++) x[j] = mine && j < n ? __ldcs(src + j * ld) : make_uint4(0, 0, 0, 0);
-    const float before = mine && in ? *scales : 0.f;
-    // magnitudes as the type's bits: their order is that of the values, and NaN is above all
+    for (int j = 0; j < kBlock; j++) x[j] = k.mine && (kWhole || j < k.n) ? __ldcs(src + j * ld) : make_uint4(0, 0, 0, 0);
+    const float before = !kWhole && k.mine && k.in ? *scales : 0.f;
     uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < kBlock; j++) {
-      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-      for (int k = 0; k < 4; k++) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
-    }
+    for (int j = 0; j < kBlock; j++)
+      top = larger2<T>(larger2<T>(larger2<T>(larger2<T>(top, x[j].x), x[j].y), x[j].z), x[j].w);
+    // magnitudes as the type's bits: their order is that of the values, and NaN is above all
     top = max(top & 0xffffu, top >> 16);
 #pragma unroll
     for (int d = D / 16; d; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
     const float2 most = pair_to_float(top, T());
     const float scale = larger_scale(before, scale_for<Store>(__float_as_uint(most.x)));
     const float inv = inverse_of(scale);
-    if (mine && in && scale != before) {
+    if (!kWhole && k.mine && k.in && scale != before) {
       const float by = before * inv;
-      for (int j = 0; j < in; j++) {
-        uint2 c = codes[(long long)j * row / 8];
+      for (int j = 0; j < k.in; j++) {
+        uint2 c = codes[j * step];
         float f[4], g[4];
         values4<Store>(c.x, f);
         values4<Store>(c.y, g);
-        c.x = code4<Store>(f[0] * by, f[1] * by, f[2] * by, f[3] * by);
-        c.y = code4<Store>(g[0] * by, g[1] * by, g[2] * by, g[3] * by);
-        codes[(long long)j * row / 8] = c;
+        c.x = code4<Store>(f[0], f[1], f[2], f[3], by);
+        c.y = code4<Store>(g[0], g[1], g[2], g[3], by);
+        codes[j * step] = c;
       }
     }
+    uint2* out = codes + (kWhole ? 0 : k.in * step);
 #pragma unroll
     for (int j = 0; j < kBlock; j++)
-      if (mine && j < n) {
+      if (k.mine && (kWhole || j < k.n)) {
         const float2 p = pair_to_float(x[j].x, T()), q = pair_to_float(x[j].y, T());
         const float2 r = pair_to_float(x[j].z, T()), s = pair_to_float(x[j].w, T());
-        codes[(long long)(in + j) * row / 8] = make_uint2(code4<Store>(p.x * inv, p.y * inv, q.x * inv, q.y * inv),
-                                                          code4<Store>(r.x * inv, r.y * inv, s.x * inv, s.y * inv));
+        out[j * step] = make_uint2(code4<Store>(p.x, p.y, q.x, q.y, inv), code4<Store>(r.x, r.y, s.x, s.y, inv));
       }
-    if (mine && at % D == 0) *scales = scale;
+    if (k.mine && k.at % D == 0) *scales = scale;
+  };
+  if (warp == 0) look_up(blockIdx.x, ring[0]);
+  __syncthreads();
+  int b = 0;
+  for (int window = blockIdx.x; window < windows; window += gridDim.x, b ^= 1, __syncthreads()) {
+    if (warp == 0 && window + (int)gridDim.x < windows) look_up(window + gridDim.x, ring[b ^ 1]);
+    const int all = ring[b].n * 2 * parts;
+    for (int it; (it = take(&ring[b].taken)) < all;) {
+      const Task k = task_of(ring[b], it, parts, row);
+      if (k.n == kBlock) run(k, std::true_type());
+      else run(k, std::false_type());
+    }
   }
 }
 
-constexpr int kReadThreads = 256;
-
-// A CTA does a.per rows: a warp finds one row's place, then all threads take 16 bytes of a row
-// of K or V at a time, four of them in flight.
-template <typename T, int Store>
-__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int kValues = Store == TFX_STORE_ACT ? 8 : 16;  // in 16 bytes
-  __shared__ long long to[kMostRows];  // a token of the pool; -1: none, -2: the row is in no list
+// The same for rows that are read: their tokens lie together in a block, and have its scale.
+// A row whose sequence does not hold its token stands for itself.
+template <typename T, int Store, int D>
+__global__ void __launch_bounds__(kThreads, Store == TFX_STORE_ACT ? 2 : 3) read_kernel(const __grid_constant__ ReadArgs a) {
+  using Word = typename std::conditional<Store == TFX_STORE_ACT, uint4, uint2>::type;  // 8 values
+  __shared__ Blocks ring[2];
   griddep_wait();
   griddep_launch();
-  const int t0 = blockIdx.x * a.per, rows = min(a.per, a.rows - t0);
-  for (int r = threadIdx.x >> 5; r < rows; r += kReadThreads / 32) {
-    const int t = t0 + r, i = entry_of(a.offsets, a.n, t);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = a.heads * D, parts = (row + 255) / 256, step = row / 8;
+  const int windows = (int)(((long long)a.rows + a.per - 1) / a.per);
+  auto look_up = [&](int window, Blocks& w) {
+    const int t0 = window * a.per, rows = min(a.per, a.rows - t0);
+    const int i = entries_of(a.offsets, a.n, t0, rows), t = t0 + lane;
     const int begin = a.offsets[i], end = a.offsets[i + 1], s = a.seqs[i];
+    const bool listed = lane < rows && t >= begin && t < end;
     const long long pos = (long long)a.starts[i] + (t - begin);
-    int page = -1;
-    if ((unsigned)s < (unsigned)a.slots && pos >= 0 && pos < a.lens[s] && pos / a.page_size < a.width)
+    int page = -1, len = 0;
+    if (listed && (unsigned)s < (unsigned)a.slots && pos >= 0 && pos < (len = a.lens[s]) && pos / a.page_size < a.width)
       page = a.table[(long long)s * a.width + pos / a.page_size];
-    if (threadIdx.x % 32 == 0) {
-      const bool listed = t >= begin && t < end, there = page >= 0 && page < a.pages;
-      to[r] = !listed ? -2 : there ? (long long)page * a.page_size + pos % a.page_size : -1;
-      if (listed && !there) atomicOr(&a.book[0], TFX_CACHE_BAD);
-    }
-  }
-  __syncthreads();
-  const int words = a.heads * a.dim / kValues, all = rows * 2 * words;
-  constexpr int kAhead = 4;
-  for (int c0 = threadIdx.x; c0 < all; c0 += kReadThreads * kAhead) {
-    uint4 x[kAhead];
-    float scale[kAhead];
+    const bool there = page >= 0 && page < a.pages;
+    if (listed && !there) atomicOr(&a.book[0], TFX_CACHE_BAD);
+    const int in = (int)(pos & (kBlock - 1));
+    w.list(listed && (!there || t == begin || in == 0), t, there ? (long long)page * a.page_size + pos % a.page_size : -1,
+           there ? (int)min((long long)min(min(kBlock - in, end - t), a.rows - t), len - pos) : 1);
+  };
+  auto run = [&](const Task& k, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    const long long ld = (k.value ? a.ldv : a.ldk) / 8;
+    const Word* src = reinterpret_cast<const Word*>(k.value ? a.v : a.k) + k.to * step + k.at / 8;
+    uint4* out = reinterpret_cast<uint4*>(k.value ? a.v_out : a.k_out) + k.t * ld + k.at / 8;
+    const bool there = k.mine && (kWhole || k.to >= 0);
+    Word x[kBlock];
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) {
-      const int c = c0 + j * kReadThreads, r = c / (2 * words), rest = c - r * 2 * words;
-      const bool value = rest >= words;
-      const int w = value ? rest - words : rest;
-      const long long from = c < all ? to[r] : -2;
-      x[j] = make_uint4(0, 0, 0, 0);
-      scale[j] = 0.f;
-      if (from < 0) continue;
-      x[j] = __ldcs(reinterpret_cast<const uint4*>(value ? a.v : a.k) + from * words + w);
-      if (Store != TFX_STORE_ACT) scale[j] = (value ? a.v_scale : a.k_scale)[from / kBlock * a.heads + w * kValues / a.dim];
-    }
+    for (int j = 0; j < kBlock; j++) x[j] = there && (kWhole || j < k.n) ? __ldcs(src + j * step) : Word{};
+    const float scale = Store != TFX_STORE_ACT && there ? (k.value ? a.v_scale : a.k_scale)[k.block * a.heads + k.at / D] : 0.f;
 #pragma unroll
-    for (int j = 0; j < kAhead; j++) {
-      const int c = c0 + j * kReadThreads, r = c / (2 * words), rest = c - r * 2 * words;
-      const bool value = rest >= words;
-      const int w = value ? rest - words : rest;
-      if (c >= all || to[r] == -2) continue;
-      uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<T*>(value ? a.v_out : a.k_out) +
-                                            (long long)(t0 + r) * (value ? a.ldv : a.ldk) + w * kValues);
-      if constexpr (Store == TFX_STORE_ACT) {
-        __stcs(out, x[j]);
-      } else {
-        const uint32_t code[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        uint32_t y[8];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-          float f[4];
-          values4<Store>(code[k], f);
-          y[2 * k] = pack2<T>(f[0] * scale[j], f[1] * scale[j]);
-          y[2 * k + 1] = pack2<T>(f[2] * scale[j], f[3] * scale[j]);
+    for (int j = 0; j < kBlock; j++)
+      if (k.mine && (kWhole || j < k.n)) {
+        if constexpr (Store == TFX_STORE_ACT) {
+          __stcs(out + j * ld, x[j]);
+        } else {
+          float f[4], g[4];
+          values4<Store>(x[j].x, f);
+          values4<Store>(x[j].y, g);
+          __stcs(out + j * ld, make_uint4(pack2<T>(f[0] * scale, f[1] * scale), pack2<T>(f[2] * scale, f[3] * scale),
+                                          pack2<T>(g[0] * scale, g[1] * scale), pack2<T>(g[2] * scale, g[3] * scale)));
         }
-        __stcs(out, make_uint4(y[0], y[1], y[2], y[3]));
-        __stcs(out + 1, make_uint4(y[4], y[5], y[6], y[7]));
       }
+  };
+  if (warp == 0) look_up(blockIdx.x, ring[0]);
+  __syncthreads();
+  int b = 0;
+  for (int window = blockIdx.x; window < windows; window += gridDim.x, b ^= 1, __syncthreads()) {
+    if (warp == 0 && window + (int)gridDim.x < windows) look_up(window + gridDim.x, ring[b ^ 1]);
+    const int all = ring[b].n * 2 * parts;
+    for (int it; (it = take(&ring[b].taken)) < all;) {
+      const Task k = task_of(ring[b], it, parts, row);
+      if (k.n == kBlock) run(k, std::true_type());
+      else run(k, std::false_type());
     }
   }
 }
 
+template <typename T, int Store>
+const void* read_of(int dim) {
+  return dim == 128 ? (const void*)read_kernel<T, Store, 128> : (const void*)read_kernel<T, Store, 256>;
+}
 template <typename T, int Store>
 const void* append_of(int dim) {
   return dim == 128 ? (const void*)append_q8_kernel<T, Store, 128> : (const void*)append_q8_kernel<T, Store, 256>;
 }
 
-}  // namespace
-
-// Rows that a CTA does: one where that leaves every SM `most` CTAs at most, else so many more.
-static int rows_per_cta(long long rows, int most) {
-  const long long per = (rows + multiprocessors() * most - 1) / (multiprocessors() * most);
-  return (int)(per < 1 ? 1 : per > kMostRows ? kMostRows : per);
+// Rows of a window, where `ctas` CTAs share them, and the CTAs that have any.
+int rows_per_window(long long rows, int ctas, int most) {
+  const long long per = (rows + ctas - 1) / ctas;
+  return (int)(per > most ? most : per);
+}
+unsigned ctas_of(long long rows, int per, int ctas) {
+  const long long windows = (rows + per - 1) / per;
+  return (unsigned)(windows < ctas ? windows : ctas);
 }
 
+}  // namespace
+
 int launch_append_q8(AppendArgs& a, int act, int store, int dim, cudaStream_t s) {
-  a.per = rows_per_cta(a.rows, 2);
+  const int ctas = 2 * multiprocessors();
+  a.per = rows_per_window(a.rows, ctas, kMostRows);
   const void* fn = store == TFX_STORE_I8
                        ? act == TFX_F16 ? append_of<__half, TFX_STORE_I8>(dim) : append_of<__nv_bfloat16, TFX_STORE_I8>(dim)
                    : act == TFX_F16 ? append_of<__half, TFX_STORE_E4M3>(dim)
                                     : append_of<__nv_bfloat16, TFX_STORE_E4M3>(dim);
-  return launch_kernel(fn, dim3((unsigned)((a.rows + a.per - 1) / a.per)), dim3(kAppendThreads), 0, s, &a,
-                       dependent_launches(), 1);
+  return launch_kernel(fn, dim3(ctas_of(a.rows, a.per, ctas)), dim3(kThreads), 0, s, &a, dependent_launches(), 1);
 }
 
 int launch_read(ReadArgs& a, int act, int store, cudaStream_t s) {
-  a.per = rows_per_cta(a.rows, 8);
+  const int ctas = 3 * multiprocessors();
+  a.per = rows_per_window(a.rows, ctas, kMostRows);
   const void* fn;
   if (store == TFX_STORE_ACT)  // 16 bits either way
-    fn = (const void*)read_kernel<__half, TFX_STORE_ACT>;
+    fn = read_of<__half, TFX_STORE_ACT>(a.dim);
   else if (store == TFX_STORE_I8)
-    fn = act == TFX_F16 ? (const void*)read_kernel<__half, TFX_STORE_I8> : (const void*)read_kernel<__nv_bfloat16, TFX_STORE_I8>;
+    fn = act == TFX_F16 ? read_of<__half, TFX_STORE_I8>(a.dim) : read_of<__nv_bfloat16, TFX_STORE_I8>(a.dim);
   else
-    fn = act == TFX_F16 ? (const void*)read_kernel<__half, TFX_STORE_E4M3>
-                        : (const void*)read_kernel<__nv_bfloat16, TFX_STORE_E4M3>;
-  return launch_kernel(fn, dim3((unsigned)((a.rows + (long long)a.per - 1) / a.per)), dim3(kReadThreads), 0, s, &a,
-                       dependent_launches(), 1);
+    fn = act == TFX_F16 ? read_of<__half, TFX_STORE_E4M3>(a.dim) : read_of<__nv_bfloat16, TFX_STORE_E4M3>(a.dim);
+  return launch_kernel(fn, dim3(ctas_of(a.rows, a.per, ctas)), dim3(kThreads), 0, s, &a, dependent_launches(), 1);
 }
 
 }  // namespace tfx

@@ -44,22 +44,26 @@ __device__ __forceinline__ float inverse_of(float scale) {
 // A NaN stays.
 __device__ __forceinline__ float larger_scale(float a, float b) { return a != a || a > b ? a : b; }
 
-// Two values in the codes' range; NaN becomes any code.
+// Codes of four values times inv, which is a power of two and brings them into the codes'
+// range; NaN becomes any code. For I8, one rounded operation adds 1.5 * 2^23, which leaves the
+// nearest whole number, ties to even, in the low bits (the conversion instruction runs at an
+// eighth of its rate).
 template <int Store>
-__device__ __forceinline__ uint32_t code2(float lo, float hi);
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float inv);
 template <>
-__device__ __forceinline__ uint32_t code2<TFX_STORE_I8>(float lo, float hi) {
-  return ((uint32_t)__float2int_rn(lo) & 0xffu) | ((uint32_t)__float2int_rn(hi) & 0xffu) << 8;
+__device__ __forceinline__ uint32_t code4<TFX_STORE_I8>(float a, float b, float c, float d, float inv) {
+  const float by = 12582912.f;
+  const uint32_t lo = __byte_perm(__float_as_uint(__fmaf_rn(a, inv, by)), __float_as_uint(__fmaf_rn(b, inv, by)), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(__fmaf_rn(c, inv, by)), __float_as_uint(__fmaf_rn(d, inv, by)), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
 }
 template <>
-__device__ __forceinline__ uint32_t code2<TFX_STORE_E4M3>(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+__device__ __forceinline__ uint32_t code4<TFX_STORE_E4M3>(float a, float b, float c, float d, float inv) {
+  uint32_t r;
+  asm("{ .reg .b16 lo, hi; cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1; cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3; mov.b32 %0, {lo, hi}; }"
+      : "=r"(r)
+      : "f"(a * inv), "f"(b * inv), "f"(c * inv), "f"(d * inv));
   return r;
-}
-template <int Store>
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
-  return code2<Store>(a, b) | code2<Store>(c, d) << 16;
 }
 
 // Values of the four codes in a word.
@@ -67,8 +71,9 @@ template <int Store>
 __device__ __forceinline__ void values4(uint32_t w, float (&x)[4]);
 template <>
 __device__ __forceinline__ void values4<TFX_STORE_I8>(uint32_t w, float (&x)[4]) {
+  w ^= 0x80808080u;  // 0x4b0000uu is 2^23 + uu
 #pragma unroll
-  for (int i = 0; i < 4; i++) x[i] = (float)(int8_t)(w >> (8 * i));
+  for (int i = 0; i < 4; i++) x[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f;
 }
 template <>
 __device__ __forceinline__ void values4<TFX_STORE_E4M3>(uint32_t w, float (&x)[4]) {
