@@ -173,6 +173,7 @@ int* lens_of(const tfx_cache* c) { return c->book + 4; }
 int* refs_of(const tfx_cache* c) { return lens_of(c) + c->slots; }
 int* tables_of(const tfx_cache* c) { return refs_of(c) + c->pages; }
 int64_t page_values(const tfx_cache* c) { return (int64_t)c->page_size * c->heads_kv * c->dim; }
+int page_shift(const tfx_cache* c) { return c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7; }
 int value_bytes(const tfx_cache* c) { return c->store == TFX_STORE_ACT ? 2 : 1; }
 int64_t page_scales(const tfx_cache* c) { return (int64_t)(c->page_size / TFX_CACHE_BLOCK) * c->heads_kv; }
 // A layer's pages and scales.
@@ -502,7 +503,7 @@ int tfx_cache_read(tfx_cache* c, int layer, const int32_t* seqs, const int32_t* 
   a.slots = c->slots;
   a.width = c->width;
   a.pages = c->pages;
-  a.page_size = c->page_size;
+  a.page_shift = page_shift(c);
   a.heads = c->heads_kv;
   a.dim = c->dim;
   return tfx::launch_read(a, c->act, c->store, stream);
@@ -593,7 +594,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.batch = batch;
   a.shared = coded ? shared / TFX_CACHE_BLOCK * TFX_CACHE_BLOCK : shared;
   a.page_size = c->page_size;
-  a.page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  a.page_shift = page_shift(c);
   a.pages = c->pages;
   a.slots = c->slots;
   a.width = c->width;

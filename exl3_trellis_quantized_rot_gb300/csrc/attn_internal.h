@@ -105,7 +105,7 @@ struct AppendArgs {
   int slots, width, pages, page_size;
   Grown grown;
   float *k_scale, *v_scale;  // 8-bit stores: the layer's
-  int heads, rows, per;  // per: rows of a CTA
+  int heads, rows, per;  // per: rows of a window
 };
 
 struct ReadArgs {
@@ -117,7 +117,7 @@ struct ReadArgs {
   int n, rows;
   int* book;
   const int *lens, *table;
-  int slots, width, pages, page_size, heads, dim, per;  // per: rows of a CTA
+  int slots, width, pages, page_shift, heads, dim, per, span;  // per: rows of a window; span: tokens of a task
 };
 
 enum Tables { kTablesNone = 0, kTablesFork = 1, kTablesCompact = 2 };

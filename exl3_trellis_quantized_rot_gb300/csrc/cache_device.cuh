@@ -21,10 +21,11 @@ __device__ __forceinline__ int entry_of(const int* offsets, int n, int t) {
 }
 
 // The same for the rows t0 .. t0 + rows - 1 (up to 32), a lane a row: the entries from the
-// first row's on are looked at together.
+// first row's on are looked at together, in a short list all of them.
 __device__ __forceinline__ int entries_of(const int* offsets, int n, int t0, int rows) {
   const int lane = threadIdx.x & 31;
-  const int i0 = entry_of(offsets, n, t0);
+  const int i0 = n <= 32 ? 0 : entry_of(offsets, n, t0);
+  if (rows == 1 && n > 32) return i0;
   const int ends = i0 + 1 + lane < n ? offsets[i0 + 1 + lane] : INT_MAX;
   int mine = i0;
   for (int r = 0; r < rows; r++) {

@@ -21,6 +21,15 @@ constexpr int kMostRows = 32;  // rows of the list that are looked at together: 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// Loads that stay where they are written: beside a test of their own the compiler moved them
+// to the values' use, one wait after another (a read of 43,695 tokens: 68 us instead of 48).
+__device__ __forceinline__ void load_here(uint2& x, const uint2* p) {
+  asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+}
+__device__ __forceinline__ void load_here(uint4& x, const uint4* p) {
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+}
+
 // The next of a window's tasks, for a warp.
 __device__ __forceinline__ int take(int* taken) {
   int it = 0;
@@ -62,7 +71,7 @@ struct Blocks {
     }
     if (lane == 0) {
       n = __popc(all);
-      taken = 0;
+      taken = kWarps;  // a warp's first one goes by its number
     }
   }
 };
@@ -106,19 +115,25 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
     const int in = at.pos % kBlock;
     w.list(at.to >= 0 && (t == at.begin || in == 0), t, at.to, min(min(kBlock - in, at.end - t), a.rows - t));
   };
-  auto run = [&](const Task& k, auto whole) {  // whole: 16 new tokens
+  // Of up to `most` new tokens, or (whole) of 16. One token has code of its own: what is laid out
+  // for 16 takes a warp that runs through it once longer to fetch than to run.
+  auto run = [&](const Task& k, auto most_of, auto whole) {
+    constexpr int kMost = decltype(most_of)::value;
     constexpr bool kWhole = decltype(whole)::value;
     const long long ld = k.value ? a.ldv : a.ldk;  // words of 8 values
     const uint4* src = reinterpret_cast<const uint4*>(k.value ? a.v_new : a.k_new) + k.t * ld + k.at / 8;
     uint2* codes = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(k.value ? a.v : a.k) + k.block * kBlock * row + k.at);
     float* scales = (k.value ? a.v_scale : a.k_scale) + k.block * a.heads + k.at / D;
-    uint4 x[kBlock];
+    uint4 x[kMost];
 #pragma unroll
-    for (int j = 0; j < kBlock; j++) x[j] = k.mine && (kWhole || j < k.n) ? __ldcs(src + j * ld) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < kMost; j++) {
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (k.mine && (kWhole || j < k.n)) load_here(x[j], src + j * ld);
+    }
     const float before = !kWhole && k.mine && k.in ? *scales : 0.f;
     uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < kBlock; j++)
+    for (int j = 0; j < kMost; j++)
       top = larger2<T>(larger2<T>(larger2<T>(larger2<T>(top, x[j].x), x[j].y), x[j].z), x[j].w);
     // magnitudes as the type's bits: their order is that of the values, and NaN is above all
     top = max(top & 0xffffu, top >> 16);
@@ -141,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
     }
     uint2* out = codes + (kWhole ? 0 : k.in * step);
 #pragma unroll
-    for (int j = 0; j < kBlock; j++)
+    for (int j = 0; j < kMost; j++)
       if (k.mine && (kWhole || j < k.n)) {
         const float2 p = pair_to_float(x[j].x, T()), q = pair_to_float(x[j].y, T());
         const float2 r = pair_to_float(x[j].z, T()), s = pair_to_float(x[j].w, T());
@@ -155,18 +170,23 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   for (int window = blockIdx.x; window < windows; window += gridDim.x, b ^= 1, __syncthreads()) {
     if (warp == 0 && window + (int)gridDim.x < windows) look_up(window + gridDim.x, ring[b ^ 1]);
     const int all = ring[b].n * 2 * parts;
-    for (int it; (it = take(&ring[b].taken)) < all;) {
+    for (int it = warp; it < all; it = take(&ring[b].taken)) {
       const Task k = task_of(ring[b], it, parts, row);
-      if (k.n == kBlock) run(k, std::true_type());
-      else run(k, std::false_type());
+      if (k.n == kBlock) run(k, std::integral_constant<int, kBlock>(), std::true_type());
+      else if (k.n == 1) run(k, std::integral_constant<int, 1>(), std::false_type());
+      else run(k, std::integral_constant<int, kBlock>(), std::false_type());
     }
   }
 }
 
-// The same for rows that are read: their tokens lie together in a block, and have its scale.
+constexpr int read_ctas(int store) { return store == TFX_STORE_ACT ? 4 : 6; }  // of an SM
+constexpr int kAhead = 8;     // tokens that a lane of a read has asked for
+
+// The same for rows that are read, a.span tokens of a block at a time: they lie together and
+// have its scale.
 // A row whose sequence does not hold its token stands for itself.
 template <typename T, int Store, int D>
-__global__ void __launch_bounds__(kThreads, Store == TFX_STORE_ACT ? 2 : 3) read_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, read_ctas(Store)) read_kernel(const __grid_constant__ ReadArgs a) {
   using Word = typename std::conditional<Store == TFX_STORE_ACT, uint4, uint2>::type;  // 8 values
   __shared__ Blocks ring[2];
   griddep_wait();
@@ -181,37 +201,17 @@ __global__ void __launch_bounds__(kThreads, Store == TFX_STORE_ACT ? 2 : 3) read
     const bool listed = lane < rows && t >= begin && t < end;
     const long long pos = (long long)a.starts[i] + (t - begin);
     int page = -1, len = 0;
-    if (listed && (unsigned)s < (unsigned)a.slots && pos >= 0 && pos < (len = a.lens[s]) && pos / a.page_size < a.width)
-      page = a.table[(long long)s * a.width + pos / a.page_size];
+    const long long column = pos >> a.page_shift;
+    if (listed && (unsigned)s < (unsigned)a.slots && pos >= 0 && column < a.width) {
+      len = a.lens[s];  // both at once
+      page = a.table[(long long)s * a.width + column];
+      if (pos >= len) page = -1;
+    }
     const bool there = page >= 0 && page < a.pages;
     if (listed && !there) atomicOr(&a.book[0], TFX_CACHE_BAD);
     const int in = (int)(pos & (kBlock - 1));
-    w.list(listed && (!there || t == begin || in == 0), t, there ? (long long)page * a.page_size + pos % a.page_size : -1,
-           there ? (int)min((long long)min(min(kBlock - in, end - t), a.rows - t), len - pos) : 1);
-  };
-  auto run = [&](const Task& k, auto whole) {
-    constexpr bool kWhole = decltype(whole)::value;
-    const long long ld = (k.value ? a.ldv : a.ldk) / 8;
-    const Word* src = reinterpret_cast<const Word*>(k.value ? a.v : a.k) + k.to * step + k.at / 8;
-    uint4* out = reinterpret_cast<uint4*>(k.value ? a.v_out : a.k_out) + k.t * ld + k.at / 8;
-    const bool there = k.mine && (kWhole || k.to >= 0);
-    Word x[kBlock];
-#pragma unroll
-    for (int j = 0; j < kBlock; j++) x[j] = there && (kWhole || j < k.n) ? __ldcs(src + j * step) : Word{};
-    const float scale = Store != TFX_STORE_ACT && there ? (k.value ? a.v_scale : a.k_scale)[k.block * a.heads + k.at / D] : 0.f;
-#pragma unroll
-    for (int j = 0; j < kBlock; j++)
-      if (k.mine && (kWhole || j < k.n)) {
-        if constexpr (Store == TFX_STORE_ACT) {
-          __stcs(out + j * ld, x[j]);
-        } else {
-          float f[4], g[4];
-          values4<Store>(x[j].x, f);
-          values4<Store>(x[j].y, g);
-          __stcs(out + j * ld, make_uint4(pack2<T>(f[0] * scale, f[1] * scale), pack2<T>(f[2] * scale, f[3] * scale),
-                                          pack2<T>(g[0] * scale, g[1] * scale), pack2<T>(g[2] * scale, g[3] * scale)));
-        }
-      }
+    w.list(listed && (!there || t == begin || in % a.span == 0), t, there ? ((long long)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1)) : -1,
+           there ? (int)min((long long)min(min(a.span - in % a.span, end - t), a.rows - t), len - pos) : 1);
   };
   if (warp == 0) look_up(blockIdx.x, ring[0]);
   __syncthreads();
@@ -219,10 +219,37 @@ __global__ void __launch_bounds__(kThreads, Store == TFX_STORE_ACT ? 2 : 3) read
   for (int window = blockIdx.x; window < windows; window += gridDim.x, b ^= 1, __syncthreads()) {
     if (warp == 0 && window + (int)gridDim.x < windows) look_up(window + gridDim.x, ring[b ^ 1]);
     const int all = ring[b].n * 2 * parts;
-    for (int it; (it = take(&ring[b].taken)) < all;) {
+    for (int it = warp; it < all; it = take(&ring[b].taken)) {
       const Task k = task_of(ring[b], it, parts, row);
-      if (k.n == kBlock) run(k, std::true_type());
-      else run(k, std::false_type());
+      if (!k.mine) continue;
+      const long long ld = (k.value ? a.ldv : a.ldk) / 8;
+      const Word* src = reinterpret_cast<const Word*>(k.value ? a.v : a.k) + k.to * step + k.at / 8;
+      uint4* out = reinterpret_cast<uint4*>(k.value ? a.v_out : a.k_out) + k.t * ld + k.at / 8;
+      const bool there = k.to >= 0;
+      const float scale = Store != TFX_STORE_ACT && there ? (k.value ? a.v_scale : a.k_scale)[k.block * a.heads + k.at / D] : 0.f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < k.n; j0 += kAhead, src += kAhead * step, out += kAhead * ld) {
+        const int n = k.n - j0;
+        Word x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; j++) {
+          x[j] = Word{};
+          if (there && j < n) load_here(x[j], src + j * step);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; j++)
+          if (j < n) {
+            if constexpr (Store == TFX_STORE_ACT) {
+              __stcs(out + j * ld, x[j]);
+            } else {
+              float f[4], g[4];
+              values4<Store>(x[j].x, f);
+              values4<Store>(x[j].y, g);
+              __stcs(out + j * ld, make_uint4(pack2<T>(f[0] * scale, f[1] * scale), pack2<T>(f[2] * scale, f[3] * scale),
+                                              pack2<T>(g[0] * scale, g[1] * scale), pack2<T>(g[2] * scale, g[3] * scale)));
+            }
+          }
+      }
     }
   }
 }
@@ -259,8 +286,13 @@ int launch_append_q8(AppendArgs& a, int act, int store, int dim, cudaStream_t s)
 }
 
 int launch_read(ReadArgs& a, int act, int store, cudaStream_t s) {
-  const int ctas = 3 * multiprocessors();
-  a.per = rows_per_window(a.rows, ctas, kMostRows);
+  const int ctas = read_ctas(store) * multiprocessors();
+  a.per = rows_per_window(a.rows, ctas, kMostRows / 2);
+  // Tokens of a task: as few as keep the SMs' first warps busy. Measured with 2, 4, 8, 16 tokens, 4
+  // heads of 256 (us on the GPU): 300 rows 3.2, 3.3, 3.9, 4.1; 2,000 rows 6.4, 4.9, 5.6, 7.2; 4,096
+  // rows 9.0, 7.2, 6.8, 8.8; 16,000 rows 28.0, 23.0, 21.3, 21.3; 43,695 rows 61.4, 46.6, 48.3, 48.0.
+  const long long warps = (long long)multiprocessors() * kWarps, parts = 2 * (((long long)a.heads * a.dim + 255) / 256);
+  a.span = a.rows * parts < 4 * warps ? 2 : a.rows * parts < 24 * warps ? 4 : 8;
   const void* fn;
   if (store == TFX_STORE_ACT)  // 16 bits either way
     fn = read_of<__half, TFX_STORE_ACT>(a.dim);

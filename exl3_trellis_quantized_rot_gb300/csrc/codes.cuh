@@ -66,27 +66,6 @@ __device__ __forceinline__ uint32_t code4<TFX_STORE_E4M3>(float a, float b, floa
   return r;
 }
 
-// Values of the four codes in a word.
-template <int Store>
-__device__ __forceinline__ void values4(uint32_t w, float (&x)[4]);
-template <>
-__device__ __forceinline__ void values4<TFX_STORE_I8>(uint32_t w, float (&x)[4]) {
-  w ^= 0x80808080u;  // 0x4b0000uu is 2^23 + uu
-#pragma unroll
-  for (int i = 0; i < 4; i++) x[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f;
-}
-template <>
-__device__ __forceinline__ void values4<TFX_STORE_E4M3>(uint32_t w, float (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; i++) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-
 // The four codes of a word as FP16: bytes (0, 1) and (2, 3), or (0, 2) and (1, 3).
 template <int Store, bool Split>
 __device__ __forceinline__ void halves(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -111,6 +90,18 @@ __device__ __forceinline__ void halves(uint32_t w, uint32_t& a, uint32_t& b) {
 // log2 of a scale, NaN of a NaN.
 __device__ __forceinline__ float log2_scale(float s) {
   return s == s ? (float)((int)(__float_as_uint(s) >> 23) - 127) : s;
+}
+
+// Values of the four codes in a word.
+template <int Store>
+__device__ __forceinline__ void values4(uint32_t w, float (&x)[4]) {
+  uint32_t a, b;
+  halves<Store, false>(w, a, b);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a)), g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  x[0] = f.x;
+  x[1] = f.y;
+  x[2] = g.x;
+  x[3] = g.y;
 }
 
 // BF16 values whose largest magnitude has the bits `top`: the power of two that brings it to
