@@ -277,17 +277,34 @@ int64_t prefix_rows(int64_t batch, int64_t heads_q, int64_t heads_kv) {
   return std::max(batch * heads_q, (int64_t)tfx::multiprocessors() / 2 * 256);
 }
 
+// Over 8-bit codes, the tokens of a prefix that the tensor cores read once; 0: each sequence
+// reads it as its own. That takes the warps as long as reading the prefix `batch` times, from L2
+// where it fits; the other kernel begins with 8 us. Measured, the tensor cores / as their own (us;
+// 100 own tokens): 24/4 heads of 256, 8,192 tokens and 2 sequences 16.6 / 16.4, 4: 21.7 / 19.2, 6: 22.6 /
+// 23.1, 16: 27.0 / 44.0; of 2,048 and 6: 19.5 / 13.5, 16: 22.8 / 19.0; of 32,768 and 2: 34.5 / 31.2, 3: 35.3 /
+// 38.5; 8/8 heads of 128, 8,192 and 4: 22.6 / 19.0, 8: 23.9 / 29.5; of 32,768 and 4: 43.5 / 52.3.
+int coded_prefix(const tfx_cache* c, int batch, int shared) {
+  shared = shared / TFX_CACHE_BLOCK * TFX_CACHE_BLOCK;
+  return batch > 2 && (int64_t)batch * shared * c->heads_kv * c->dim * 2 > (64LL << 20) ? shared : 0;
+}
+// Partial results of that kernel's shares, at most: as prefix_rows, in tiles of its own.
+int64_t coded_prefix_rows(int64_t batch, int64_t heads_q) {
+  return std::max(batch * heads_q, (int64_t)tfx::multiprocessors() * tfx::prefix_q8_rows());
+}
+
+int decode_warps(const tfx_cache* c) { return tfx::multiprocessors() * (c->store == TFX_STORE_ACT ? 4 : tfx::kCodedWarps); }
 // Decode scratch for `batch` sequences: byte offsets of its parts. No part shrinks with batch or heads.
 struct DecodeScratch {
   size_t runs, own_ml, pre_ml, own_o, pre_o, bytes;
 };
-DecodeScratch decode_scratch(int batch, int heads_q, int heads_kv, int dim, int warps) {
+DecodeScratch decode_scratch(const tfx_cache* c, int batch, int heads_q) {
+  const int heads_kv = c->heads_kv, dim = c->dim, warps = decode_warps(c);
   const int64_t group = heads_q / heads_kv, tiles = (group + kRowTile - 1) / kRowTile;
   const int64_t ptiles = (batch * group + kRowTile - 1) / kRowTile;
   const int64_t own_rows = group < kRowTile ? group : kRowTile;
   const int64_t own = (warps + heads_kv * tiles * batch) * own_rows;
   const int64_t few = (warps + heads_kv * ptiles) * kRowTile, many = prefix_rows(batch, heads_q, heads_kv);
-  const int64_t pre = few > many ? few : many;
+  const int64_t pre = c->store != TFX_STORE_ACT ? coded_prefix_rows(batch, heads_q) : few > many ? few : many;
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
   DecodeScratch d;
   int64_t at = 0;
@@ -304,7 +321,6 @@ DecodeScratch decode_scratch(int batch, int heads_q, int heads_kv, int dim, int 
   d.bytes = (size_t)at;
   return d;
 }
-int decode_warps(const tfx_cache* c) { return tfx::multiprocessors() * (c->store == TFX_STORE_ACT ? 4 : tfx::kCodedWarps); }
 
 // Rows of the given lists (null: the last extend's).
 int append_rows(tfx_cache* c, int layer, const void* k, int64_t ldk, const void* v, int64_t ldv, int rows,
@@ -432,7 +448,7 @@ int tfx_cache_reserve(tfx_cache* c, int max_batch, int heads_q, cudaStream_t str
     return fail_with(TFX_ECUDA, "clearing %zu bytes failed", page_scratch_ints(c) * 4);
   }
   const int b = max_batch > pv->max_batch ? max_batch : pv->max_batch, hq = heads_q > pv->heads_q ? heads_q : pv->heads_q;
-  const size_t part = decode_scratch(b, hq, c->heads_kv, c->dim, decode_warps(c)).bytes;
+  const size_t part = decode_scratch(c, b, hq).bytes;
   if ((rc = grow(reinterpret_cast<void**>(&pv->part), &pv->part_bytes, part, stream))) return rc;
   pv->max_batch = b;
   pv->heads_q = hq;
@@ -592,13 +608,13 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   a.heads_kv = h->heads_kv;
   a.group = h->heads_q / h->heads_kv;
   a.batch = batch;
-  a.shared = coded ? shared / TFX_CACHE_BLOCK * TFX_CACHE_BLOCK : shared;
+  a.shared = coded ? coded_prefix(c, batch, shared) : shared;
   a.page_size = c->page_size;
   a.page_shift = page_shift(c);
   a.pages = c->pages;
   a.slots = c->slots;
   a.width = c->width;
-  if (coded && many_rows(batch, a.group) && a.shared >= 256) {
+  if (coded && a.shared) {
     const int64_t rows = (int64_t)batch * a.group, per = tfx::prefix_q8_rows();
     a.mt = (int)((rows + per - 1) / per);
     const int64_t rest = (int64_t)c->heads_kv * a.mt, fill = tfx::multiprocessors() / rest, tiles = tfx::prefix_q8_tiles(a.shared);
@@ -607,8 +623,6 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
     a.pre_splits = (int)((tiles + most - 1) / most);
     if (rest * a.pre_splits > INT32_MAX) return fail_with(TFX_EUNSUPPORTED, "%lld tiles of rows", (long long)rest);
     a.items = (int)(rest * a.pre_splits);
-    a.codes_k = static_cast<const uint8_t*>(kl);
-    a.codes_v = static_cast<const uint8_t*>(vl);
   }
   if (!coded && many_rows(batch, a.group) && shared >= 256) {
     a.per_tile = heads_per_tile(a.group);
@@ -627,7 +641,7 @@ int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void
   }
   a.warps = decode_warps(c);
   a.own_rows = a.group < kRowTile ? a.group : kRowTile;
-  const DecodeScratch d = decode_scratch(batch, h->heads_q, c->heads_kv, c->dim, a.warps);
+  const DecodeScratch d = decode_scratch(c, batch, h->heads_q);
   if (d.bytes > pv->part_bytes)
     return fail_with(TFX_ENOTRESERVED, "%d sequences of %d heads take more scratch than was reserved", batch, h->heads_q);
   a.runs = reinterpret_cast<int2*>(pv->part + d.runs);

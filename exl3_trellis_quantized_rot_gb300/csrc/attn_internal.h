@@ -69,8 +69,7 @@ struct DecodeAttnArgs {
   float2* pre_ml;
   int* err;
   long long spin;
-  const uint8_t *codes_k, *codes_v;  // 8-bit stores: the layer's pages and scales
-  const float *k_scale, *v_scale;
+  const float *k_scale, *v_scale;  // 8-bit stores: the layer's
 };
 
 // What appends need to know of the extends before them. Only an extend writes it,

@@ -19,7 +19,8 @@
 //
 // A warp owns its rows, its slices (8 KB of K and V of one K/V head: 16 keys of 256, 32 of
 // 128) and a ring of three of them, which it fills itself, a slice as soon as one is done.
-// Every warp gets the same number of slices, as in attn_warp.cu; decode_join_kernel joins.
+// Every warp gets the same number of slices, as in attn_warp.cu; decode_join_kernel joins. A
+// long prefix that many sequences share is attn_q8_tc.cu's; here keys begin behind it.
 #include <cuda_fp16.h>
 
 #include "attn_split.cuh"
@@ -67,7 +68,6 @@ struct Rows {
   float o[NT][D / 16][4];     // O^T: dims 16 i + 2 g (elements 0, 1) and + 1 (2, 3)
   float m[NT][2], M[NT][2], l[NT][2];
   float by[NT][2];  // factor of the scores
-  int hi[NT][2];    // keys the row sees end here
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -188,25 +188,12 @@ struct Ring {
   }
 };
 
-// The rows against slices [s0, s1) of the keys lo <= key < hi. False: a wait gave up.
+// The rows against slices [s0, s1) of a sequence's keys lo <= key < hi. False: a wait gave up.
 template <int Store, int NT, int D>
 __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const DecodeAttnArgs& a, const Walk& w,
-                                       const int* starts, int s0, int s1, int lo, int lane) {
+                                       const int* starts, int s0, int s1, int lo, int hi, int lane) {
   constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks, kStages = Shape<NT, D>::kStages;
   const int g = lane >> 2, mi = lane >> 3, mr = lane & 7;
-  int hmin = INT_MAX, hmax = 0;
-#pragma unroll
-  for (int n = 0; n < NT; n++)
-#pragma unroll
-    for (int c = 0; c < 2; c++) {
-      hmin = min(hmin, R.hi[n][c]);
-      hmax = max(hmax, R.hi[n][c]);
-    }
-#pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
-    hmin = min(hmin, __shfl_xor_sync(~0u, hmin, d));
-    hmax = max(hmax, __shfl_xor_sync(~0u, hmax, d));
-  }
   // 16-byte column c of a key's 8: where the copies' 128-byte swizzle put it
   const int key = (mi & 1) * 8 + mr;
   auto at = [&](int block, int c) {
@@ -220,11 +207,11 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const De
     uint8_t* vb = kb + Slice<D>::kHalf;
     const float* sc = rg.scales + st * 2 * NB;
     const int k0 = s * KS;
-    const bool edge = k0 < lo || k0 + KS > hmin;
+    const bool edge = k0 < lo || k0 + KS > hi;
     // what no row may see: 0 * NaN would be NaN in the product, so V's codes there become zeros
-    if (k0 < lo || k0 + KS > hmax) {
+    if (edge) {
       for (int r = 0; r < KS; r++)
-        if (k0 + r < lo || k0 + r >= hmax)
+        if (k0 + r < lo || k0 + r >= hi)
           for (int c = lane; c < D / 16; c += 32)
             *reinterpret_cast<uint4*>(vb + (r >> 4) * Slice<D>::kBlock + (c >> 3) * 2048 + (r & 15) * 128 + (c & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -264,7 +251,7 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const De
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             const int k = k0 + b * 16 + g + (c >> 1) * 8;
-            if (k < lo || k >= R.hi[n][c & 1]) sx[b][n][c] = -INFINITY;
+            if (k < lo || k >= hi) sx[b][n][c] = -INFINITY;
           }
       }
     }
@@ -388,29 +375,18 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, 1)
   bool ok = true;
   while (ok && x < end) {
     const Segment g = segment_at<KS, 8 * NT>(a, w, starts, x, end);
-    auto source = [&](int r, int* seq) {  // row r of the tile: its row of q, its sequence
-      const int row = g.row0 + (r < g.rows ? r : 0);
-      *seq = g.prefix ? row / a.group : g.seq;
-      const int head = g.head * a.group + (g.prefix ? row % a.group : row);
-      return r < g.rows ? q + (long long)*seq * a.ldq + (long long)head * D : nullptr;
-    };
+    const int len = seq_len(a, g.seq);
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      int seq;
-      R.load(n, source(8 * n + (lane >> 2), &seq), a.scale_log2, lane);
-#pragma unroll
-      for (int c = 0; c < 2; c++) {
-        const bool in = source(8 * n + 2 * (lane & 3) + c, &seq) != nullptr;
-        const int len = seq_len(a, seq);
-        R.hi[n][c] = !g.prefix ? len : in ? min(a.shared, len) : 0;
-      }
+      const int r = 8 * n + (lane >> 2), head = g.head * a.group + g.row0 + r;
+      R.load(n, r < g.rows ? q + (long long)g.seq * a.ldq + (long long)head * D : nullptr, a.scale_log2, lane);
     }
     R.reset();
-    ok = attend<Store>(R, rg, a, w, starts, g.s0, g.s1, g.prefix ? 0 : a.shared, lane);
+    ok = attend<Store>(R, rg, a, w, starts, g.s0, g.s1, a.shared, len, lane);
     if (!ok) break;
     const long long slot = me + g.group;
-    float* po = g.prefix ? a.pre_o + slot * 16 * D : a.own_o + slot * a.own_rows * D;
-    float2* pml = g.prefix ? a.pre_ml + slot * 16 : a.own_ml + slot * a.own_rows;
+    float* po = a.own_o + slot * a.own_rows * D;
+    float2* pml = a.own_ml + slot * a.own_rows;
     x += g.s1 - g.s0;
 #pragma unroll
     for (int n = 0; n < NT; n++)
@@ -442,8 +418,7 @@ int run_of(DecodeAttnArgs& a, cudaStream_t s) {
 }
 template <typename T, int Store>
 int run_of(DecodeAttnArgs& a, int dim, cudaStream_t s) {
-  // a prefix's rows fill 16 columns; a group of up to 8 rows does not
-  const bool few = a.group <= 8 && (a.shared == 0 || a.pre_splits);
+  const bool few = a.group <= 8;
   if (dim == 128) return few ? run_of<T, Store, 1, 128>(a, s) : run_of<T, Store, 2, 128>(a, s);
   return few ? run_of<T, Store, 1, 256>(a, s) : run_of<T, Store, 2, 256>(a, s);
 }

@@ -142,6 +142,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
     const float2 most = pair_to_float(top, T());
     const float scale = larger_scale(before, scale_for<Store>(__float_as_uint(most.x)));
     const float inv = inverse_of(scale);
+    // a block of scale NaN holds zeros: rows that see nothing of it multiply its codes by 0
+    const uint32_t keep = scale == scale ? ~0u : 0u;
     if (!kWhole && k.mine && k.in && scale != before) {
       const float by = before * inv;
       for (int j = 0; j < k.in; j++) {
@@ -149,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
         float f[4], g[4];
         values4<Store>(c.x, f);
         values4<Store>(c.y, g);
-        c.x = code4<Store>(f[0], f[1], f[2], f[3], by);
-        c.y = code4<Store>(g[0], g[1], g[2], g[3], by);
+        c.x = code4<Store>(f[0], f[1], f[2], f[3], by) & keep;
+        c.y = code4<Store>(g[0], g[1], g[2], g[3], by) & keep;
         codes[j * step] = c;
       }
     }
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
       if (k.mine && (kWhole || j < k.n)) {
         const float2 p = pair_to_float(x[j].x, T()), q = pair_to_float(x[j].y, T());
         const float2 r = pair_to_float(x[j].z, T()), s = pair_to_float(x[j].w, T());
-        out[j * step] = make_uint2(code4<Store>(p.x, p.y, q.x, q.y, inv), code4<Store>(r.x, r.y, s.x, s.y, inv));
+        out[j * step] = make_uint2(code4<Store>(p.x, p.y, q.x, q.y, inv) & keep, code4<Store>(r.x, r.y, s.x, s.y, inv) & keep);
       }
     if (k.mine && k.at % D == 0) *scales = scale;
   };

@@ -176,7 +176,8 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * them must then be finite). A sequence that holds no token, or a slot out of
  * range, gives zeros. h->heads_kv, dim and act are the cache's. Same arithmetic as
  * tfx_attn_prompt, with partial results of FP32 joined in a fixed order.
- * Over an 8-bit store, whole blocks of the first `shared` tokens are read through the
+ * Over an 8-bit store, in a batch above 2 whose sequences would read more than 64 MiB of
+ * codes there (batch * shared tokens), the whole blocks of the first `shared` tokens are read through the
  * one table, the tokens behind the last whole block through each sequence's own; q
  * and the probabilities (times a block's scale) are matrix operands of FP16, q of
  * BF16 after a power of two that brings the row's largest magnitude below 2^15. */

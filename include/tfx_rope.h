@@ -28,10 +28,10 @@ typedef struct {
 } tfx_rope;
 
 /* The n frequencies (radians a position, finite, host memory) as fractions of a
- * turn in 64 bits (host memory). A position times such a fraction wraps exactly, so
- * an angle is good to 2^-63 of a turn a position and FP32's rounding, however far the
- * position. Scalings for long contexts are the caller's choice of frequencies and
- * gain. Host only. */
+ * turn in 64 bits (host memory). A position times such a fraction wraps exactly, so an
+ * angle has the frequency's own rounding (2^-52 of it, in 64-bit floating point) and
+ * FP32's, however far the position. Scalings for long contexts are the caller's choice
+ * of frequencies and gain. Host only. */
 int tfx_rope_table(const double* freqs, int n, uint64_t* table);
 
 /* Rows of q (heads_q heads of dim values next to each other, ldq elements apart)

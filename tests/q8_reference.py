@@ -83,11 +83,11 @@ def attend(q, k, v, scale):
     return p @ v, p @ v.abs(), (q.abs() @ k.abs().T).max() * scale
 
 
-def assert_near(got, out, A, qk, n, dim, most):
+def assert_near(got, out, A, qk, n, dim, most, largest=0.0):
     u = U[got.dtype]
     es = 2 * (dim * 2.0 ** -23 * qk + 2.0 ** -19)
     ea = 2 * (n / 8 + 64) * 2.0 ** -23
-    tol = u * out.abs() + (2.0 ** -11 + es + ea) * A + n * 2.0 ** -32 * most
+    tol = u * out.abs() + (2.0 ** -11 + es + ea) * A + n * (2.0 ** -32 * most + 2.0 ** -126 * largest)
     d = (got.double() - out).abs()
     assert torch.isfinite(got).all()
     assert bool((d <= tol).all()), f"error {float(d.max()):.3e}, {float((d / tol.clamp(min=1e-300)).max()):.2f} of its bound"
