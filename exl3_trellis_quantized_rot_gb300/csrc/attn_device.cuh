@@ -24,6 +24,11 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* tm, in
   tma_load_5d(s_addr(dst), tm, c0, c1, c2, c3, c4, b);
 }
 
+// A map's descriptor on its way, ahead of the first copy by it.
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

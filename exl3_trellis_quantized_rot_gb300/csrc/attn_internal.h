@@ -10,7 +10,7 @@
 
 namespace tfx {
 
-constexpr int kCodedWarps = 12;    // of a CTA of the decode kernel over 8-bit codes, at most
+constexpr int kCodedWarps = 8;     // of a CTA of the decode kernel over 8-bit codes
 constexpr int kAttnMaxSeqs = 512;  // sequences of one prompt launch (longer lists take several launches)
 
 // Work of one prompt launch, in the kernel's parameters: nothing is copied to
@@ -146,7 +146,7 @@ int launch_join(const DecodeAttnArgs& a, int act, int dim, bool wide, cudaStream
 int prefix_q8_rows();            // rows of a tile of that kernel
 int prefix_q8_tiles(int shared);  // key tiles of the prefix
 int launch_prefix_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
-int launch_decode_q8(DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
+int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s);
 
 // exl3_host.cu
 tfx_exl3_driver driver_hooks();

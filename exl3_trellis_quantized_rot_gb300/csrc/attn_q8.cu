@@ -29,6 +29,8 @@
 namespace tfx {
 namespace {
 
+constexpr int kThreads = kCodedWarps * 32;
+constexpr int kStages = 3;     // of a warp's ring
 constexpr int kFewest = 2;     // slices a warp takes at least
 constexpr float kShift = 7.f;  // the largest weight is 2^kShift: 11 bits down to 2^-21 of it
 
@@ -40,13 +42,7 @@ struct Slice {
   static constexpr int kBlock = 16 * D;   // bytes of one copy of 16 tokens
   static constexpr int kStage = 2 * kHalf;
 };
-// Warps of a CTA, and stages of each one's ring.
-template <int NT, int D>
-struct Shape {
-  static constexpr int kWarps = 8;
-  static constexpr int kStages = 3;
-};
-constexpr size_t kSmem = 24 * 8192 + 1024;
+constexpr size_t kSmem = kCodedWarps * kStages * 8192 + 1024;
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -121,8 +117,7 @@ struct Rows {
 // A warp's ring, and what of its slices is asked for.
 template <int D, int NT>
 struct Ring {
-  static constexpr int kStages = Shape<NT, D>::kStages, Rows = 8 * NT;
-  static constexpr int NB = Slice<D>::kBlocks;
+  static constexpr int Rows = 8 * NT, NB = Slice<D>::kBlocks;
   uint8_t* buf;
   uint64_t* full;
   float* scales;    // [kStages][K, V][NB]
@@ -192,7 +187,7 @@ struct Ring {
 template <int Store, int NT, int D>
 __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const DecodeAttnArgs& a, const Walk& w,
                                        const int* starts, int s0, int s1, int lo, int hi, int lane) {
-  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks, kStages = Shape<NT, D>::kStages;
+  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks;
   const int g = lane >> 2, mi = lane >> 3, mr = lane & 7;
   // 16-byte column c of a key's 8: where the copies' 128-byte swizzle put it
   const int key = (mi & 1) * 8 + mr;
@@ -337,10 +332,8 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const De
 }
 
 template <typename T, int Store, int NT, int D>
-__global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, 1)
-    decode_q8_kernel(const __grid_constant__ DecodeAttnArgs a) {
-  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks;
-  constexpr int kWarps = Shape<NT, D>::kWarps, kStages = Shape<NT, D>::kStages;
+__global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const __grid_constant__ DecodeAttnArgs a) {
+  constexpr int KS = Slice<D>::kKeys, NB = Slice<D>::kBlocks, kWarps = kCodedWarps;
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ float scales[kWarps][kStages * 2 * NB];
@@ -351,6 +344,8 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, 1)
     // a slice's bytes, and its scales
     for (int i = 0; i < kWarps * kStages; i++) mbar_init(&full[0][0] + i, 2);
     fence_mbar_init();
+    tma_prefetch(&a.k);
+    tma_prefetch(&a.v);
   }
   // after the tensor-core kernel, this one starts where that leaves room: see attn_warp.cu
   if (!a.pre_splits) griddep_wait();
@@ -408,16 +403,15 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, 1)
 }
 
 template <typename T, int Store, int NT, int D>
-int run_of(DecodeAttnArgs& a, cudaStream_t s) {
-  a.warps = multiprocessors() * Shape<NT, D>::kWarps;
+int run_of(const DecodeAttnArgs& a, cudaStream_t s) {
   const void* fn = (const void*)decode_q8_kernel<T, Store, NT, D>;
   const int rc = opt_in_smem(fn, kSmem);
   if (rc) return rc;
-  return launch_kernel(fn, dim3((unsigned)multiprocessors()), dim3(Shape<NT, D>::kWarps * 32), kSmem, s, &a,
+  return launch_kernel(fn, dim3((unsigned)multiprocessors()), dim3(kThreads), kSmem, s, const_cast<DecodeAttnArgs*>(&a),
                        dependent_launches(), 1);
 }
 template <typename T, int Store>
-int run_of(DecodeAttnArgs& a, int dim, cudaStream_t s) {
+int run_of(const DecodeAttnArgs& a, int dim, cudaStream_t s) {
   const bool few = a.group <= 8;
   if (dim == 128) return few ? run_of<T, Store, 1, 128>(a, s) : run_of<T, Store, 2, 128>(a, s);
   return few ? run_of<T, Store, 1, 256>(a, s) : run_of<T, Store, 2, 256>(a, s);
@@ -425,7 +419,7 @@ int run_of(DecodeAttnArgs& a, int dim, cudaStream_t s) {
 
 }  // namespace
 
-int launch_decode_q8(DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s) {
+int launch_decode_q8(const DecodeAttnArgs& a, int act, int store, int dim, cudaStream_t s) {
   int rc;
   if (store == TFX_STORE_I8)
     rc = act == TFX_F16 ? run_of<__half, TFX_STORE_I8>(a, dim, s) : run_of<__nv_bfloat16, TFX_STORE_I8>(a, dim, s);

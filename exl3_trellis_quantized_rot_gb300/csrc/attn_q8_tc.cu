@@ -190,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
     mbar_init(&bars.q_full, kSoft);
     mbar_init(&bars.ends_full, kSoft / 2);
     fence_mbar_init();
+    tma_prefetch(&a.k);
+    tma_prefetch(&a.v);
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(s_addr(&tmem_slot)) : "memory");
