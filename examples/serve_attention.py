@@ -1,13 +1,11 @@
 """The attention half of one layer, as a serving engine runs it: q/k/v group ->
-K/V cache -> attention -> o_proj, for a system prompt, the chats that share it,
-and the steps in which each of them gets its next token.
+rotary positions -> K/V cache -> attention -> o_proj, for a system prompt, the chats that
+share it, and the steps in which each of them gets its next token.
 
-    python examples/serve_attention.py
+    python examples/serve_attention.py [int8 | e4m3]
 
-Weights and activations are synthetic, and q and k go to attention as the group gives
-them: a model that normalises or rotates them does so in between, before ``cache_append``.
-``Layer`` is the layer, ``serve`` the
-life of a small batch; it returns what each step computed.
+With int8 or e4m3 the cache holds codes of 8 bits. Weights and activations are synthetic.
+``Layer`` is the layer, ``serve`` the life of a small batch; it returns what each step computed.
 """
 from __future__ import annotations
 
@@ -36,26 +34,32 @@ def weight(seed: int, K: int, N: int, member: int = 0, max_rows: int = 1024) -> 
 
 
 class Layer:
-    def __init__(self, slots: int, pages: int, page_size: int, width: int):
+    def __init__(self, slots: int, pages: int, page_size: int, width: int, store=torch.float16):
         self.qkv = [weight(1, HIDDEN, n * DIM, m) for m, n in enumerate((HEADS, KV_HEADS, KV_HEADS))]
         self.o = weight(2, HEADS * DIM, HIDDEN)
         shape = (1, pages, page_size, KV_HEADS, DIM)
         # pages are never read past what a sequence holds: what they contain before does not matter
-        self.cache = tfx.Cache(torch.empty(shape, dtype=torch.float16, device="cuda"),
-                               torch.empty(shape, dtype=torch.float16, device="cuda"), slots, width)
+        self.cache = tfx.Cache(torch.empty(shape, dtype=store, device="cuda"), torch.empty(shape, dtype=store, device="cuda"),
+                               slots, width, act=torch.float16)
+        self.rope = tfx.Rope(DIM, rotary=DIM // 4)  # a quarter of each head
         tfx.cache_reserve(self.cache, max_batch=slots, heads=HEADS)
 
-    def project(self, x, seqs, offsets):
-        """q of the rows x; their k and v join the cache, rows offsets[i]:offsets[i+1] as sequence seqs[i]'s next tokens."""
+    def project(self, x, seqs, offsets, positions=None):
+        """q of the rows x, rotated to their positions (of single tokens: what their sequences hold); their k and v
+        join the cache, rows offsets[i]:offsets[i+1] as sequence seqs[i]'s next tokens."""
         q, k, v = (y.unflatten(1, (-1, DIM)) for y in tfx.group(self.qkv, x))
-        tfx.cache_extend(self.cache, seqs, offsets)  # once a step; append once a layer
+        tfx.cache_extend(self.cache, seqs, offsets)  # once a step; rope and append once a layer
+        if positions is None:
+            positions = self.cache.lens[seqs] - 1
+        tfx.rope(self.rope, q, k, positions, out=(q, k))  # in place
         tfx.cache_append(self.cache, 0, k, v)
         return q, k, v
 
     def prompt(self, x, slot: int):
         """A whole prompt into an empty slot."""
         ends = torch.tensor([0, x.shape[0]], dtype=torch.int32)
-        q, k, v = self.project(x, torch.tensor([slot], dtype=torch.int32, device="cuda"), ends.cuda())
+        q, k, v = self.project(x, torch.tensor([slot], dtype=torch.int32, device="cuda"), ends.cuda(),
+                               torch.arange(x.shape[0], dtype=torch.int32, device="cuda"))
         a = tfx.attn_prompt(q, k, v, ends)
         return q, a, tfx.linear(self.o, a.flatten(1))
 
@@ -66,14 +70,14 @@ class Layer:
         return q, a, tfx.linear(self.o, a.flatten(1))
 
 
-def serve(system: int = 300, chats: int = 8, steps: int = 3, page_size: int = 32):
+def serve(system: int = 300, chats: int = 8, steps: int = 3, page_size: int = 32, store=torch.float16):
     """A system prompt, `chats` forks of it, some steps, then half of them end and the pool is compacted."""
     g = torch.Generator(device="cuda")
     g.manual_seed(0)
     rows = lambda n: torch.randn((n, HIDDEN), generator=g, device="cuda").half()  # noqa: E731
     ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
     width = (system + 4 * steps) // page_size + 2
-    layer = Layer(slots=chats + 1, pages=width + 3 * chats, page_size=page_size, width=width)
+    layer = Layer(slots=chats + 1, pages=width + 3 * chats, page_size=page_size, width=width, store=store)
     told = [("prompt", layer.prompt(rows(system), 0), [0])]
     live = list(range(1, chats + 1))
     tfx.cache_fork(layer.cache, ints(*[0] * chats), ints(*live))
@@ -88,7 +92,7 @@ def serve(system: int = 300, chats: int = 8, steps: int = 3, page_size: int = 32
 
 
 def main() -> None:
-    layer, told = serve()
+    layer, told = serve(store={"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[sys.argv[1]] if sys.argv[1:] else torch.float16)
     for kind, (_, a, y), live in told:
         print(f"{kind:7s} sequences {live}: attention {tuple(a.shape)}, layer output rms {float(y.float().square().mean().sqrt()):.3f}")
     c = layer.cache

@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = kCodedWarps * 32;
 constexpr int kStages = 3;     // of a warp's ring
-constexpr int kFewest = 2;     // slices a warp takes at least
+constexpr int kFewest = 1;     // slices a warp takes at least (one sequence of 1,000 tokens: 8.0 us, with two 9.0)
 constexpr float kShift = 7.f;  // the largest weight is 2^kShift: 11 bits down to 2^-21 of it
 
 template <int D>
@@ -79,16 +79,19 @@ struct Rows {
       }
     }
   }
-  // Row g of 8 rows; null: zeros. BF16 rows become FP16 under a power of two that brings their
-  // largest magnitude to [2^14, 2^15).
+  // Row g of 8 rows; null: zeros.
   template <typename T>
-  __device__ __forceinline__ void load(int n, const T* row, float scale, int lane) {
+  __device__ __forceinline__ void fetch(int n, const T* row, int lane) {
 #pragma unroll
     for (int i = 0; i < D / 16; i++) {
       const uint2 x = row ? *reinterpret_cast<const uint2*>(row + 16 * i + 4 * (lane & 3)) : make_uint2(0, 0);
       q[n][i][0] = x.x;
       q[n][i][1] = x.y;
     }
+  }
+  // BF16 rows become FP16 under a power of two that brings their largest magnitude to [2^14, 2^15).
+  template <typename T>
+  __device__ __forceinline__ void finish(int n, float scale, int lane) {
     by[n][0] = by[n][1] = scale;
     if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) {
       uint32_t top = 0;
@@ -126,41 +129,46 @@ struct Ring {
   long long x, end;
   int s, s1, head;  // the next one to ask for
   const int* table;
-  int page[NB];     // its pages
+  int base, page, next;  // pages of the blocks base + lane, and of 32 further on
 
-  __device__ __forceinline__ void look(const DecodeAttnArgs& a) {
-#pragma unroll
-    for (int b = 0; b < NB; b++) {
-      const int p = (s * Slice<D>::kKeys + 16 * b) >> a.page_shift;
-      page[b] = p < a.width ? __ldg(table + p) : -1;
-    }
+  __device__ __forceinline__ int page_of(const DecodeAttnArgs& a, int block) const {
+    const int p = (block * 16) >> a.page_shift;
+    return p < a.width ? __ldg(table + p) : -1;
   }
-  __device__ __forceinline__ void begin(const DecodeAttnArgs& a, const Walk& w, const int* starts) {
-    if (x >= end) return;
-    const Segment g = segment_at<Slice<D>::kKeys, Rows>(a, w, starts, x, end);
+  __device__ __forceinline__ void begin(const DecodeAttnArgs& a, const Segment& g, int lane) {
     s = g.s0;
     s1 = g.s1;
     head = g.head;
     table = g.table;
-    look(a);
+    base = s * NB;
+    page = page_of(a, base + lane);
+    next = page_of(a, base + 32 + lane);
   }
   // The next slice into its stage, whose last reads are behind the warp.
   __device__ __forceinline__ void ask(const DecodeAttnArgs& a, const Walk& w, const int* starts, int lane) {
     if (x >= end) return;
     const int st = asked % kStages;
+    if (s * NB - base >= 32) {
+      base += 32;
+      page = next;
+      next = page_of(a, base + 32 + lane);
+    }
+    int pages[NB];
+#pragma unroll
+    for (int b = 0; b < NB; b++) pages[b] = __shfl_sync(~0u, page, s * NB - base + b);
     if (lane == 0) {
       uint8_t* dst = buf + st * Slice<D>::kStage;
       uint64_t* bar = full + st;
       float* sc = scales + st * 2 * NB;
 #pragma unroll
       for (int b = 0; b < NB; b++)
-        if ((unsigned)page[b] >= (unsigned)a.pages) sc[b] = sc[NB + b] = 1.f;
+        if ((unsigned)pages[b] >= (unsigned)a.pages) sc[b] = sc[NB + b] = 1.f;
       mbar_expect_tx(bar, Slice<D>::kStage);
 #pragma unroll
       for (int b = 0; b < NB; b++) {
         const int at = (s * Slice<D>::kKeys + 16 * b) & (a.page_size - 1);
-        const bool in = (unsigned)page[b] < (unsigned)a.pages;
-        const int p = in ? page[b] : -1;  // -1 is out of the map's range: zeros
+        const bool in = (unsigned)pages[b] < (unsigned)a.pages;
+        const int p = in ? pages[b] : -1;  // -1 is out of the map's range: zeros
         tma_load_5d(dst + b * Slice<D>::kBlock, &a.k, 0, at, 0, head, p, bar);
         tma_load_5d(dst + Slice<D>::kHalf + b * Slice<D>::kBlock, &a.v, 0, at, 0, head, p, bar);
         if (in) {
@@ -173,10 +181,7 @@ struct Ring {
     }
     asked++;
     x++;
-    if (++s < s1)
-      look(a);
-    else
-      begin(a, w, starts);
+    if (++s == s1 && x < end) begin(a, segment_at<Slice<D>::kKeys, Rows>(a, w, starts, x, end), lane);
   }
   static __device__ __forceinline__ void copy4(float* dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_addr(dst)), "l"(src) : "memory");
@@ -361,34 +366,43 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const __grid_con
   rg.end = min(rg.x + per, w.total);
   long long x = rg.x;
   const long long end = rg.end;
-  rg.begin(a, w, starts);
-  for (int i = 0; i < kStages; i++) rg.ask(a, w, starts, lane);
-  note_runs(a, w, starts, per);
-  griddep_launch();
   const T* q = reinterpret_cast<const T*>(a.q);
   Rows<NT, D> R;
-  bool ok = true;
-  while (ok && x < end) {
-    const Segment g = segment_at<KS, 8 * NT>(a, w, starts, x, end);
-    const int len = seq_len(a, g.seq);
+  Segment g;
+  auto begin = [&]() {  // the segment at x: its rows of q are asked for
+    g = segment_at<KS, 8 * NT>(a, w, starts, x, end);
 #pragma unroll
     for (int n = 0; n < NT; n++) {
       const int r = 8 * n + (lane >> 2), head = g.head * a.group + g.row0 + r;
-      R.load(n, r < g.rows ? q + (long long)g.seq * a.ldq + (long long)head * D : nullptr, a.scale_log2, lane);
+      R.fetch(n, r < g.rows ? q + (long long)g.seq * a.ldq + (long long)head * D : nullptr, lane);
     }
+  };
+  if (x < end) {
+    begin();
+    rg.begin(a, g, lane);
+  }
+  for (int i = 0; i < kStages; i++) rg.ask(a, w, starts, lane);
+  note_runs(a, w, starts, per);
+  griddep_launch();
+  bool ok = true;
+  while (ok && x < end) {
+#pragma unroll
+    for (int n = 0; n < NT; n++) R.template finish<T>(n, a.scale_log2, lane);
     R.reset();
-    ok = attend<Store>(R, rg, a, w, starts, g.s0, g.s1, a.shared, len, lane);
+    ok = attend<Store>(R, rg, a, w, starts, g.s0, g.s1, a.shared, seq_len(a, g.seq), lane);
     if (!ok) break;
     const long long slot = me + g.group;
     float* po = a.own_o + slot * a.own_rows * D;
     float2* pml = a.own_ml + slot * a.own_rows;
+    const int rows = g.rows;
     x += g.s1 - g.s0;
+    if (x < end) begin();  // the next segment's q is on its way while this one's result is stored
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
       for (int c = 0; c < 2; c++) {
         const int r = 8 * n + 2 * (lane & 3) + c;
-        if (r >= g.rows) continue;
+        if (r >= rows) continue;
         if (lane < 4) pml[r] = make_float2(R.m[n][c], R.l[n][c]);
         // o relative to m, in two steps that stay in FP32's range
         const float by = R.m[n][c] == -INFINITY ? 0.f : exp2_fast(R.M[n][c] - R.m[n][c]);
