@@ -16,7 +16,10 @@ namespace tfx {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCtas = 4;  // of an SM: five and six keep fewer words in registers and are slower (16,384 rows: 76.8, 78.3, 79.3 us)
 constexpr int kMostRotary = 2048;
+constexpr uint32_t kSide = 1u << 31;
+constexpr int kCopies = 3;  // words that a thread copies at a time
 
 struct RopeArgs {
   const uint64_t* table;
@@ -30,38 +33,60 @@ struct RopeArgs {
   int copy;          // whether the values behind the rotated ones are written
 };
 
-// One CTA per row. Items of a head: rotary/16 pairs of 16-byte words (half) or rotary/8
-// words (interleaved), then the words that are only copied. A thread asks for its first items
-// before it works out the row's sines.
+// One CTA per row. Items of a head: rotary/16 pairs of 16-byte words (half) or rotary/8 words
+// (interleaved). A thread asks for its first items, and copies what is only copied, before it
+// works out its share of the row's sines.
 template <typename T, bool Interleaved>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kAhead = Interleaved ? 4 : 2;
   __shared__ __align__(16) float cosine[kMostRotary / 2], sine[kMostRotary / 2];
   griddep_wait();
   griddep_launch();
   const int t = blockIdx.x, half = a.rotary / 2;
   const int turned = Interleaved ? a.rotary / 8 : a.rotary / 16;
-  const int per = turned + (a.copy ? (a.dim - a.rotary) / 8 : 0);
-  const int all = (a.heads[0] + a.heads[1]) * per;
+  const int all = (a.heads[0] + a.heads[1]) * turned;
+  const T* in[2];
+  T* out[2];
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    in[i] = reinterpret_cast<const T*>(a.in[i]) + t * a.ld_in[i];
+    out[i] = reinterpret_cast<T*>(a.out[i]) + t * a.ld_out[i];
+  }
   uint4 x[kAhead], y[Interleaved ? 1 : kAhead];
-  T* out[kAhead];
-  int word[kAhead];  // a copied one's: -1
+  uint32_t place[kAhead];  // the first value's number in the row, and whether it is k's
+  // Item or word `it` of `per` a head: its place where a head's first is at `at0`.
+  auto place_of = [&](int it, int per, int at0) {
+    const int h = it / per, side = h >= a.heads[0];
+    return (uint32_t)((side ? h - a.heads[0] : h) * a.dim + at0 + (it - h * per) * 8) | (side ? kSide : 0u);
+  };
   auto ask = [&](int it0) {
 #pragma unroll
     for (int n = 0; n < kAhead; n++) {
       const int it = it0 + n * kThreads;
-      out[n] = nullptr;
-      if (it >= all) continue;
-      const int h = it / per, j = it - h * per, side = h >= a.heads[0];
-      const int at = (side ? h - a.heads[0] : h) * a.dim + (j < turned ? j * 8 : a.rotary + (j - turned) * 8);
-      const T* in = reinterpret_cast<const T*>(a.in[side]) + t * a.ld_in[side] + at;
-      out[n] = reinterpret_cast<T*>(a.out[side]) + t * a.ld_out[side] + at;
-      word[n] = j < turned ? j : -1;
-      x[n] = *reinterpret_cast<const uint4*>(in);
-      if (!Interleaved && j < turned) y[Interleaved ? 0 : n] = *reinterpret_cast<const uint4*>(in + half);
+      if (it >= all) break;
+      place[n] = place_of(it, turned, 0);
+      const T* from = (place[n] & kSide ? in[1] : in[0]) + (place[n] & ~kSide);
+      x[n] = *reinterpret_cast<const uint4*>(from);
+      if (!Interleaved) y[Interleaved ? 0 : n] = *reinterpret_cast<const uint4*>(from + half);
     }
   };
   ask(threadIdx.x);
+  if (a.copy) {
+    const int rest = (a.dim - a.rotary) / 8, words = (a.heads[0] + a.heads[1]) * rest;
+    for (int c0 = threadIdx.x; c0 < words; c0 += kThreads * kCopies) {
+      uint4 w[kCopies];
+      uint32_t at[kCopies];
+#pragma unroll
+      for (int n = 0; n < kCopies; n++)
+        if (c0 + n * kThreads < words) {
+          at[n] = place_of(c0 + n * kThreads, rest, a.rotary);
+          w[n] = *reinterpret_cast<const uint4*>((at[n] & kSide ? in[1] : in[0]) + (at[n] & ~kSide));
+        }
+#pragma unroll
+      for (int n = 0; n < kCopies; n++)
+        if (c0 + n * kThreads < words) *reinterpret_cast<uint4*>((at[n] & kSide ? out[1] : out[0]) + (at[n] & ~kSide)) = w[n];
+    }
+  }
   const long long position = a.positions[t];
   for (int i = threadIdx.x; i < half; i += kThreads) {
     const uint64_t turn = (uint64_t)position * a.table[i];
@@ -75,32 +100,32 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     if (it0 != threadIdx.x) ask(it0);
 #pragma unroll
     for (int n = 0; n < kAhead; n++) {
-      if (!out[n]) continue;
+      if (it0 + n * kThreads >= all) break;
+      const int at = (int)(place[n] & ~kSide), word = at % a.dim / 8;
+      T* to = (place[n] & kSide ? out[1] : out[0]) + at;
       uint32_t v[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-      if (word[n] >= 0) {
-        if constexpr (Interleaved) {
-          const float4 c = *reinterpret_cast<const float4*>(cosine + word[n] * 4);
-          const float4 s = *reinterpret_cast<const float4*>(sine + word[n] * 4);
-          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+      if constexpr (Interleaved) {
+        const float4 c = *reinterpret_cast<const float4*>(cosine + word * 4);
+        const float4 s = *reinterpret_cast<const float4*>(sine + word * 4);
+        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-          for (int k = 0; k < 4; k++) {
-            const float2 f = pair_to_float(v[k], T());
-            v[k] = pack2<T>(f.x * cs[k] - f.y * sn[k], f.y * cs[k] + f.x * sn[k]);
-          }
-        } else {
-          uint32_t u[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
-#pragma unroll
-          for (int k = 0; k < 4; k++) {
-            const float2 f = pair_to_float(v[k], T()), g = pair_to_float(u[k], T());
-            const float2 c = *reinterpret_cast<const float2*>(cosine + word[n] * 8 + 2 * k);
-            const float2 s = *reinterpret_cast<const float2*>(sine + word[n] * 8 + 2 * k);
-            v[k] = pack2<T>(f.x * c.x - g.x * s.x, f.y * c.y - g.y * s.y);
-            u[k] = pack2<T>(g.x * c.x + f.x * s.x, g.y * c.y + f.y * s.y);
-          }
-          *reinterpret_cast<uint4*>(out[n] + half) = make_uint4(u[0], u[1], u[2], u[3]);
+        for (int k = 0; k < 4; k++) {
+          const float2 f = pair_to_float(v[k], T());
+          v[k] = pack2<T>(f.x * cs[k] - f.y * sn[k], f.y * cs[k] + f.x * sn[k]);
         }
+      } else {
+        uint32_t u[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const float2 f = pair_to_float(v[k], T()), g = pair_to_float(u[k], T());
+          const float2 c = *reinterpret_cast<const float2*>(cosine + word * 8 + 2 * k);
+          const float2 s = *reinterpret_cast<const float2*>(sine + word * 8 + 2 * k);
+          v[k] = pack2<T>(f.x * c.x - g.x * s.x, f.y * c.y - g.y * s.y);
+          u[k] = pack2<T>(g.x * c.x + f.x * s.x, g.y * c.y + f.y * s.y);
+        }
+        *reinterpret_cast<uint4*>(to + half) = make_uint4(u[0], u[1], u[2], u[3]);
       }
-      *reinterpret_cast<uint4*>(out[n]) = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
 }
@@ -152,7 +177,7 @@ int tfx_rope_apply(const tfx_rope* r, int act, int dim, const void* q, int64_t l
   if (r->rotary < 16 || r->rotary % 16 || r->rotary > dim || r->rotary > tfx::kMostRotary)
     return fail_with(TFX_EUNSUPPORTED, "rotary=%d of dim=%d: a multiple of 16, at most %d", r->rotary, dim, tfx::kMostRotary);
   if (!std::isfinite(r->gain)) return fail_with(TFX_EINVAL, "gain=%g", (double)r->gain);
-  if (heads_q < 1 || heads_k < 0 || heads_q > 65535 || heads_k > 65535 || ((int64_t)heads_q + heads_k) * dim > INT32_MAX)
+  if (heads_q < 1 || heads_k < 0 || heads_q > 65535 || heads_k > 65535 || ((int64_t)heads_q + heads_k) * dim > (1 << 30))
     return fail_with(TFX_EINVAL, "heads_q=%d, heads_k=%d of %d values", heads_q, heads_k, dim);
   if (rows < 0) return fail_with(TFX_EINVAL, "rows=%d", rows);
   if (!rows) return 0;
