@@ -100,11 +100,10 @@ __device__ __forceinline__ int growth(const BookArgs& a, int i, int* slot, int* 
 }
 
 __global__ void __launch_bounds__(kBookThreads) extend_kernel(const __grid_constant__ BookArgs a) {
-  __shared__ int status, asked;
-  __shared__ int3 given[kBookThreads];  // of an entry: its first page in the free list, how many, and its slot
-  __shared__ int from[kBookThreads];    // column of its table
+  __shared__ int status, asked, large;
+  __shared__ int4 given[kBookThreads];  // of an entry: its first page in the free list, how many, its slot, its table's column
   griddep_wait();
-  if (threadIdx.x == 0) status = asked = 0;
+  if (threadIdx.x == 0) status = asked = large = 0;
   __syncthreads();
   // pages that the list asks for
   int mine = 0;
@@ -124,10 +123,19 @@ __global__ void __launch_bounds__(kBookThreads) extend_kernel(const __grid_const
     int all;
     const int first = carry + block_scan(cnt, &all);
     if (cnt && first + cnt > have) bad = TFX_CACHE_FULL;
-    given[threadIdx.x] = make_int3(first, i < a.n && !bad ? cnt : 0, s);
     if (i < a.n) {
       if (!bad) {
-        from[threadIdx.x] = pages_for(a, old);
+        const int column = pages_for(a, old);
+        if (cnt > 4) {
+          given[atomicAdd(&large, 1)] = make_int4(first, cnt, s, column);
+        } else {
+          int* row = a.tables + (long long)s * a.width + column;
+          for (int c = 0; c < cnt; c++) {
+            const int p = a.free_list[first + c];
+            row[c] = p;
+            a.refs[p] = 1;
+          }
+        }
         a.lens[s] = old + add;
       }
       // for the appends; a slot that asks for nothing keeps what it has
@@ -138,17 +146,21 @@ __global__ void __launch_bounds__(kBookThreads) extend_kernel(const __grid_const
     if (bad) atomicOr(&status, bad);
     carry += all;
     __syncthreads();
-    // a warp an entry: a prompt's pages are many (250 of three prompts: 8.1 -> 4.7 us)
-    for (int e = threadIdx.x >> 5; e < min(a.n - i0, kBookThreads); e += kBookThreads / 32) {
-      const int3 g = given[e];
-      int* row = a.tables + (long long)g.z * a.width + (g.y ? from[e] : 0);
+    // many pages are an entry's by a warp (250 of three prompts: 8.1 -> 4.7 us)
+    for (int e = threadIdx.x >> 5; e < large; e += kBookThreads / 32) {
+      const int4 g = given[e];
+      int* row = a.tables + (long long)g.z * a.width + g.w;
       for (int c = threadIdx.x & 31; c < g.y; c += 32) {
         const int p = a.free_list[g.x + c];
         row[c] = p;
         a.refs[p] = 1;
       }
     }
-    __syncthreads();
+    if (i0 + kBookThreads < a.n) {
+      __syncthreads();
+      if (threadIdx.x == 0) large = 0;
+      __syncthreads();
+    }
   }
   if (threadIdx.x == 0) {
     *a.grown.n = a.n;
