@@ -499,6 +499,7 @@ int tfx_cache_read(tfx_cache* c, int layer, const int32_t* seqs, const int32_t* 
   if (!n || !rows) return 0;
   if ((rc = check_rows("k", k, ldk, (int64_t)c->heads_kv * c->dim))) return rc;
   if ((rc = check_rows("v", v, ldv, (int64_t)c->heads_kv * c->dim))) return rc;
+  if (k == v) return fail_with(TFX_EINVAL, "k and v are one tensor");
   tfx::ReadArgs a = {};
   a.k = layer_of<const void>(c, c->k, layer);
   a.v = layer_of<const void>(c, c->v, layer);

@@ -184,6 +184,9 @@ int tfx_rope_apply(const tfx_rope* r, int act, int dim, const void* q, int64_t l
   int rc = check_side("q", q, ldq, q_out, ldqo, (int64_t)heads_q * dim);
   if (rc) return rc;
   if (heads_k && (rc = check_side("k", k, ldk, k_out, ldko, (int64_t)heads_k * dim))) return rc;
+  // a row's items are written while others are still read
+  if (heads_k && (q_out == k || k_out == q || k_out == q_out))
+    return fail_with(TFX_EINVAL, "an output is the other one, or the other's input");
   if (!positions) return fail_with(TFX_EINVAL, "null positions");
   if (reinterpret_cast<uintptr_t>(positions) & 3u || reinterpret_cast<uintptr_t>(r->table) & 7u)
     return fail_with(TFX_EALIGN, "positions or table is not aligned");

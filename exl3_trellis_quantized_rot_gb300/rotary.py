@@ -100,7 +100,7 @@ class Rope:
 def rope(r: Rope, q, k, positions, out=None, inverse: bool = False, stream=None):
     """q (rows, heads, dim) and k (rows, kv_heads, dim; or None) with row t rotated to
     positions[t] (tfx_rope_apply; an int32 vector on the device). out: the tensors to write
-    to, (q, k) themselves for a rotation in place; made here by default. inverse: by the
+    to, (q, k) themselves for a rotation in place, else none that overlaps an input; made here by default. inverse: by the
     negative angles. Returns (q, k)."""
     torch = _at.torch
     shape, dev, dtype, dim = q.shape, q.get_device(), q.dtype, r.dim

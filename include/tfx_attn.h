@@ -142,7 +142,7 @@ int tfx_cache_append_listed(tfx_cache* c, int layer, const void* k, int64_t ldk,
  * of the 8-bit stores are rounded to act once (I8: exact but for FP16's range).
  * Rows outside the lists, and rows of the list past `rows`, are not touched; a row
  * whose sequence does not hold its token gets zeros and leaves TFX_CACHE_BAD.
- * ldk, ldv as in tfx_cache_append. k and v must not overlap the cache. */
+ * ldk, ldv as in tfx_cache_append. k and v must overlap neither one another nor the cache. */
 int tfx_cache_read(tfx_cache* c, int layer, const int32_t* seqs, const int32_t* starts, const int32_t* offsets, int n,
                    int rows, void* k, int64_t ldk, void* v, int64_t ldv, cudaStream_t stream);
 

@@ -37,7 +37,8 @@ int tfx_rope_table(const double* freqs, int n, uint64_t* table);
 /* Rows of q (heads_q heads of dim values next to each other, ldq elements apart)
  * and of k (heads_k; 0 where there is none) to q_out and k_out: row t is at position
  * positions[t] (device; any int32). Values behind the first `rotary` of a head are
- * copied. An output may be its input, with the same pitch, or must not overlap it.
+ * copied. An output may be its own input, with the same pitch; else it overlaps no
+ * other tensor of the call.
  * dim, pitches: multiples of 8, pointers 16-byte aligned (TFX_EALIGN otherwise);
  * act: tfx_dtype. FP32 inside, rounded once.
  * inverse: rotates by -w instead, with the same gain: the transpose, which the

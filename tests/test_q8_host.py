@@ -84,7 +84,7 @@ def test_read_refusals(L, drv, store):
     assert read(layer=-1) == tfx.EINVAL and read(layer=2) == tfx.EINVAL and read(n=-1) == tfx.EINVAL and read(rows=-1) == tfx.EINVAL
     assert read(seqs=None) == tfx.EINVAL and read(starts=None) == tfx.EINVAL and read(off=None) == tfx.EINVAL
     assert read(k=None) == tfx.EINVAL and read(v=None) == tfx.EINVAL and read(ldk=1016) == tfx.EINVAL
-    assert read(k=P + 8) == tfx.EALIGN and read(ldv=1028) == tfx.EALIGN
+    assert read(k=P + 8) == tfx.EALIGN and read(ldv=1028) == tfx.EALIGN and read(k=P, v=P) == tfx.EINVAL
     n = tfx.launch_count()
     assert read(n=0, seqs=None, starts=None, off=None) == 0 and read(rows=0, k=None, v=None) == 0
     assert tfx.launch_count() == n
@@ -123,6 +123,14 @@ def test_rope_refusals(L, kw, code):
     n = tfx.launch_count()
     assert L.tfx_rope_apply(C.byref(r), *rope_args(**kw)) == code
     assert tfx.last_error() and tfx.launch_count() == n
+
+
+@pytest.mark.parametrize("kw", [dict(q_out=P + (1 << 31)), dict(k_out=P), dict(k_out=P + (1 << 30))])
+def test_rope_outputs_that_are_other_tensors(L, kw):
+    r = rotary.RopeStruct(P, 64, 0, 1.0)
+    n = tfx.launch_count()
+    assert L.tfx_rope_apply(C.byref(r), *rope_args(**kw)) == tfx.EINVAL
+    assert "output" in tfx.last_error() and tfx.launch_count() == n
 
 
 @pytest.mark.parametrize("table,rotary_dim,gain,code", [
