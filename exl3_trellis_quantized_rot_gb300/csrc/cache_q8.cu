@@ -4,6 +4,12 @@
 // touches a block's bytes once: a warp takes the block's new values, their largest
 // magnitude, and with it the scale; codes that the block holds already are rounded again
 // only where the scale grows.
+//
+// Bound: memory at large sizes: three prompts of 32,001 tokens (8 heads of 128) are appended in 36 us (131 MB
+// read, 66 written; DRAM busy half the time, issue slots 41 %), 43,695 tokens (4 heads of 256) read back
+// in 47.5 to 49.5 us (268 MB, 5.6 TB/s). 64 single tokens: 3.4 us, 300 rows read: 3.2 us, the latency
+// of lists, table, scale and codes one after another. Two CTAs an SM hold a block in registers (128 a
+// thread); copies into shared memory for eight warps an SM took 60 us where this took 46.
 #include <cuda_runtime.h>
 
 #include <type_traits>

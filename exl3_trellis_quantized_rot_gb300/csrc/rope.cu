@@ -4,6 +4,10 @@
 // An angle is held as a fraction of a turn in 64 bits: f_i / 2 pi as F_i / 2^64, so
 // n F_i mod 2^64 is the angle without its whole turns, exactly but for F_i's own rounding.
 // Its top 32 bits, as a signed number of half turns, go to sincospi.
+//
+// Bound: memory at large sizes: 16,384 rows of 24 + 4 heads of 256 (470 MB) take 76.7 us, 6.1 TB/s, 4,097 rows of
+// 48 + 8 of 128 (118 MB, partly in L2) 22.3. 64 rows: 2.4 us, position, frequency and sine one after
+// another. A row a CTA: CTAs that go from row to row took 29 us where this took 22.7.
 #include <cuda_runtime.h>
 
 #include <cmath>
