@@ -280,9 +280,9 @@ int64_t prefix_rows(int64_t batch, int64_t heads_q, int64_t heads_kv) {
 // Over 8-bit codes, the tokens of a prefix that the tensor cores read once; 0: each sequence
 // reads it as its own. That takes the warps as long as reading the prefix `batch` times, from L2
 // where it fits; the other kernel begins with 8 us. Measured, the tensor cores / as their own (us;
-// 100 own tokens): 24/4 heads of 256, 8,192 tokens and 2 sequences 16.6 / 16.4, 4: 21.7 / 19.2, 6: 22.6 /
-// 23.1, 16: 27.0 / 44.0; of 2,048 and 6: 19.5 / 13.5, 16: 22.8 / 19.0; of 32,768 and 2: 34.5 / 31.2, 3: 35.3 /
-// 38.5; 8/8 heads of 128, 8,192 and 4: 22.6 / 19.0, 8: 23.9 / 29.5; of 32,768 and 4: 43.5 / 52.3.
+// 100 own tokens): 24/4 heads of 256, 8,192 tokens and 2 sequences 18.1 / 15.3, 4: 18.7 / 17.7, 6: 19.2 /
+// 21.2, 16: 23.8 / 41.0; of 2,048 and 6: 16.0 / 11.9, 16: 19.8 / 17.2; of 32,768 and 2: 31.9 / 28.8, 3: 32.0 /
+// 35.2; 8/8 heads of 128, 8,192 and 4: 18.5 / 16.8, 8: 20.0 / 26.3; of 32,768 and 4: 39.5 / 44.9.
 int coded_prefix(const tfx_cache* c, int batch, int shared) {
   shared = shared / TFX_CACHE_BLOCK * TFX_CACHE_BLOCK;
   return batch > 2 && (int64_t)batch * shared * c->heads_kv * c->dim * 2 > (64LL << 20) ? shared : 0;

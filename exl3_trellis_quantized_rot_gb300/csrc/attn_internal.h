@@ -10,7 +10,7 @@
 
 namespace tfx {
 
-constexpr int kCodedWarps = 8;     // of a CTA of the decode kernel over 8-bit codes
+constexpr int kCodedWarps = 7;     // of a CTA of the decode kernel over 8-bit codes (attn_q8.cu says why)
 constexpr int kAttnMaxSeqs = 512;  // sequences of one prompt launch (longer lists take several launches)
 
 // Work of one prompt launch, in the kernel's parameters: nothing is copied to

@@ -18,17 +18,19 @@
 // which the conversion to FP16 takes apart: even dims are rows 0-7 of V^T, odd ones 8-15.
 //
 // A warp owns its rows, its slices (8 KB of K and V of one K/V head: 16 keys of 256, 32 of
-// 128) and a ring of three of them, which it fills itself, a slice as soon as one is done.
+// 128) and a ring of two of them, which it fills itself, a slice as soon as one is done.
 // Every warp gets the same number of slices, as in attn_warp.cu; decode_join_kernel joins. A
 // long prefix that many sequences share is attn_q8_tc.cu's; here keys begin behind it.
 //
 // Bound: the codes' bytes. 64 sequences of up to 8,192 tokens (553 MB of codes and scales, 24/4 heads of 256)
-// take 103 us with the join, 262,144 tokens of one (538 MB, 48/8 of 128) 103: 5.3 TB/s. About 18 us do
-// not grow with the tokens (the first loads 4, the join 5 to 10, warps that end apart); what 8,192
-// more tokens add comes at 6.7 TB/s. One sequence of 1,000 tokens: 8 us, the latency of two launches
-// and of their loads. At half that size the counters show DRAM busy 65 % of the time, issue slots 36 %,
-// MMAs 16 %. Eight warps of three stages: twelve of two had as much in flight and were no faster (103) or
-// slower (112, dim 128).
+// take 95 us with the join, 262,144 tokens of one (538 MB, 48/8 of 128) 99: 5.8 and 5.4 TB/s. About 15 us do
+// not grow with the tokens (the first loads, the join, SMs that end apart: those of the fullest
+// parts of the chip are 10 us behind the others). One sequence of 1,000 tokens: 8 us, the latency of two
+// launches and of their loads.
+// The fewer bytes are asked for at a time, the faster the memory gives them, down to what its latency
+// takes: 7 warps of 2 slices (112 KB an SM) 95 and 99 us, 8 of 2 96 and 99 to 103, 8 of 3 101 and 108, 6 of 2
+// 98 and 105, 10 of 2 100 and 110; slices of 4 KB at dim 128 (8 warps of 2, 3 and 4, 12 of 2) 104, 103, 104,
+// 100. A barrier a slice, so that a CTA's heads are read together, was no faster.
 #include <cuda_fp16.h>
 
 #include "attn_split.cuh"
@@ -38,9 +40,11 @@ namespace tfx {
 namespace {
 
 constexpr int kThreads = kCodedWarps * 32;
-constexpr int kStages = 3;     // of a warp's ring
+constexpr int kStages = 2;     // of a warp's ring: see above
 constexpr int kFewest = 1;     // slices a warp takes at least (one sequence of 1,000 tokens: 8.0 us, with two 9.0)
-constexpr float kShift = 7.f;  // the largest weight is 2^kShift: 11 bits down to 2^-21 of it
+// A weight at its reference is 2^kShift, so the largest is between that and 2^15: 11 bits down to
+// 2^-21 of it, or further.
+constexpr float kShift = 7.f, kSlack = 8.f;
 
 template <int D>
 struct Slice {
@@ -161,31 +165,23 @@ struct Ring {
       page = next;
       next = page_of(a, base + 32 + lane);
     }
-    int pages[NB];
-#pragma unroll
-    for (int b = 0; b < NB; b++) pages[b] = __shfl_sync(~0u, page, s * NB - base + b);
-    if (lane == 0) {
-      uint8_t* dst = buf + st * Slice<D>::kStage;
-      uint64_t* bar = full + st;
-      float* sc = scales + st * 2 * NB;
-#pragma unroll
-      for (int b = 0; b < NB; b++)
-        if ((unsigned)pages[b] >= (unsigned)a.pages) sc[b] = sc[NB + b] = 1.f;
-      mbar_expect_tx(bar, Slice<D>::kStage);
-#pragma unroll
-      for (int b = 0; b < NB; b++) {
-        const int at = (s * Slice<D>::kKeys + 16 * b) & (a.page_size - 1);
-        const bool in = (unsigned)pages[b] < (unsigned)a.pages;
-        const int p = in ? pages[b] : -1;  // -1 is out of the map's range: zeros
-        tma_load_5d(dst + b * Slice<D>::kBlock, &a.k, 0, at, 0, head, p, bar);
-        tma_load_5d(dst + Slice<D>::kHalf + b * Slice<D>::kBlock, &a.v, 0, at, 0, head, p, bar);
-        if (in) {
-          const long long i = ((long long)p * (a.page_size / 16) + at / 16) * a.heads_kv + head;
-          copy4(sc + b, a.k_scale + i);
-          copy4(sc + NB + b, a.v_scale + i);
-        }
+    // a lane a block of K or of V: its copy and its scale
+    const int b = lane % NB, got = __shfl_sync(~0u, page, s * NB - base + b);
+    uint64_t* bar = full + st;
+    if (lane == 0) mbar_expect_tx(bar, Slice<D>::kStage);
+    __syncwarp();
+    if (lane < 2 * NB) {
+      const bool value = lane >= NB, in = (unsigned)got < (unsigned)a.pages;
+      const int at = (s * Slice<D>::kKeys + 16 * b) & (a.page_size - 1), p = in ? got : -1;  // -1 is out of the map's range: zeros
+      tma_load_5d(buf + st * Slice<D>::kStage + lane * Slice<D>::kBlock, value ? &a.v : &a.k, 0, at, 0, head, p, bar);
+      float* to = scales + st * 2 * NB + lane;
+      if (in) {
+        copy4(to, (value ? a.v_scale : a.k_scale) + ((long long)p * (a.page_size / 16) + at / 16) * a.heads_kv + head);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s_addr(bar)) : "memory");
+      } else {
+        *to = 1.f;
+        mbar_arrive(bar);
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s_addr(bar)) : "memory");
     }
     asked++;
     x++;
@@ -263,56 +259,69 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const De
           }
       }
     }
+    // The references follow the maxima where one is passed by more than 2^kSlack, which few slices
+    // do: the exchange between lanes that the maxima take is left out of the others.
+    float off[NB][NT][2];
+    bool over = edge;
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      const float lv = log2_scale(sc[NB + b]);
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          const float mx = fmaxf(sx[b][n][c], sx[b][n][c + 2]);
+          over = over || mx > R.m[n][c] + kSlack || mx + lv > R.M[n][c] + kSlack;
+          off[b][n][c] = lv + (kShift - (R.M[n][c] == -INFINITY ? 0.f : R.M[n][c]));
+        }
+    }
+    if (__any_sync(~0u, over)) {
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          float mn = R.m[n][c], Mn = R.M[n][c];
+#pragma unroll
+          for (int b = 0; b < NB; b++) {
+            float mx = fmaxf(sx[b][n][c], sx[b][n][c + 2]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+            mn = fmaxf(mn, mx);
+            // a block of which the row sees nothing may have any scale
+            off[b][n][c] = mx == -INFINITY ? 0.f : log2_scale(sc[NB + b]);
+            Mn = fmaxf(Mn, mx + off[b][n][c]);
+          }
+          const float Ref = Mn == -INFINITY ? 0.f : Mn, keep = exp2_fast(R.M[n][c] - Ref);
+          R.l[n][c] *= exp2_fast(R.m[n][c] - (mn == -INFINITY ? 0.f : mn));
+          R.m[n][c] = mn;
+          R.M[n][c] = Mn;
+#pragma unroll
+          for (int b = 0; b < NB; b++) off[b][n][c] += kShift - Ref;
+#pragma unroll
+          for (int i = 0; i < D / 16; i++) {
+            R.o[n][i][c] *= keep;
+            R.o[n][i][c + 2] *= keep;
+          }
+        }
+    }
     uint32_t p[NB][NT][2];  // W^T: m16n8k16 B fragments
-    float keep[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      float ref[2], off[NB][2];
+      float ref[2];
 #pragma unroll
-      for (int c = 0; c < 2; c++) {
-        float mn = R.m[n][c], Mn = R.M[n][c];
-#pragma unroll
-        for (int b = 0; b < NB; b++) {
-          float mx = fmaxf(sx[b][n][c], sx[b][n][c + 2]);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-          mn = fmaxf(mn, mx);
-          // a block of which the row sees nothing may have any scale
-          off[b][c] = mx == -INFINITY ? 0.f : log2_scale(sc[NB + b]);
-          Mn = fmaxf(Mn, mx + off[b][c]);
-        }
-        ref[c] = mn == -INFINITY ? 0.f : mn;
-        const float Ref = Mn == -INFINITY ? 0.f : Mn;
-        keep[n][c] = exp2_fast(R.M[n][c] - Ref);
-        R.l[n][c] *= exp2_fast(R.m[n][c] - ref[c]);
-        R.m[n][c] = mn;
-        R.M[n][c] = Mn;
-#pragma unroll
-        for (int b = 0; b < NB; b++) off[b][c] += kShift - Ref;
-      }
+      for (int c = 0; c < 2; c++) ref[c] = R.m[n][c] == -INFINITY ? 0.f : R.m[n][c];
 #pragma unroll
       for (int b = 0; b < NB; b++) {
         float e[4];
 #pragma unroll
         for (int c = 0; c < 4; c++) {
           R.l[n][c & 1] += exp2_fast(sx[b][n][c] - ref[c & 1]);
-          e[c] = exp2_fast(sx[b][n][c] + off[b][c & 1]);
+          e[c] = exp2_fast(sx[b][n][c] + off[b][n][c & 1]);
         }
         // the weights become matrix operands of FP16
         p[b][n][0] = transposed(pack2<__half>(e[0], e[1]));
         p[b][n][1] = transposed(pack2<__half>(e[2], e[3]));
       }
-    }
-    bool move = false;
-#pragma unroll
-    for (int n = 0; n < NT; n++) move = move || keep[n][0] != 1.f || keep[n][1] != 1.f;
-    if (__any_sync(~0u, move)) {
-#pragma unroll
-      for (int n = 0; n < NT; n++)
-#pragma unroll
-        for (int i = 0; i < D / 16; i++)
-#pragma unroll
-          for (int c = 0; c < 4; c++) R.o[n][i][c] *= keep[n][c & 1];
     }
 #pragma unroll
     for (int b = 0; b < NB; b++) {
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const __grid_con
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     // a slice's bytes, and its scales
-    for (int i = 0; i < kWarps * kStages; i++) mbar_init(&full[0][0] + i, 2);
+    for (int i = 0; i < kWarps * kStages; i++) mbar_init(&full[0][0] + i, 1 + 2 * NB);
     fence_mbar_init();
     tma_prefetch(&a.k);
     tma_prefetch(&a.v);
