@@ -7,7 +7,7 @@
 //
 // Bound: memory at large sizes: three prompts of 32,001 tokens (8 heads of 128) are appended in 36 us (131 MB
 // read, 66 written; DRAM busy half the time, issue slots 41 %), 43,695 tokens (4 heads of 256) read back
-// in 47.5 to 49.5 us (268 MB, 5.6 TB/s). 64 single tokens: 3.4 us, 300 rows read: 3.2 us, the latency
+// in 46 us (268 MB, 5.8 TB/s). 64 single tokens: 3.4 us, 300 rows read: 3.1 us, the latency
 // of lists, table, scale and codes one after another. Two CTAs an SM hold a block in registers (128 a
 // thread); copies into shared memory for eight warps an SM took 60 us where this took 46.
 #include <cuda_runtime.h>
@@ -188,7 +188,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
 }
 
 constexpr int read_ctas(int store) { return store == TFX_STORE_ACT ? 4 : 6; }  // of an SM
-constexpr int kAhead = 8;     // tokens that a lane of a read has asked for
+// Tokens that a lane of a read has asked for. 43,695 rows of 4 heads of 256 (us on the GPU): 8 tokens 47.6
+// (E4M3 49.1), 4 45.8 to 46.3, 2 47.6; 4 of eight CTAs an SM 50.4, 8 of five and four 51 and 61.
+constexpr int kAhead = 4;
 
 // The same for rows that are read, a.span tokens of a block at a time: they lie together and
 // have its scale.
@@ -297,8 +299,10 @@ int launch_read(ReadArgs& a, int act, int store, cudaStream_t s) {
   const int ctas = read_ctas(store) * multiprocessors();
   a.per = rows_per_window(a.rows, ctas, kMostRows / 2);
   // Tokens of a task: as few as keep the SMs' first warps busy. Measured with 2, 4, 8, 16 tokens, 4
-  // heads of 256 (us on the GPU): 300 rows 3.2, 3.3, 3.9, 4.1; 2,000 rows 6.4, 4.9, 5.6, 7.2; 4,096
-  // rows 9.0, 7.2, 6.8, 8.8; 16,000 rows 28.0, 23.0, 21.3, 21.3; 43,695 rows 61.4, 46.6, 48.3, 48.0.
+  // heads of 256 (us on the GPU, with 8 tokens asked for): 300 rows 3.2, 3.3, 3.9, 4.1; 2,000 rows 6.4,
+  // 4.9, 5.6, 7.2; 4,096 rows 9.0, 7.2, 6.8, 8.8; 16,000 rows 28.0, 23.0, 21.3, 21.3; 43,695 rows 61.4,
+  // 46.6, 48.3, 48.0. With 4, of 4, 8 and 16 tokens: 2,000 rows 5.2, 5.1, 5.2; 4,096 rows 7.0, 7.0, 9.3;
+  // 16,000 rows 22.7, 22.6, 22.5; 43,695 rows 48.8, 46.3, 46.2.
   const long long warps = (long long)multiprocessors() * kWarps, parts = 2 * (((long long)a.heads * a.dim + 255) / 256);
   a.span = a.rows * parts < 4 * warps ? 2 : a.rows * parts < 24 * warps ? 4 : 8;
   const void* fn;
