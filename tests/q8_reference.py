@@ -4,7 +4,8 @@ Bound of an attention output value over a cache of codes, from the number format
 u the unit roundoff of the rows' type (2^-11 FP16, 2^-8 BF16), A = sum_j p_j |v_j|, v_j
 the values that the codes of V stand for, and `most` = top * the largest scale of V:
 
-    u |out|                   the output's rounding
+    u |out|, 2^-25            the output's rounding: FP16's values below 2^-14 lie 2^-24 apart,
+                              so that one is off by up to 2^-25 there, however small it is
   + 2^-11 A                   the weights' (probability times scale) rounding to FP16 operands
   + n 2^-32 most              operands below FP16's normal range: half a step of 2^-24
                               where the largest is 2^7
@@ -87,7 +88,8 @@ def assert_near(got, out, A, qk, n, dim, most, largest=0.0):
     u = U[got.dtype]
     es = 2 * (dim * 2.0 ** -23 * qk + 2.0 ** -19)
     ea = 2 * (n / 8 + 64) * 2.0 ** -23
-    tol = u * out.abs() + (2.0 ** -11 + es + ea) * A + n * (2.0 ** -32 * most + 2.0 ** -126 * largest)
+    least = 2.0 ** -25 if got.dtype == torch.float16 else 0.0
+    tol = (u * out.abs()).clamp(min=least) + (2.0 ** -11 + es + ea) * A + n * (2.0 ** -32 * most + 2.0 ** -126 * largest)
     d = (got.double() - out).abs()
     assert torch.isfinite(got).all()
     assert bool((d <= tol).all()), f"error {float(d.max()):.3e}, {float((d / tol.clamp(min=1e-300)).max()):.2f} of its bound"

@@ -394,3 +394,33 @@ def test_prefix_of_values_with_very_different_scales(store):
             p = torch.softmax(q[i, h:h + 1].double() @ kk.T, 1)[0]
             most = TOP[store] * float((p.view(-1, 16).amax(1).cpu() * scales).max())
             assert_near(got[i:i + 1, h], o, A, qk, n, 128, most)
+
+
+@pytest.mark.parametrize("store", STORES)
+@pytest.mark.parametrize("dim,page", [(128, 32), (256, 16)])
+@pytest.mark.parametrize("rise,grow", [(7.9, 0), (8.2, 0), (0.6, 0), (-2.0, 8), (4.0, 4), (0.0, 7), (3.0, -11)])
+def test_scores_and_values_that_rise_from_block_to_block(store, dim, page, rise, grow):
+    """By less and by more than what moves the references: log2 of a weight by `rise`, of a value by `grow`."""
+    n = 16 * 12
+    c = make(store, F16, layers=1, page=page, heads=1, dim=dim, pages=n // page + 1, width=n // page)
+    m = Model(c, store)
+    k, v = normal((n, 1, dim), F16, 1, 0.05), normal((n, 1, dim), F16, 2, 2.0 ** -8 if grow > 0 else 1.0)
+    block = torch.arange(n, device="cuda") // 16
+    k[:, 0, 0] = (block - 6) * rise * float(np.log(2))
+    v = (v.float() * torch.exp2(block.float().clamp(max=2) * grow)[:, None, None]).to(F16)  # the factor alone passes FP16's range
+    q = normal((1, 3, dim), F16, 3, 0.1)
+    q[0, :, 0] = torch.tensor([1.0, -1.0, 0.5])
+    tfx.cache_extend(c, dev(0), dev(0, n))
+    tfx.cache_append(c, 0, k, v)
+    m.seqs[0] = [Coded(store, 1, dim) for _ in range(2)]
+    for x, y in zip(m.seqs[0], (k, v)):
+        x.append(y.double().cpu().numpy())
+    got = tfx.attn_decode(c, 0, q, dev(0), scale=1.0)
+    kk, vv = (torch.tensor(x.values()).cuda()[:, 0] for x in m.seqs[0])
+    for h in range(3):
+        o, A, qk = attend(q[0, h:h + 1], kk, vv, 1.0)
+        # what counts for FP16's steps: as above, the largest product of a weight and a scale
+        p = torch.softmax(q[0, h:h + 1].double() @ kk.T, 1)[0]
+        most = TOP[store] * float((p.view(-1, 16).amax(1).cpu() * torch.tensor(m.seqs[0][1].scales[:, 0])).max())
+        assert_near(got[:, h], o, A, qk, n, dim, most)
+    assert tfx.attn_error() == 0
