@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, read_ctas(Store)) read_kernel(const 
               float f[4], g[4];
               values4<Store>(x[j].x, f);
               values4<Store>(x[j].y, g);
-              __stcs(out + j * ld, make_uint4(pack2<T>(f[0] * scale, f[1] * scale), pack2<T>(f[2] * scale, f[3] * scale),
-                                              pack2<T>(g[0] * scale, g[1] * scale), pack2<T>(g[2] * scale, g[3] * scale)));
+              __stcs(out + j * ld, make_uint4(pack2_finite<T>(f[0] * scale, f[1] * scale), pack2_finite<T>(f[2] * scale, f[3] * scale),
+                                              pack2_finite<T>(g[0] * scale, g[1] * scale), pack2_finite<T>(g[2] * scale, g[3] * scale)));
             }
           }
       }

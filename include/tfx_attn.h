@@ -139,7 +139,8 @@ int tfx_cache_append_listed(tfx_cache* c, int layer, const void* k, int64_t ldk,
 /* Rows of a layer's K and V out of the cache, in act: row t of k and v, offsets[i] <=
  * t < offsets[i+1], is token starts[i] + t - offsets[i] of sequence seqs[i] (device
  * lists; n sequences, any of them several times; n+1 offsets, not decreasing). Values
- * of the 8-bit stores are rounded to act once (I8: exact but for FP16's range).
+ * of the 8-bit stores are rounded to act once (I8: exact but where FP16 is subnormal); one
+ * beyond act's range, which the nearest code of a value near its end can be, is its largest.
  * Rows outside the lists, and rows of the list past `rows`, are not touched; a row
  * whose sequence does not hold its token gets zeros and leaves TFX_CACHE_BAD.
  * ldk, ldv as in tfx_cache_append. k and v must overlap neither one another nor the cache. */
