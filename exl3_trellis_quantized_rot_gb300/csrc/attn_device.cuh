@@ -50,6 +50,18 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   return r;
 }
 
+// Two values as T, rounded; beyond its range its largest, a NaN stays. For what 8-bit codes stand for, which
+// can be beyond it where no appended value was: 65,504 of FP16 is code 64 under the I8 scale 2^10.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_finite(float lo, float hi) {
+  uint32_t r;
+  if constexpr (__is_same(T, __half))
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // The largest probability is 2^kShift: FP16 has no normal numbers below 2^-14,
 // and a shift of 7 keeps 11 bits down to 2^-21 of the row's largest term. BF16
 // has the range of FP32 and needs none.

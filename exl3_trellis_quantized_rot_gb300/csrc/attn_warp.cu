@@ -450,8 +450,10 @@ __global__ void __launch_bounds__(W * 32) decode_join_kernel(const __grid_consta
       x += so[k][c] * f[k];
       y += so[k][c + 1] * f[k];
     }
+    // a mean of values of 8-bit codes can be beyond FP16; of BF16's only where FP32 sums overflow, which shows as infinity
+    const uint32_t w = __is_same(T, __half) && a.k_scale ? pack2_finite<T>(x * inv, y * inv) : pack2<T>(x * inv, y * inv);
     // a sequence without tokens: zeros
-    *reinterpret_cast<uint32_t*>(out + c) = len == 0 ? 0u : pack2<T>(x * inv, y * inv);
+    *reinterpret_cast<uint32_t*>(out + c) = len == 0 ? 0u : w;
   }
 }
 

@@ -104,18 +104,6 @@ __device__ __forceinline__ void values4(uint32_t w, float (&x)[4]) {
   x[3] = g.y;
 }
 
-// Two values as T, rounded; beyond its range its largest, a NaN stays. A code times its scale can be
-// beyond it where no appended value was: 65,504 of FP16 is code 64 under the I8 scale 2^10.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2_finite(float lo, float hi) {
-  uint32_t r;
-  if constexpr (__is_same(T, __half))
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // BF16 values whose largest magnitude has the bits `top`: the power of two that brings it to
 // [2^14, 2^15), where FP16 holds them exactly but for those 2^28 times smaller; at most 2^126.
 __device__ __forceinline__ float brings_up(uint32_t top) { return __uint_as_float((268u - max(top >> 7, 15u)) << 23); }

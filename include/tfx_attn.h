@@ -181,7 +181,9 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * codes there (batch * shared tokens), the whole blocks of the first `shared` tokens are read through the
  * one table, the tokens behind the last whole block through each sequence's own; q
  * and the probabilities (times a block's scale) are matrix operands of FP16, q of
- * BF16 after a power of two that brings the row's largest magnitude below 2^15. */
+ * BF16 after a power of two that brings the row's largest magnitude below 2^15. A result
+ * beyond FP16's range is its largest there (values near it, see tfx_cache_read); sums of BF16
+ * values that pass FP32's range are infinite, over either store. */
 int tfx_attn_decode(tfx_cache* c, int layer, const tfx_attn_heads* h, const void* q, int64_t ldq, const int32_t* seqs,
                     int batch, int shared, void* out, int64_t ldo, cudaStream_t stream);
 

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import exl3_trellis_quantized_rot_gb300 as tfx
-from q8_reference import BLOCK, Coded
+from q8_reference import BLOCK, TOP, Coded, assert_near, attend
 
 pytestmark = pytest.mark.gpu
 F16, BF16, I8, E4M3 = torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn
@@ -72,3 +72,40 @@ def test_rows_near_the_end_of_their_type_are_read_back_finite(store, act, heads,
     assert bool(c.k_scale[0, c.tables[0, :2].long()].isfinite().all())
     back, _ = tfx.cache_read(c, 0, dev(0), dev(0), dev(0, n), n)
     assert torch.equal(back, rk) and c.status() == 0
+
+
+@pytest.mark.parametrize("store", [I8, E4M3])
+@pytest.mark.parametrize("hq,heads,dim", [(6, 2, 256), (4, 4, 128), (20, 1, 128)])
+def test_attention_over_values_near_the_end_of_fp16(store, hq, heads, dim):
+    """A mean of finite values is finite: beyond FP16's range it is its largest. The bound is that of an unlimited
+    result, since a limit brings no two numbers further apart."""
+    c = make(store, F16, heads, dim, hq)
+    lens = [1, 53, 40]
+    at = [0, 1, 54, 94]
+    k = near_the_end(94, heads, dim, F16, 1) * 2.0 ** -15
+    v = near_the_end(94, heads, dim, F16, 2)
+    v[54:] = torch.finfo(F16).max  # the third sequence: all of them the largest
+    v[54:, :, ::2] *= -1
+    tfx.cache_extend(c, dev(0, 1, 2), dev(*at))
+    tfx.cache_append(c, 0, k, v)
+    q = torch.randn((3, hq, dim), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(F16)
+    got = tfx.attn_decode(c, 0, q, dev(0, 1, 2))
+    beyond = False
+    for i, n in enumerate(lens):
+        kk, vv = (Coded(store, heads, dim) for _ in range(2))
+        for m, x in ((kk, k), (vv, v)):
+            m.append(x[at[i]:at[i + 1]].double().cpu().numpy())
+        most = TOP[store] * float(vv.scales.max())
+        kk, vv = (torch.from_numpy(m.values()).cuda() for m in (kk, vv))
+        for h in range(heads):
+            rows = slice(h * (hq // heads), (h + 1) * (hq // heads))
+            out, A, qk = attend(q[i, rows], kk[:, h], vv[:, h], dim ** -0.5)
+            beyond = beyond or bool((out.abs() >= 65520).any())
+            assert_near(got[i, rows], out.clamp(-65504, 65504), A, qk, n, dim, most)
+    assert beyond
+    assert bool((got[2].abs() == 65504).all())
+    v[70, 0, 5] = float("nan")
+    tfx.cache_append(c, 0, k, v)
+    got = tfx.attn_decode(c, 0, q, dev(0, 1, 2))
+    group = hq // heads
+    assert bool(got[2, :group].isnan().all()) and bool(got[2, group:].isfinite().all()) and bool(got[:2].isfinite().all())
