@@ -148,7 +148,10 @@ def _ints(name: str, t, device: int) -> tuple:
     """(length, address) of a contiguous int32 vector; device -1 is the CPU."""
     if t.dtype is not _int32 or t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 vector on {'the CPU' if device < 0 else f'CUDA device {device}'} is wanted")
-    return t.numel(), t.data_ptr()
+    n = t.numel()
+    if n >= _TOP:  # the library counts in 32 bits
+        raise ValueError(f"{name} of {n} values: fewer than 2^31 are wanted")
+    return n, t.data_ptr()
 
 
 def attn_prompt(q, k, v, offsets, scale: float | None = None, out=None, stream=None):

@@ -67,3 +67,24 @@ def test_shapes_types_and_devices_that_do_not_go_together(calls):  # noqa: F811
     assert not calls
     e["cache_read"](out=(t(9, 4, 256), t(7, 4, 256)))  # more rows than are read
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 2])
+def test_lists_past_32_bits_are_refused(calls, n):  # noqa: F811
+    """Modulo 2^32 the library would see a few of their entries, or none."""
+    i = lambda n: Fake(n, dtype=I32)  # noqa: E731
+    t = lambda *s, dtype=F16: Fake(*s, dtype=dtype)  # noqa: E731
+    c = tfx.Cache(t(2, 10, 32, 4, 256), t(2, 10, 32, 4, 256), 3, 5, book=i(4 + 3 + 10 + 15))
+    k = t(5, 4, 256)
+    r = tfx.Rope.__new__(tfx.Rope)
+    r.dim, r.rotary, r.device, r.s = 16, 16, 0, rotary.RopeStruct(0x7F0000000000, 16, 0, 1.0)
+    r.ref = rotary.C.byref(r.s)
+    x = t(n, 1, 16)
+    for call in (lambda: tfx.cache_read(c, 0, i(n), i(n), i(n + 1), 5, out=(k, k), stream=7),
+                 lambda: tfx.cache_extend(c, i(n), i(n + 1), stream=7),
+                 lambda: tfx.cache_append(c, 0, k, k, i(n), i(n + 1), stream=7),
+                 lambda: tfx.cache_fork(c, i(n), i(n), stream=7), lambda: tfx.cache_copy(c, i(n), i(n), stream=7),
+                 lambda: tfx.cache_free(c, i(n), stream=7), lambda: tfx.rope(r, x, x, i(n), out=(x, x), stream=7)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    assert not calls
