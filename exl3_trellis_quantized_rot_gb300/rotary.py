@@ -115,6 +115,8 @@ def rope(r: Rope, q, k, positions, out=None, inverse: bool = False, stream=None)
     n, pp = _at._ints("positions", positions, dev)
     if nk != rows or n != rows:
         raise ValueError(f"{rows} rows of q, {nk} of k, {n} positions")
+    if heads >= _at._TOP or kv >= _at._TOP:
+        _at._int32s(heads=heads, kv_heads=kv)
     on = _at._stream(stream, dev)
     if out is None:
         if stream is None:

@@ -88,3 +88,15 @@ def test_lists_past_32_bits_are_refused(calls, n):  # noqa: F811
         with pytest.raises(ValueError, match="2\\^31"):
             call()
     assert not calls
+
+
+@pytest.mark.parametrize("heads,kv", [(2 ** 32 + 24, 1), (1, 2 ** 32), (2 ** 31, 0)])
+def test_rotated_heads_past_32_bits_are_refused(calls, heads, kv):  # noqa: F811
+    """Modulo 2^32 the library would see a few of them and leave the rest as they are."""
+    r = tfx.Rope.__new__(tfx.Rope)
+    r.dim, r.rotary, r.device, r.s = 16, 16, 0, rotary.RopeStruct(0x7F0000000000, 16, 0, 1.0)
+    r.ref = rotary.C.byref(r.s)
+    q, k = Fake(2, heads, 16), Fake(2, kv, 16) if kv else None
+    with pytest.raises(ValueError, match="32 bits"):
+        tfx.rope(r, q, k, Fake(2, dtype=I32), out=(q, k), stream=7)
+    assert not calls
