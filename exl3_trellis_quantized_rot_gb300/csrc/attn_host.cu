@@ -283,12 +283,14 @@ int64_t prefix_rows(int64_t batch, int64_t heads_q, int64_t heads_kv) {
 // 100 own tokens): 24/4 heads of 256, 8,192 tokens and 2 sequences 18.1 / 15.3, 4: 18.7 / 17.7, 6: 19.2 /
 // 21.2, 16: 23.8 / 41.0; of 2,048 and 6: 16.0 / 11.9, 16: 19.8 / 17.2; of 32,768 and 2: 31.9 / 28.8, 3: 32.0 /
 // 35.2; 8/8 heads of 128, 8,192 and 4: 18.5 / 16.8, 8: 20.0 / 26.3; of 32,768 and 4: 39.5 / 44.9.
+constexpr int kFewSequences = 2;  // batches up to this never go there, and reserve nothing for it
 int coded_prefix(const tfx_cache* c, int batch, int shared) {
   shared = shared / TFX_CACHE_BLOCK * TFX_CACHE_BLOCK;
-  return batch > 2 && (int64_t)batch * shared * c->heads_kv * c->dim * 2 > (64LL << 20) ? shared : 0;
+  return batch > kFewSequences && (int64_t)batch * shared * c->heads_kv * c->dim * 2 > (64LL << 20) ? shared : 0;
 }
 // Partial results of that kernel's shares, at most: as prefix_rows, in tiles of its own.
 int64_t coded_prefix_rows(int64_t batch, int64_t heads_q) {
+  if (batch <= kFewSequences) return 0;
   return std::max(batch * heads_q, (int64_t)tfx::multiprocessors() * tfx::prefix_q8_rows());
 }
 

@@ -104,6 +104,27 @@ def test_a_reservation_grows_with_heads_and_sequences(L, drv):
         assert all(m <= n for (x, y), m in size.items() if x <= b and y <= g)
 
 
+def test_a_reservation_for_two_sequences_has_no_room_for_the_prefix_s_kernel(L, drv):
+    """Batches of one and two read a prefix as their own: 128 rows of FP32 an SM less than a batch of three takes."""
+    def taken(batch):
+        c = cache(heads_kv=1)
+        assert L.tfx_cache_reserve(C.byref(c), batch, 1, None) == 0
+        n = sum(drv.live.values())
+        assert L.tfx_cache_release(C.byref(c)) == 0
+        return n
+
+    one, two, three = taken(1), taken(2), taken(3)
+    assert one <= two < three
+    assert three - two >= 128 * 256 * 4 * 100  # GB300 has 152 SMs
+    c = cache(heads_kv=1)
+    r = C.byref(c)
+    assert L.tfx_cache_reserve(r, 2, 1, None) == 0
+    h = C.byref(at.HeadsStruct(1, 1, 256, 0, 0.0625))
+    assert L.tfx_attn_decode(r, 0, h, P, 256, P, 3, 80, P, 256, None) == tfx.ENOTRESERVED
+    assert L.tfx_cache_reserve(r, 3, 1, None) == 0  # it grows
+    assert L.tfx_cache_release(r) == 0 and not drv.live
+
+
 def rope_args(**kw):
     d = dict(act=0, dim=128, q=P, ldq=512, heads_q=4, q_out=P + (1 << 30), ldqo=512, k=P + (1 << 31), ldk=256, heads_k=2,
              k_out=P + (1 << 32), ldko=256, positions=P, rows=3, inverse=0, stream=None)
