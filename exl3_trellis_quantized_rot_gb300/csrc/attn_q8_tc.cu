@@ -11,7 +11,7 @@
 // heads are grouped. Warps of a CTA: 0-7 softmax, and Q before it: warps w and w + 4 share 32
 // rows (a thread a row) and halve their columns; 8-15 turn codes into operands, 16 at a time as
 // two 16-byte pieces into the 128-byte swizzle; 16 issues the MMAs; 17 asks for codes and
-// scales. All but these two store the result. Codes as registers of the converting warps
+// scales. Warps 0-15 store the result; 18 and 19 only fill the last four of the register split. Codes as registers of the converting warps
 // instead of tensor copies made a tile take 3,400 cycles, most of it in issuing the loads.
 // Bound: the converting warps, busy in all of a tile's 2,440 cycles (dim 256), of which its MMAs take
 // 1,100 beside them. 64 sequences behind 16,384 tokens (24/4 heads of 256): 37 us, issue slots 47 %,
@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_q8_kernel(const __grid_con
     for (int k = 0; k < 8; k++)
       to[k] = reinterpret_cast<float*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(po), k * 4 + (lane >> 3)));
     const float scale = row_end[r];
-    const uint32_t mine = sq + warp * 2048;  // nothing reads Q any more
+    // 2 KB a warp of Q's memory, which nothing reads any more
+    static_assert((kSoft + kConvert) * 2048 <= G::kQ && kSoft + kConvert == 16, "sixteen warps store the result");
+    const uint32_t mine = sq + warp * 2048;
     const int q = lane & 7;
 #pragma unroll 1
     for (int i = (warp >> 2) * 32; i < D; i += 128) {
