@@ -128,6 +128,8 @@ int check_cache(const tfx_cache* c) {
                      c->heads_kv, c->slots, c->width);
   if (c->act != TFX_F16 && c->act != TFX_BF16) return fail_with(TFX_EINVAL, "act=%d", c->act);
   if (c->dim != 128 && c->dim != 256) return fail_with(TFX_EUNSUPPORTED, "dim=%d (128 or 256)", c->dim);
+  if ((int64_t)c->heads_kv * c->dim > (1 << 30))
+    return fail_with(TFX_EUNSUPPORTED, "heads_kv=%d of dim=%d: a token has more than 2^30 values", c->heads_kv, c->dim);
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return fail_with(TFX_EUNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", c->page_size);
   if ((int64_t)c->pages * c->page_size > INT32_MAX || (int64_t)c->width * c->page_size > kMostTokens)

@@ -47,7 +47,7 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
 
 /* A paged K/V cache. All memory but priv is the caller's.
  * k, v  : [layers][pages][page_size][heads_kv][dim] in act, 16-byte aligned;
- *         page_size 16, 32, 64 or 128; dim 128 or 256.
+ *         page_size 16, 32, 64 or 128; dim 128 or 256; heads_kv * dim at most 2^30.
  *         pages * page_size and slots * width below 2^31, width * page_size at
  *         most 2^31 - 2048, and that times the batch of a decode call below
  *         2^31 * 4096 / dim (TFX_EUNSUPPORTED otherwise).

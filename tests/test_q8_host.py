@@ -125,6 +125,18 @@ def test_a_reservation_for_two_sequences_has_no_room_for_the_prefix_s_kernel(L, 
     assert L.tfx_cache_release(r) == 0 and not drv.live
 
 
+@pytest.mark.parametrize("store", [at.STORE_ACT, at.STORE_I8, at.STORE_E4M3])
+@pytest.mark.parametrize("heads,dim", [(1 << 23, 256), ((1 << 22) + 1, 256), (1 << 24, 128), (1 << 27, 128)])
+def test_tokens_of_more_values_than_the_kernels_count(L, drv, store, heads, dim):
+    """heads_kv * dim is a 32-bit number in the append, read and copy kernels."""
+    c = cache(store=store, heads_kv=heads, dim=dim)
+    r = C.byref(c)
+    assert L.tfx_cache_reserve(r, 1, heads, None) == tfx.EUNSUPPORTED and "2^30" in tfx.last_error()
+    assert L.tfx_cache_append(r, 0, P, heads * dim, P, heads * dim, 1, None) == tfx.EUNSUPPORTED
+    assert L.tfx_cache_read(r, 0, P, P, P, 1, 1, P, heads * dim, P, heads * dim, None) == tfx.EUNSUPPORTED
+    assert not drv.live
+
+
 def rope_args(**kw):
     d = dict(act=0, dim=128, q=P, ldq=512, heads_q=4, q_out=P + (1 << 30), ldqo=512, k=P + (1 << 31), ldk=256, heads_k=2,
              k_out=P + (1 << 32), ldko=256, positions=P, rows=3, inverse=0, stream=None)
