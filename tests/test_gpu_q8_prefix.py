@@ -3,6 +3,9 @@ limit of 64 MiB (batch * shared tokens) reach it is told by their number of laun
 that rise and fall along the prefix by less and by more than what moves its references, shares of many
 tiles, more tiles of rows than SMs, and steps one behind another."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -144,3 +147,105 @@ def test_steps_behind_a_prefix_one_after_another(store):
         for u, v in ((a.k_scale, b.k_scale), (a.v_scale, b.v_scale)):
             assert torch.equal(u.nan_to_num(), v.nan_to_num())
     assert a.status() == 0 and b.status() == 0 and tfx.attn_error() == 0
+
+
+@pytest.mark.parametrize("store", [I8, E4M3])
+@pytest.mark.parametrize("hq,hkv,dim,page,shared,n", [(24, 4, 256, 16, 1211, 30), (6, 2, 128, 64, 100, 5)])
+def test_layers_have_their_own_codes_and_scales(store, hq, hkv, dim, page, shared, n):
+    """Attention, with and without the prefix's kernel, and reads of three layers that hold different values."""
+    layers, act = 3, F16
+    width = shared // page + 3
+    c = make(store, act, width + 3 * n, page, hkv, dim, n + 1, width, n, hq, layers=layers)
+
+    def put(adds, seed):
+        at = [0]
+        for _, m in adds:
+            at.append(at[-1] + m)
+        tfx.cache_extend(c, dev(s for s, _ in adds), dev(at))
+        for layer in range(layers):
+            tfx.cache_append(c, layer, *(normal((at[-1], hkv, dim), act, seed + 10 * layer + i, 4.0 ** layer) for i in range(2)))
+
+    put([(n, shared)], 1)
+    tfx.cache_fork(c, dev([n] * n), dev(range(n)))
+    put([(i, 1 + i % 5) for i in range(n)], 3)
+    assert c.status() == 0
+    q = normal((n, hq, dim), act, 7, 0.05)
+    launches = 3 if n * (shared // BLOCK * BLOCK) * hkv * dim * 2 > 64 << 20 else 2
+    outs = [decode(c, layer, q, dev(range(n)), shared=shared, launches=launches) for layer in range(layers)]
+    for layer, got in enumerate(outs):
+        # the same cache as one of a single layer
+        one = tfx.Cache(*(x[layer:layer + 1].contiguous() for x in (c.k, c.v)), n + 1, width, book=c.book.clone(),
+                        k_scale=c.k_scale[layer:layer + 1].contiguous(), v_scale=c.v_scale[layer:layer + 1].contiguous(), act=act)
+        tfx.cache_reserve(one, n, hq)
+        check(one, q, list(range(n)), got, shared, n, dim ** -0.5)
+        lists = dev([n, 0]), dev([3, 0]), dev([0, shared - 3, shared - 3 + 7])
+        for u, v in zip(tfx.cache_read(c, layer, *lists, shared + 4), tfx.cache_read(one, 0, *lists, shared + 4)):
+            assert torch.equal(u, v)
+        assert one.status() == 0
+
+
+FIRST = """
+import torch
+import exl3_trellis_quantized_rot_gb300 as tfx
+h = lambda *s: torch.randn(s, device="cuda").half()
+i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+pages = lambda: torch.empty((1, 80, 16, 1, 256), dtype=torch.int8, device="cuda")
+c = tfx.Cache(pages(), pages(), 4, 70, act=torch.float16)
+tfx.cache_reserve(c, 140, 8)
+r = tfx.Rope(256, 64)
+k, kr, q, out, rk, rv = h(1000, 1, 256), h(1000, 1, 256), h(140, 8, 256), h(140, 8, 256), h(1000, 1, 256), h(1000, 1, 256)
+s, d, o, same, z = i(0), i(1), i(0, 1000), i(*[0] * 140), i(0)
+at = torch.arange(1000, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    tfx.rope(r, k, None, at, out=(kr, None))
+    tfx.cache_extend(c, s, o)
+    tfx.cache_append(c, 0, kr, k)
+    tfx.attn_decode(c, 0, q, same, shared=1000, out=out)  # the prefix's kernel, the own tokens', the join
+    tfx.attn_decode(c, 0, q, same, out=q)
+    tfx.cache_read(c, 0, s, z, o, 1000, out=(rk, rv))
+    tfx.cache_fork(c, s, d)
+g.replay()
+torch.cuda.synchronize()
+assert c.lens.tolist() == [1000, 1000, 0, 0] and c.status() == 0 and tfx.attn_error() == 0
+assert torch.equal(kr, tfx.rope(r, k, None, at)[0])
+read = tfx.cache_read(c, 0, s, z, o, 1000)
+assert torch.equal(read[0], rk) and torch.equal(read[1], rv)
+# two ways over the same codes: apart by the bounds of each, 2^-10 of the largest value and the output's two steps
+assert float((out.float() - q.float()).abs().max()) <= float(rv.float().abs().max()) * 2.0 ** -8
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST], check=True, cwd=root, timeout=300)
+
+
+def test_calls_of_several_streams_at_once():
+    """Two caches and a prompt on three streams, kernels of each with tensor memory of their own: the bits of one after another."""
+    shapes = [(I8, F16, 8, 1, 128, 16, 703, 400), (E4M3, BF16, 24, 4, 256, 64, 1605, 30)]
+    calls = []
+    for store, act, hq, hkv, dim, page, shared, n in shapes:
+        width = shared // page + 3
+        c = make(store, act, width + 4 * n, page, hkv, dim, n + 1, width, n, hq)
+        behind(c, n, shared, n, lambda i: 1 + i % 19)
+        q, seqs, out = normal((n, hq, dim), act, 7, 0.3), dev(range(n)), normal((n, hq, dim), act, 8)
+        calls.append((lambda c=c, q=q, seqs=seqs, shared=shared, out=out: tfx.attn_decode(c, 0, q, seqs, shared=shared, out=out), out))
+    q, k, out = normal((3000, 24, 128), F16, 1), normal((3000, 4, 128), F16, 2), normal((3000, 24, 128), F16, 3)
+    off = torch.tensor([0, 1700, 3000], dtype=torch.int32)
+    calls.append((lambda: tfx.attn_prompt(q, k, k, off, out=out), out))
+    want = [call().clone() for call, _ in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(10):
+        for _, out in calls:
+            out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, (call, _) in zip(streams, calls):
+                with torch.cuda.stream(s):
+                    call()
+        torch.cuda.synchronize()
+        for w, (_, out) in zip(want, calls):
+            assert torch.equal(out, w)
+    assert tfx.attn_error() == 0
