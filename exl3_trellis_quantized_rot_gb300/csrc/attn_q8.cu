@@ -31,6 +31,10 @@
 // takes: 7 warps of 2 slices (112 KB an SM) 95 and 99 us, 8 of 2 96 and 99 to 103, 8 of 3 101 and 108, 6 of 2
 // 98 and 105, 10 of 2 100 and 110; slices of 4 KB at dim 128 (8 warps of 2, 3 and 4, 12 of 2) 104, 103, 104,
 // 100. A barrier a slice, so that a CTA's heads are read together, was no faster.
+// One query head to a K/V head: 102 us for 554 MB (16/16 heads of 128), 173 for 1,103 (8/8 of 256). Groups of 9 to 16 take
+// the variant of 16 rows (at dim 256 255 registers and 120 to 172 bytes of spills), larger ones walk the codes
+// again for every 16: 64 sequences of up to 8,192 tokens, one K/V head of 256, 8, 16, 32, 64 and 128 query heads
+// 37, 49, 74, 133 and 246 us (of up to 16,384, heads of 128: 36, 42, 69, 120, 227).
 #include <cuda_fp16.h>
 
 #include "attn_split.cuh"
@@ -318,7 +322,9 @@ __device__ __forceinline__ bool attend(Rows<NT, D>& R, Ring<D, NT>& rg, const De
           R.l[n][c & 1] += exp2_fast(sx[b][n][c] - ref[c & 1]);
           e[c] = exp2_fast(sx[b][n][c] + off[b][n][c & 1]);
         }
-        // the weights become matrix operands of FP16
+        // The weights become matrix operands of FP16, 11 bits of each, as TF32 operands would have at half the rate;
+        // two operands each would double the product's MMAs. Outputs in FP16 are off by 0.00024 of their
+        // size instead of 0.00021 with weights of FP32, nearly all of it their own rounding.
         p[b][n][0] = transposed(pack2<__half>(e[0], e[1]));
         p[b][n][1] = transposed(pack2<__half>(e[2], e[3]));
       }

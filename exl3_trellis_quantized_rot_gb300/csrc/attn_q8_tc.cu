@@ -16,7 +16,8 @@
 // Bound: the converting warps, busy in all of a tile's 2,440 cycles (dim 256), of which its MMAs take
 // 1,100 beside them. 64 sequences behind 16,384 tokens (24/4 heads of 256): 37 us, issue slots 47 %,
 // behind 65,536 with up to 2,048 tokens of their own: 146 for the whole step; over 16-bit pages, whose
-// tiles need no conversion, 131 to 133. Fewer CTAs here, so that decode_q8_kernel runs beside
+// tiles need no conversion, 131 to 133. Each tile of 128 rows converts for itself, so that the same codes are
+// converted three times for the 384 rows of a K/V head here. Fewer CTAs here, so that decode_q8_kernel runs beside
 // them, were no faster.
 // Order of the MMAs: S0, S1, P0 V0, S2, P1 V1, ... Tensor memory: O in columns 0..dim-1, two
 // buffers of 64 columns for scores, whose first 32 take the weights.

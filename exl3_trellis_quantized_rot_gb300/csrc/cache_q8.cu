@@ -5,10 +5,11 @@
 // magnitude, and with it the scale; codes that the block holds already are rounded again
 // only where the scale grows.
 //
-// Bound: memory at large sizes: three prompts of 32,001 tokens (8 heads of 128) are appended in 36 us (131 MB
+// Bound: memory at large sizes: three prompts of 32,001 tokens (8 heads of 128) are appended in 39 us (131 MB
 // read, 66 written; DRAM busy half the time, issue slots 41 %), 43,695 tokens (4 heads of 256) read back
-// in 46 us (268 MB, 5.8 TB/s). 64 single tokens: 3.4 us, 300 rows read: 3.1 us, the latency
-// of lists, table, scale and codes one after another. Two CTAs an SM hold a block in registers (128 a
+// in 46 us (268 MB, 5.8 TB/s), out of 16-bit pages in 58 to 61 (358 MB, 5.8 to 6.2 TB/s). 64 single tokens: 3.4 us,
+// 300 rows read: 3.1 us, the latency of lists, table, scale and codes one after another. It stands in front of the
+// 3.7 us that the bytes of 4,096 tokens take, too (7.2 us, a window a CTA: nothing hides the first look-up). Two CTAs an SM hold a block in registers (128 a
 // thread); copies into shared memory for eight warps an SM took 60 us where this took 46.
 #include <cuda_runtime.h>
 

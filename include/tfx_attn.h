@@ -77,7 +77,8 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
  * is larger; x becomes x / scale rounded to the nearest code, ties to even. Where a
  * block that holds tokens gets a larger e, its codes are rounded again in the same
  * way (for I8 that can add half a step of the new scale; for E4M3 it is exact down to
- * its subnormals). A value that is not finite makes the block's scale NaN until its
+ * its subnormals): a scale is the same however its block's tokens are spread over appends,
+ * I8 codes need not be. A value that is not finite makes the block's scale NaN until its
  * page is used anew: the block reads as NaN, as do rows that attend to it. */
 typedef struct {
   void* k;
@@ -174,7 +175,9 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * heads_q/heads_kv) where it has more than 32 and there are 256 such tokens or more,
  * else once for every 16 rows; 0 where nothing is shared. A sequence shorter than
  * that attends to as many of them as its length says (what it does not hold of
- * them must then be finite). A sequence that holds no token, or a slot out of
+ * them must then be finite). Whether a sequence's shared tokens are read through its own
+ * table or another's depends on the batch. Over an 8-bit store that is the same where their
+ * codes are, as in forks; the same tokens appended twice, in different pieces, can differ. A sequence that holds no token, or a slot out of
  * range, gives zeros. h->heads_kv, dim and act are the cache's. Same arithmetic as
  * tfx_attn_prompt, with partial results of FP32 joined in a fixed order.
  * Over an 8-bit store, in a batch above 2 whose sequences would read more than 64 MiB of
