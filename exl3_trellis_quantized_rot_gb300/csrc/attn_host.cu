@@ -281,13 +281,14 @@ int64_t prefix_rows(int64_t batch, int64_t heads_q, int64_t heads_kv) {
 
 // Over 8-bit codes, the tokens of a prefix that the tensor cores read once; 0: each sequence
 // reads it as its own. That takes the warps as long as reading the prefix `batch` times, from L2
-// where it fits, and once more for every further 16 heads of a group. The rule leaves those out: it is measured for groups of
-// up to 16, and late for wider ones. The other kernel begins with 8 us. Measured, the tensor cores / as their own (us;
+// where it fits, and once more for every further 16 heads of a group. The rule leaves those out: it is
+// measured with groups of 6 and 1, and late for those above 16. The other kernel begins with 8 us.
+// Measured, the tensor cores / as their own (us;
 // 100 own tokens): 24/4 heads of 256, 8,192 tokens and 2 sequences 18.1 / 15.3, 4: 18.7 / 17.7, 6: 19.2 /
 // 21.2, 16: 23.8 / 41.0; of 2,048 and 6: 16.0 / 11.9, 16: 19.8 / 17.2; of 32,768 and 2: 31.9 / 28.8, 3: 32.0 /
 // 35.2; 8/8 heads of 128, 8,192 and 4: 18.5 / 16.8, 8: 20.0 / 26.3; of 32,768 and 4: 39.5 / 44.9.
-// Wide groups just above / below 64 MiB, one K/V head of 256: 16 sequences of 32 heads behind 8,300 / 8,000 tokens 31.3 / 46.7,
-// of 64 heads 42.1 / 77.6, of 128 heads 65.0 / 138.
+// Wide groups just above / below 64 MiB, one K/V head of 256: 16 sequences of 32 heads behind 8,300 / 8,000
+// tokens 31.3 / 46.7, of 64 heads 42.1 / 77.6, of 128 heads 65.0 / 138.
 constexpr int kFewSequences = 2;  // batches up to this never go there, and reserve nothing for it
 int coded_prefix(const tfx_cache* c, int batch, int shared) {
   shared = shared / TFX_CACHE_BLOCK * TFX_CACHE_BLOCK;

@@ -11,7 +11,8 @@
 // heads are grouped. Warps of a CTA: 0-7 softmax, and Q before it: warps w and w + 4 share 32
 // rows (a thread a row) and halve their columns; 8-15 turn codes into operands, 16 at a time as
 // two 16-byte pieces into the 128-byte swizzle; 16 issues the MMAs; 17 asks for codes and
-// scales. Warps 0-15 store the result; 18 and 19 only fill the last four of the register split. Codes as registers of the converting warps
+// scales. Warps 0-15 store the result; 18 and 19 only fill the last four of the register split.
+// Codes as registers of the converting warps
 // instead of tensor copies made a tile take 3,400 cycles, most of it in issuing the loads.
 // Bound: the converting warps, busy in all of a tile's 2,440 cycles (dim 256), of which its MMAs take
 // 1,100 beside them. 64 sequences behind 16,384 tokens (24/4 heads of 256): 37 us, issue slots 47 %,

@@ -78,7 +78,7 @@ int tfx_attn_prompt(const tfx_attn_heads* h, const void* q, int64_t ldq, const v
  * block that holds tokens gets a larger e, its codes are rounded again in the same
  * way (for I8 that can add half a step of the new scale; for E4M3 it is exact down to
  * its subnormals): a scale is the same however its block's tokens are spread over appends,
- * I8 codes need not be. A value that is not finite makes the block's scale NaN until its
+ * codes of I8, and subnormal ones of E4M3, need not be. A value that is not finite makes the block's scale NaN until its
  * page is used anew: the block reads as NaN, as do rows that attend to it. */
 typedef struct {
   void* k;
@@ -177,8 +177,8 @@ int tfx_cache_copy(tfx_cache* c, const int32_t* src, const int32_t* dst, int n, 
  * that attends to as many of them as its length says (what it does not hold of
  * them must then be finite). Whether a sequence's shared tokens are read through its own
  * table or another's depends on the batch. Over an 8-bit store that is the same where their
- * codes are, as in forks; the same tokens appended twice, in different pieces, can differ. A sequence that holds no token, or a slot out of
- * range, gives zeros. h->heads_kv, dim and act are the cache's. Same arithmetic as
+ * codes are, as in forks; the same tokens appended twice, in different pieces, can differ.
+ * A sequence that holds no token, or a slot out of range, gives zeros. h->heads_kv, dim and act are the cache's. Same arithmetic as
  * tfx_attn_prompt, with partial results of FP32 joined in a fixed order.
  * Over an 8-bit store, in a batch above 2 whose sequences would read more than 64 MiB of
  * codes there (batch * shared tokens), the whole blocks of the first `shared` tokens are read through the
